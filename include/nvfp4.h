@@ -13,6 +13,8 @@
  *   MoE steps           moe_sort_by_expert, moe_gather_rows, nvfp4_quantize_experts,
  *                       nvfp4_gather_quantize_experts (the two fused),
  *                       nvfp4_silu_mul_quantize_experts, nvfp4_grouped_gemm, moe_combine
+ *   decoder block       block_norm, block_norm_quantize, block_norm_backward (the norms before and
+ *                       after a block with its gate and residual sum)
  *   sizes and status    nvfp4_sf_bytes, mxfp4_grouped_sf_bytes, moe_sort_workspace_size,
  *                       nvfp4_check_status, nvfp4_last_error
  *
@@ -360,6 +362,61 @@ nvfp4_status_t nvfp4_grouped_gemm(const uint8_t *a, const uint8_t *sfa, const in
 nvfp4_status_t moe_combine(const void *y, int64_t rows, const int32_t *pos, const float *weights,
                            int64_t num_tokens, int topk, int64_t h, void *out, uint32_t flags,
                            nvfp4_stream_t stream);
+
+/* ---------------------------------------------------------------- norms around a decoder block
+ * The RMS norm after a block, the block's gate, the residual sum and the norm before the next
+ * block, in one pass over the rows.  For a row of n channels, in fp32:
+ *   p = y * rsqrt(mean(y^2) + eps) * (weight_offset + w_post)    (p = y when w_post is NULL)
+ *   r = x + residual_scale * (gate * p)                          (gate = 1 when NULL; r = x when y is NULL)
+ *   h = r * rsqrt(mean(r^2) + eps) * (weight_offset + w_pre)
+ * r is rounded once, to x's type, when it is stored in x_out; h is computed from the unrounded r
+ * and rounded once, to bf16.  Not operations of the pages: they are what a decoder runs between
+ * the products of this library.  weight_offset is 1 for weights stored around zero, else 0.
+ *   x       bf16 or fp32 (x_type: NVFP4_DTYPE_*) [m, n], row stride ldx elements
+ *   y       bf16 [m, n], row stride ldy; NULL: no block before this norm (then w_post, gate and
+ *           x_out are NULL too)
+ *   w_post, w_pre   bf16 [n]; w_pre and h may both be NULL (no norm after the sum)
+ *   gate    bf16 [m, n] with row stride ldg, or [n] shared by all rows with ldg = 0
+ *   x_out   x's type [m, n], row stride ldxo; may be x itself (same stride); no other overlap
+ *   h       bf16 [m, n], row stride ldh
+ *   1 <= n <= 32768.  Any strides and alignments of whole elements are taken; rows that all start
+ *   on 16 bytes (and n % 8 == 0) are moved with 16-byte accesses.
+ * Every input is read and every output written after the PDL wait. */
+enum { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_F32 = 1 };
+nvfp4_status_t block_norm(const void *x, int x_type, int64_t ldx, const void *y, int64_t ldy, const void *w_post,
+                          const void *gate, int64_t ldg, const void *w_pre, float residual_scale, float eps,
+                          float weight_offset, void *x_out, int64_t ldxo, void *h, int64_t ldh, int64_t m, int64_t n,
+                          uint32_t flags, nvfp4_stream_t stream);
+
+/* block_norm whose h goes out as NVFP4, ready for nvfp4_gemm: q and sf equal nvfp4_quantize of
+ * block_norm's h under global scale gs, bit for bit (scale rows up to the next multiple of 128 are
+ * zeroed).  n % 16 == 0; every row of x, y, gate and x_out, the weights and sf on 16 bytes. */
+nvfp4_status_t block_norm_quantize(const void *x, int x_type, int64_t ldx, const void *y, int64_t ldy,
+                                   const void *w_post, const void *gate, int64_t ldg, const void *w_pre,
+                                   float residual_scale, float eps, float weight_offset, void *x_out, int64_t ldxo,
+                                   const float *gs, uint8_t *q, uint8_t *sf, int64_t m, int64_t n, uint32_t flags,
+                                   nvfp4_stream_t stream);
+
+/* Backward pass of block_norm, from what the forward pass stored.  dh is the gradient of h, dx_out
+ * the gradient that reaches x_out from elsewhere (NULL: zero), x_out the stored stream (x itself
+ * when y was NULL).
+ *   dx       x's type [m, n]: gradient of x, which is also the whole gradient of x_out
+ *   dy       bf16 [m, n]
+ *   dw_pre, dw_post   fp32 [n], summed over the rows in a fixed order (bit-reproducible)
+ *   dgate    bf16 [m, n] (row stride lddg) for a gate per token, fp32 [n] for a gate per channel
+ *   dh and w_pre may both be NULL (h was not computed); a NULL w_post or gate has no gradient.
+ *   dx may be dx_out and dy may be y (same strides); no other overlap.
+ *   workspace   device, 16-B aligned, at least block_norm_backward_workspace_size(m, n) bytes (the
+ *               teams' column sums; no initialisation); may be NULL when nothing is summed over rows.
+ *               Calls that may overlap need separate ones.
+ * Two launches (one when nothing is summed over rows).  m = 0 writes zero to the row sums. */
+size_t block_norm_backward_workspace_size(int64_t m, int64_t n);
+nvfp4_status_t block_norm_backward(const void *dh, int64_t lddh, const void *dx_out, int64_t lddxo, const void *x_out,
+                                   int x_type, int64_t ldxo, const void *y, int64_t ldy, const void *w_post,
+                                   const void *gate, int64_t ldg, const void *w_pre, float residual_scale, float eps,
+                                   float weight_offset, void *dx, int64_t lddx, void *dy, int64_t lddy, float *dw_pre,
+                                   float *dw_post, void *dgate, int64_t lddg, int64_t m, int64_t n, void *workspace,
+                                   size_t workspace_bytes, uint32_t flags, nvfp4_stream_t stream);
 
 /* Scale layout conversion between a row-major scale matrix [rows, cols] (bytes) and the
  * 128x4 swizzled layout of nvfp4_sf_bytes size (swizzle writes the zero padding).

@@ -20,6 +20,7 @@ if not os.path.exists(_LIB_PATH):
 _lib = ctypes.CDLL(_LIB_PATH)
 
 _i64, _u32, _int, _vp, _sz = ctypes.c_int64, ctypes.c_uint32, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_f32 = ctypes.c_float
 
 FLAG_PDL = 1 << 0
 FLAG_SF_SM103 = 1 << 2
@@ -59,6 +60,13 @@ _SIGS = {
     "nvfp4_silu_mul_quantize_experts": (_int, [_vp, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _sz, _u32, _vp]),
     "nvfp4_grouped_gemm": (_int, [_vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _u32, _vp]),
     "moe_combine": (_int, [_vp, _i64, _vp, _vp, _i64, _int, _i64, _vp, _u32, _vp]),
+    "block_norm": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _f32, _f32, _f32, _vp, _i64, _vp, _i64,
+                          _i64, _i64, _u32, _vp]),
+    "block_norm_quantize": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _f32, _f32, _f32, _vp, _i64, _vp,
+                                   _vp, _vp, _i64, _i64, _u32, _vp]),
+    "block_norm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "block_norm_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _f32, _f32,
+                                   _f32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _u32, _vp]),
     "nvfp4_check_status": (_int, [_vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -134,6 +142,15 @@ def _contig(t, stream):
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
     with torch.cuda.stream(s):
         return t.contiguous()
+
+
+def _scratch(nbytes: int, device, stream):
+    """An uninitialised uint8 workspace that belongs to the launch stream (see _contig)."""
+    if stream is None:
+        return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(s):
+        return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
 def sf_bytes(rows: int, k: int, sf_vec: int = 16) -> int:
@@ -505,6 +522,145 @@ def moe_combine(y, pos, weights, out=None, flags: int = 0, stream=None):
     _check(_lib.moe_combine(_ptr(y), rows, _ptr(pos), _ptr(weights), T, topk, h, _ptr(out),
                             flags, _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- norms around a decoder block
+_STREAM_TYPES = {torch.bfloat16: 0, torch.float32: 1}   # NVFP4_DTYPE_*
+
+
+def _rows(t, dtype, name, m, n):
+    """A [m, n] operand with contiguous rows at any row stride; returns the stride."""
+    _need(t, dtype, name, 2)
+    if tuple(t.shape) != (m, n):
+        raise ValueError(f"{name} must have shape {(m, n)}, got {tuple(t.shape)}")
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    return t.stride(0) if m > 1 else max(n, t.stride(0))
+
+
+def _channels(t, name, n):
+    """A bf16 [n] vector (None: absent)."""
+    if t is None:
+        return
+    _need(t, torch.bfloat16, name, 1)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+
+
+def _block_operands(x, w_pre, y, w_post, gate):
+    """Checks what the forward and backward norms share: (x_type, m, n, row strides of x, y and gate)."""
+    _check_device(x, "x")
+    if x.dtype not in _STREAM_TYPES:
+        raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError("x must have 2 dimensions")
+    m, n = x.shape
+    ldx = _rows(x, x.dtype, "x", m, n)
+    _channels(w_pre, "w_pre", n)
+    if y is None:
+        if w_post is not None or gate is not None:
+            raise ValueError("w_post and gate belong to y")
+        return _STREAM_TYPES[x.dtype], m, n, ldx, 0, 0
+    ldy = _rows(y, torch.bfloat16, "y", m, n)
+    _channels(w_post, "w_post", n)
+    ldg = 0
+    if gate is not None:
+        if gate.dim() == 2:
+            ldg = _rows(gate, torch.bfloat16, "gate", m, n)
+        else:
+            _channels(gate, "gate", n)
+    return _STREAM_TYPES[x.dtype], m, n, ldx, ldy, ldg
+
+
+def block_norm(x, w_pre=None, y=None, w_post=None, gate=None, residual_scale: float = 1.0, eps: float = 1e-6,
+               weight_offset: float = 0.0, x_out=None, h=None, flags: int = 0, stream=None):
+    """The RMS norm after a block (w_post), its gate, the residual sum and the norm before the next
+    block (w_pre), one pass: r = x + residual_scale * gate * norm(y), h = norm(r).
+
+    x bf16 or fp32 [m, n], y bf16 [m, n] or None (h = norm(x) only), weights bf16 [n] or None, gate
+    bf16 [n] or [m, n] or None.  Returns (x_out, h): the stream in x's type (x itself without y) and
+    bf16 [m, n] (None without w_pre).  x_out may be x."""
+    xt, m, n, ldx, ldy, ldg = _block_operands(x, w_pre, y, w_post, gate)
+    ldo = ldh = 0
+    if y is not None:
+        if x_out is None:
+            x_out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+        ldo = _rows(x_out, x.dtype, "x_out", m, n)
+    elif x_out is not None:
+        raise ValueError("x_out belongs to y")
+    if w_pre is not None:
+        if h is None:
+            h = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
+        ldh = _rows(h, torch.bfloat16, "h", m, n)
+    elif h is not None:
+        raise ValueError("h belongs to w_pre")
+    _check(_lib.block_norm(_ptr(x), xt, ldx, _ptr(y), ldy, _ptr(w_post), _ptr(gate), ldg, _ptr(w_pre), residual_scale,
+                           eps, weight_offset, _ptr(x_out), ldo, _ptr(h), ldh, m, n, flags, _stream(stream)))
+    return (x if y is None else x_out), h
+
+
+def block_norm_quantize(x, w_pre, gs, y=None, w_post=None, gate=None, residual_scale: float = 1.0, eps: float = 1e-6,
+                        weight_offset: float = 0.0, x_out=None, q=None, sf=None, flags: int = 0, stream=None):
+    """block_norm whose h is quantised on the way out: (x_out, q, sf) with q and sf equal to
+    nvfp4_quantize(h, gs)."""
+    xt, m, n, ldx, ldy, ldg = _block_operands(x, w_pre, y, w_post, gate)
+    if w_pre is None:
+        raise ValueError("w_pre is needed")
+    _room(gs, torch.float32, "gs", 1)
+    ldo = 0
+    if y is not None:
+        if x_out is None:
+            x_out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+        ldo = _rows(x_out, x.dtype, "x_out", m, n)
+    elif x_out is not None:
+        raise ValueError("x_out belongs to y")
+    if q is None:
+        q = torch.empty((m, n // 2), dtype=torch.uint8, device=x.device)
+    if sf is None:
+        sf = torch.empty(sf_bytes(m, n // 16 * 16, 16), dtype=torch.uint8, device=x.device)
+    _room(q, torch.uint8, "q", m * (n // 2))
+    _room(sf, torch.uint8, "sf", sf_bytes(m, n // 16 * 16, 16))
+    _check(_lib.block_norm_quantize(_ptr(x), xt, ldx, _ptr(y), ldy, _ptr(w_post), _ptr(gate), ldg, _ptr(w_pre),
+                                    residual_scale, eps, weight_offset, _ptr(x_out), ldo, _ptr(gs), _ptr(q), _ptr(sf),
+                                    m, n, flags, _stream(stream)))
+    return (x if y is None else x_out), q, sf
+
+
+def block_norm_backward_workspace_size(m: int, n: int) -> int:
+    return int(_lib.block_norm_backward_workspace_size(m, n))
+
+
+def block_norm_backward(dh, dx_out, x_out, w_pre=None, y=None, w_post=None, gate=None, residual_scale: float = 1.0,
+                        eps: float = 1e-6, weight_offset: float = 0.0, workspace=None, flags: int = 0, stream=None):
+    """Backward pass of block_norm: dh the gradient of h (None without w_pre), dx_out the gradient that
+    reaches x_out from elsewhere (None: zero), x_out the stream the forward pass returned.
+
+    Returns (dx, dy, dw_pre, dw_post, dgate): dx in x_out's type, dy bf16, the weights' gradients fp32 [n],
+    dgate fp32 [n] for a gate per channel or bf16 [m, n] for a gate per token; None for what was absent."""
+    xt, m, n, ldr, ldy, ldg = _block_operands(x_out, w_pre, y, w_post, gate)
+    if (dh is None) != (w_pre is None):
+        raise ValueError("dh and w_pre: give both or neither")
+    lddh = 0 if dh is None else _rows(dh, torch.bfloat16, "dh", m, n)
+    lddr = 0 if dx_out is None else _rows(dx_out, x_out.dtype, "dx_out", m, n)
+    dev = x_out.device
+
+    def new(shape, dtype, wanted):
+        return torch.empty(shape, dtype=dtype, device=dev) if wanted else None
+
+    dx = new((m, n), x_out.dtype, True)
+    dy = new((m, n), torch.bfloat16, y is not None)
+    dw_pre = new(n, torch.float32, w_pre is not None)
+    dw_post = new(n, torch.float32, w_post is not None)
+    dgate = new((m, n), torch.bfloat16, True) if ldg else new(n, torch.float32, gate is not None)
+    if workspace is None:
+        # made on the launch stream, so that its memory is not handed out before that stream is done with it
+        workspace = _scratch(block_norm_backward_workspace_size(m, n), dev, stream)
+    _room(workspace, torch.uint8, "workspace", 0)      # the library checks its size
+    _check(_lib.block_norm_backward(_ptr(dh), lddh, _ptr(dx_out), lddr, _ptr(x_out), xt, ldr, _ptr(y), ldy, _ptr(w_post),
+                                    _ptr(gate), ldg, _ptr(w_pre), residual_scale, eps, weight_offset, _ptr(dx), n,
+                                    _ptr(dy), n, _ptr(dw_pre), _ptr(dw_post), _ptr(dgate), n if ldg else 0, m, n,
+                                    _ptr(workspace), workspace.numel(), flags, _stream(stream)))
+    return dx, dy, dw_pre, dw_post, dgate
 
 
 def check_status(stream=None) -> None:

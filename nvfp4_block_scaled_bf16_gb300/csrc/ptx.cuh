@@ -449,17 +449,24 @@ __device__ __forceinline__ float e4m3_value(uint32_t c) {
   if (e == 0) return __uint2float_rn(m) * 0.001953125f;  // m * 2^-9, exact
   return __uint_as_float(((e + 120u) << 23) | (m << 20));  // (1 + m/8) * 2^(e-7)
 }
-// One 16-element NVFP4 block under global scale gs: the e4m3 code of gs * amax / 6 (RNE,
-// saturating) and the 16 e2m1 codes of x * (gs / scale) packed two per byte (element 2t in the
-// low nibble of byte t); a zero scale gives zero codes.  Every quantiser of the library calls
-// this, so a block quantised anywhere gets the same codes.
+// Scale of an NVFP4 block whose largest magnitude is amax, under global scale gs: the e4m3 code of
+// gs * amax / 6 (RNE, saturating); returns the factor gs / scale that takes an element to its code
+// (0 for a zero scale).
+__device__ __forceinline__ float nvfp4_block_scale(float amax, float gs, uint32_t &code) {
+  code = e4m3_code(__fdiv_rn(__fmul_rn(gs, amax), 6.0f));
+  const float sd = e4m3_value(code);
+  return (sd == 0.0f) ? 0.0f : __fdiv_rn(gs, sd);
+}
+// One 16-element NVFP4 block under global scale gs: the e4m3 code of its scale and the 16 e2m1
+// codes of x * (gs / scale) packed two per byte (element 2t in the low nibble of byte t); a zero
+// scale gives zero codes.  Every quantiser of the library computes a block's scale with
+// nvfp4_block_scale and its codes with the same products, so a block quantised anywhere gets the
+// same codes.
 __device__ __forceinline__ uint2 nvfp4_block16(const float (&f)[16], float gs, uint32_t &code) {
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-  code = e4m3_code(__fdiv_rn(__fmul_rn(gs, amax), 6.0f));
-  const float sd = e4m3_value(code);
-  const float inv = (sd == 0.0f) ? 0.0f : __fdiv_rn(gs, sd);
+  const float inv = nvfp4_block_scale(amax, gs, code);
   float y0[8], y1[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
