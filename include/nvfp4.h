@@ -13,6 +13,8 @@
  *   MoE steps           moe_sort_by_expert, moe_gather_rows, nvfp4_quantize_experts,
  *                       nvfp4_gather_quantize_experts (the two fused),
  *                       nvfp4_silu_mul_quantize_experts, nvfp4_grouped_gemm, moe_combine
+ *   nvfp4_gated_gemm    both projections of a feed-forward block, the activation and the product in
+ *                       one kernel; nvfp4_gated_gemm_backward: the gradients of both projections
  *   decoder block       block_norm, block_norm_quantize, block_norm_backward (the norms before and
  *                       after a block with its gate and residual sum)
  *   sizes and status    nvfp4_sf_bytes, mxfp4_grouped_sf_bytes, moe_sort_workspace_size,
@@ -240,6 +242,45 @@ nvfp4_status_t nvfp4_quantize_gemm(const void *x, int64_t ldx, const float *gs_x
 nvfp4_status_t nvfp4_gemm_noalloc(const uint8_t *a, const uint8_t *sfa, const uint8_t *b, const uint8_t *sfb,
                                   const float *alpha, void *d, int64_t m, int64_t n, int64_t k,
                                   uint32_t flags, nvfp4_stream_t stream);
+
+/* Gated product of a feed-forward block: both projections, the activation and the product in one
+ * kernel, bf16 out.
+ *   h[t, j] = bf16( act(alpha[0] * sum_k A[t,k] Bg[j,k]) * (alpha[1] * sum_k A[t,k] Bu[j,k]) )
+ * with A, Bg and Bu the dequantised operands, fp32 sums, and act
+ *   NVFP4_ACT_SILU       g / (1 + exp(-g))
+ *   NVFP4_ACT_GELU_TANH  g/2 * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
+ * (fp32, approximate exponential and reciprocal, a few fp32 ulps; one rounding, at the end).
+ * The pages fuse the activation with the quantiser after the product ([vLLM-SM103] ops.h,
+ * silu_and_mul_scaled_fp4_experts_quant); here it is the product's epilogue, so the [m, 2 inter]
+ * pre-activations never reach memory.
+ *   a, sfa   as nvfp4_gemm
+ *   b, sfb   uint8 [2*inter, k/2] and its scales (of 2*inter rows): the gate and the up weight in one
+ *            matrix whose rows alternate in groups of 16, gate rows first: row 32 j + i is gate row
+ *            16 j + i and row 32 j + 16 + i is up row 16 j + i, for i < 16.  Laid out once, when the
+ *            weight is quantised.
+ *   alpha    device fp32 [2]: the factor of the gate and of the up product, 4-B aligned
+ *   h        bf16 [m, inter] row-major, 32-B aligned
+ *   workspace, flags, stream: as nvfp4_gemm with n = 2*inter (nvfp4_gemm_workspace_size(m, 2*inter, k))
+ *   inter % 16 == 0, k % 32 == 0.  PDL and reproducibility as nvfp4_gemm. */
+enum { NVFP4_ACT_SILU = 0, NVFP4_ACT_GELU_TANH = 1 };
+nvfp4_status_t nvfp4_gated_gemm(const uint8_t *a, const uint8_t *sfa, const uint8_t *b, const uint8_t *sfb,
+                                const float *alpha, int activation, void *h, int64_t m, int64_t inter, int64_t k,
+                                void *workspace, size_t workspace_bytes, uint32_t flags, nvfp4_stream_t stream);
+
+/* Backward pass of nvfp4_gated_gemm up to its two products: with g and u the products (computed again
+ * from the packed operands, so the forward pass stores nothing),
+ *   dgu[t, 32 j + i]      = bf16(dh[t, 16 j + i] * u * act'(g))       gradient of the gate product
+ *   dgu[t, 32 j + 16 + i] = bf16(dh[t, 16 j + i] * act(g))            gradient of the up product
+ * in the row order of b, so that the gradient of the input is dgu B and that of the weight dgu^T A:
+ * products that nvfp4_quantize and nvfp4_gemm compute from the transposed operands.
+ *   dh   bf16 [m, inter], 32-B aligned;  dgu  bf16 [m, 2*inter], 32-B aligned
+ *   h    bf16 [m, inter], 32-B aligned, or NULL: the forward result, which the gradient of the next
+ *        weight needs
+ * Everything else as nvfp4_gated_gemm. */
+nvfp4_status_t nvfp4_gated_gemm_backward(const uint8_t *a, const uint8_t *sfa, const uint8_t *b, const uint8_t *sfb,
+                                         const float *alpha, int activation, const void *dh, void *dgu, void *h,
+                                         int64_t m, int64_t inter, int64_t k, void *workspace, size_t workspace_bytes,
+                                         uint32_t flags, nvfp4_stream_t stream);
 
 /* MXFP4 grouped (MoE) GEMM: for every expert e, D[rows of e, :] = alpha * deq(A_e) deq(B_e)^T.
  * The kernel checks row_offsets on the device (row_offsets[0] == 0, row_offsets[E] == t,

@@ -48,6 +48,9 @@ _SIGS = {
     "nvfp4_gemm": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _u32, _vp]),
     "nvfp4_gemm_noalloc": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _u32, _vp]),
     "nvfp4_quantize_gemm": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _u32, _vp]),
+    "nvfp4_gated_gemm": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _sz, _u32, _vp]),
+    "nvfp4_gated_gemm_backward": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _u32,
+                                         _vp]),
     "mxfp4_grouped_gemm": (_int, [_vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _u32, _vp]),
     "sf_swizzle": (_int, [_vp, _vp, _i64, _i64, _int, _vp]),
     "nvfp4_sf_convert_layout": (_int, [_vp, _vp, _i64, _i64, _int, _vp]),
@@ -315,6 +318,85 @@ def nvfp4_gemm_noalloc(a, sfa, b, sfb, alpha, d=None, flags: int = 0, stream=Non
     _check(_lib.nvfp4_gemm_noalloc(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(alpha), _ptr(d), m, n, 2 * kh,
                                    flags, _stream(stream)))
     return d
+
+
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}   # NVFP4_ACT_*
+
+
+def interleave_gate_up(gate, up):
+    """The gate and the up weight [inter, ...] as one [2 inter, ...] matrix whose rows alternate in
+    groups of 16, gate rows first: what nvfp4_gated_gemm reads once quantised (inter % 16 == 0).
+    Done once per weight."""
+    if gate.shape != up.shape or gate.shape[0] % 16:
+        raise ValueError(f"gate and up must agree and have a multiple of 16 rows, got {tuple(gate.shape)} and {tuple(up.shape)}")
+    groups = (gate.shape[0] // 16, 16) + tuple(gate.shape[1:])
+    return torch.stack((gate.reshape(groups), up.reshape(groups)), dim=1).reshape(2 * gate.shape[0], *gate.shape[1:])
+
+
+def _gated_operands(a, sfa, b, sfb, alpha, activation, workspace):
+    """Checks what the gated products share: (m, inter, k, activation, workspace)."""
+    _need(a, torch.uint8, "a", 2)
+    _need(b, torch.uint8, "b", 2)
+    m, kh = a.shape
+    n = b.shape[0]
+    if b.shape[1] != kh:
+        raise ValueError("a and b disagree on K")
+    if n % 2:
+        raise ValueError("b must hold as many gate rows as up rows")
+    for t_, name in ((a, "a"), (b, "b")):
+        if not t_.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _room(sfa, torch.uint8, "sfa", sf_bytes(m, 2 * kh))
+    _room(sfb, torch.uint8, "sfb", sf_bytes(n, 2 * kh))
+    _room(alpha, torch.float32, "alpha", 2)
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    if workspace is None and m > 0 and n > 0:
+        need = gemm_workspace_size(m, n, 2 * kh)
+        if need:
+            workspace = _default_workspace(need, a.device)
+    if workspace is not None:
+        _room(workspace, torch.uint8, "workspace", 0)   # the library checks its size
+    return m, n // 2, 2 * kh, ACTIVATIONS[activation], workspace
+
+
+def nvfp4_gated_gemm(a, sfa, b, sfb, alpha, activation: str = "silu", h=None, flags: int = 0, stream=None,
+                     workspace=None):
+    """h[m, inter] = bf16(act(alpha[0] * a @ gate^T) * (alpha[1] * a @ up^T)): both projections, the
+    activation and the product in one kernel.
+
+    a [m, k/2] packed, b [2 inter, k/2] packed with gate and up rows alternating in groups of 16
+    (interleave_gate_up), alpha fp32 [2], activation "silu" or "gelu_tanh"; workspace as nvfp4_gemm."""
+    m, inter, k, act, workspace = _gated_operands(a, sfa, b, sfb, alpha, activation, workspace)
+    if h is None:
+        h = torch.empty((m, inter), dtype=torch.bfloat16, device=a.device)
+    _room(h, torch.bfloat16, "h", m * inter)
+    _check(_lib.nvfp4_gated_gemm(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(alpha), act, _ptr(h), m, inter, k,
+                                 _ptr(workspace), 0 if workspace is None else workspace.numel(), flags, _stream(stream)))
+    return h
+
+
+def nvfp4_gated_gemm_backward(a, sfa, b, sfb, alpha, dh, activation: str = "silu", dgu=None, h=None, flags: int = 0,
+                              stream=None, workspace=None):
+    """The gradients of nvfp4_gated_gemm's two products given dh, the gradient of h (bf16 [m, inter]).
+
+    Returns (dgu, h): dgu bf16 [m, 2 inter] in the row order of b, and the forward result, both
+    computed again from the packed operands."""
+    m, inter, k, act, workspace = _gated_operands(a, sfa, b, sfb, alpha, activation, workspace)
+    _need(dh, torch.bfloat16, "dh", 2)
+    if tuple(dh.shape) != (m, inter):
+        raise ValueError(f"dh must have shape {(m, inter)}, got {tuple(dh.shape)}")
+    dh = _contig(dh, stream)
+    if dgu is None:
+        dgu = torch.empty((m, 2 * inter), dtype=torch.bfloat16, device=a.device)
+    if h is None:
+        h = torch.empty((m, inter), dtype=torch.bfloat16, device=a.device)
+    _room(dgu, torch.bfloat16, "dgu", m * 2 * inter)
+    _room(h, torch.bfloat16, "h", m * inter)
+    _check(_lib.nvfp4_gated_gemm_backward(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(alpha), act, _ptr(dh), _ptr(dgu),
+                                          _ptr(h), m, inter, k, _ptr(workspace),
+                                          0 if workspace is None else workspace.numel(), flags, _stream(stream)))
+    return dgu, h
 
 
 def mxfp4_grouped_gemm(a, sfa, row_offsets, b, sfb, alpha=None, d=None, flags: int = 0, stream=None):

@@ -163,9 +163,10 @@ struct GemmCfg {
   // with bulk copies completing on the receiver's own barrier, instead of publishing every
   // partial with a cluster-scope release and reading it remotely.  The buffer holds one slice per
   // other rank: with U = BN*32 units of 16 bytes and S <= 8 ranks, (S-1) * ceil(U/S) <= U - U/8
-  // + 7 units; it follows the control block.
+  // + 7 units, and 16 over U - U/8 where the slices are whole groups of 8 units (the gated
+  // epilogues); it follows the control block.
   static constexpr bool PUSH_RED = !MULTI_TILE_ && BN_ == 32;
-  static constexpr int RCV_BYTES = PUSH_RED ? (BN_ * 32 - BN_ * 32 / 8 + 8) * 16 : 0;
+  static constexpr int RCV_BYTES = PUSH_RED ? (BN_ * 32 - BN_ * 32 / 8 + 16) * 16 : 0;
   static constexpr int smem_bytes(bool grouped) {
     return 1024 + RING_BYTES + CTRL_BYTES + RCV_BYTES + (grouped ? TABLE_BYTES : 0);
   }
@@ -224,7 +225,110 @@ struct GemmArgs {
   const __nv_bfloat16 *xq;
   int64_t ldx;
   const float *gs_q;
+  // Gated epilogues (EPI != kEpiPlain): operand rows alternate between 16 gate and 16 up rows,
+  // alpha points to two values (gate, up), the activation is g * sigmoid(g * (act_a + act_b g^2))
+  float act_a, act_b;
+  const __nv_bfloat16 *dh;  // kEpiGatedGrad: [tokens, n/2], the gradient of h
+  __nv_bfloat16 *h;         // kEpiGatedGrad: [tokens, n/2] or nullptr
+  int64_t ldh;              // row stride of dh and h (elements)
 };
+
+// What the epilogue makes of a tile.
+enum : int {
+  kEpiPlain = 0,      // d = bf16(alpha * C)
+  kEpiGated = 1,      // d = bf16(act(alpha0 * C_gate) * (alpha1 * C_up))
+  kEpiGatedGrad = 2   // d = the gradients of both products given dh, interleaved as C; h as above
+};
+
+// f = g * sigmoid(q), q = g * (a + b g^2), and its derivative f' = s + g s (1 - s) (a + 3 b g^2):
+// SiLU with a = 1, b = 0, GELU's tanh form with a = sqrt(8 / pi), b = 0.044715 a, because
+// (1 + tanh z) / 2 = sigmoid(2 z).  q is taken at g clamped to +-128, where the sigmoid is 0 or 1
+// in fp32 already, so that an infinite g gives no inf * 0.  (Approximate exp and reciprocal: both
+// are within a few fp32 ulps, and every result is rounded to bf16.)
+__device__ __forceinline__ void gate_act(const GemmArgs &p, float g, float &f, float &df) {
+  const float gc = fminf(fmaxf(g, -128.0f), 128.0f), g2 = gc * gc;
+  const float s = __fdividef(1.0f, 1.0f + __expf(-gc * (p.act_a + p.act_b * g2)));
+  f = g * s;
+  df = s + gc * s * (1.0f - s) * (p.act_a + 3.0f * p.act_b * g2);
+}
+
+// The gated epilogue of 32 columns of one row (16 gate, then 16 up) held by one thread: column
+// 32 j of the product is column 16 j of h.
+template <int EPI>
+__device__ __forceinline__ void gated_row_chunk(const GemmArgs &p, int64_t row, int64_t col, const float (&c)[32],
+                                                float a0, float a1) {
+  const int64_t hc = col >> 1;
+  uint32_t hv[8];
+  if constexpr (EPI == kEpiGated) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f[2], df;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        gate_act(p, a0 * c[2 * i + e], f[e], df);
+        f[e] *= a1 * c[16 + 2 * i + e];
+      }
+      hv[i] = pack_bf16x2(f[0], f[1]);
+    }
+    st_global_v8(p.d + row * p.ldd + hc, hv);
+  } else {
+    uint32_t dv[8], gv[8], uv[8];
+    ld_global_nc_v8(p.dh + row * p.ldh + hc, dv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f[2], df[2], u[2];
+      const float d[2] = {__uint_as_float(dv[i] << 16), __uint_as_float(dv[i] & 0xFFFF0000u)};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        gate_act(p, a0 * c[2 * i + e], f[e], df[e]);
+        u[e] = a1 * c[16 + 2 * i + e];
+      }
+      gv[i] = pack_bf16x2(d[0] * u[0] * df[0], d[1] * u[1] * df[1]);
+      uv[i] = pack_bf16x2(d[0] * f[0], d[1] * f[1]);
+      hv[i] = pack_bf16x2(f[0] * u[0], f[1] * u[1]);
+    }
+    st_global_v8(p.d + row * p.ldd + col, gv);
+    st_global_v8(p.d + row * p.ldd + col + 16, uv);
+    if (p.h) st_global_v8(p.h + row * p.ldh + hc, hv);
+  }
+}
+
+// The gated epilogue where operand A is the weight: one token, `N` neighbouring gate rows and their
+// up rows; wr is the first gate row in the interleaved weight.
+template <int EPI, int N>
+__device__ __forceinline__ void gated_col_units(const GemmArgs &p, int64_t token, int64_t wr, const float (&g)[N],
+                                                const float (&u)[N], float a0, float a1) {
+  const int64_t hc = ((wr >> 5) << 4) + (wr & 15);
+  float f[N], df[N], uu[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    gate_act(p, a0 * g[i], f[i], df[i]);
+    uu[i] = a1 * u[i];
+  }
+  auto store = [](__nv_bfloat16 *dst, const float (&v)[N]) {
+    if constexpr (N == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else
+      for (int i = 0; i < N; ++i) dst[i] = __float2bfloat16_rn(v[i]);
+  };
+  float hv[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) hv[i] = f[i] * uu[i];
+  if constexpr (EPI == kEpiGated) {
+    store(p.d + token * p.ldd + hc, hv);
+  } else {
+    float gv[N], uv[N];
+    const __nv_bfloat16 *dh = p.dh + token * p.ldh + hc;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float d = __bfloat162float(dh[i]);
+      gv[i] = d * uu[i] * df[i];
+      uv[i] = d * f[i];
+    }
+    store(p.d + token * p.ldd + wr, gv);
+    store(p.d + token * p.ldd + wr + 16, uv);
+    if (p.h) store(p.h + token * p.ldh + hc, hv);
+  }
+}
 
 // The 16 scale bytes of 512-byte scale tile `tile` that lane i of a scale writer puts in its
 // tensor-memory lane: rows i, i+32, i+64, i+96 (4 consecutive bytes each, one per scale column).
@@ -460,9 +564,9 @@ __device__ __forceinline__ float *sk_slot(const GemmArgs &p, int cta, int j) {
 // (every copy in flight at once, 16-byte pieces XOR-swizzled by row so the row-wise reads hit
 // distinct banks), then each thread adds its row and writes 64 bytes of bf16 per chunk with
 // 256-bit stores.  The plan keeps n * 16 KB within the ring.
-template <class C>
-__device__ __forceinline__ void sk_fixup(const GemmArgs &p, const TileInfo &t, const Seg &s, float alpha, int tid,
-                                         uint8_t *smem) {
+template <class C, int EPI>
+__device__ __forceinline__ void sk_fixup(const GemmArgs &p, const TileInfo &t, const Seg &s, float alpha, float alpha1,
+                                         int tid, uint8_t *smem) {
   constexpr int RING = C::RING_BYTES;
   constexpr int CHUNK_BYTES = 128 * 32 * 4;  // one 32-column chunk of a partial
   if (s.n * CHUNK_BYTES > RING) {  // never planned (the host caps contributors); uniform exit
@@ -508,6 +612,10 @@ __device__ __forceinline__ void sk_fixup(const GemmArgs &p, const TileInfo &t, c
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[4 * q + i] = jj == 0 ? f[i] : __fadd_rn(acc[4 * q + i], f[i]);
         }
+      }
+      if constexpr (EPI != kEpiPlain) {
+        gated_row_chunk<EPI>(p, t.out_i0 + row, t.out_j0 + 32 * c, acc, alpha, alpha1);
+        continue;
       }
       __nv_bfloat16 *out = p.d + (t.out_i0 + row) * p.ldd + t.out_j0 + 32 * c;
 #pragma unroll
@@ -670,6 +778,47 @@ __device__ __forceinline__ void reduce_read(const GemmArgs &p, const TileInfo &t
   }
 }
 
+// reduce_read of the gated epilogues: the work unit is four rows of h in one column, i.e. the gate
+// unit q*8 + i of 32-row group q and the up unit four after it (this rank takes units [u0, u1)).
+template <int EPI, int UPT, int SMAX>
+__device__ __forceinline__ void reduce_read_gated(const GemmArgs &p, const TileInfo &t, uint32_t red0, int u0, int u1,
+                                                  float a0, float a1, int tid, int nt) {
+  for (int ub = u0 + tid; ub < u1; ub += UPT * nt) {
+    float4 part[UPT][2][SMAX];
+#pragma unroll
+    for (int h = 0; h < UPT; ++h) {
+      const int u = ub + h * nt < u1 ? ub + h * nt : ub;
+      const int unit = (u >> 4) * 32 + ((u >> 2) & 3) * 8 + (u & 3);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int s = 0; s < SMAX; ++s)
+          if (s < p.splits) part[h][e][s] = ld_cluster_v4(map_to_rank(red0 + static_cast<uint32_t>((unit + 4 * e) * 16), s));
+    }
+#pragma unroll
+    for (int h = 0; h < UPT; ++h) {
+      const int u = ub + h * nt;
+      if (u >= u1) break;
+      float v[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float4 w = part[h][e][0];
+#pragma unroll
+        for (int s = 1; s < SMAX; ++s)
+          if (s < p.splits) {
+            w.x += part[h][e][s].x;
+            w.y += part[h][e][s].y;
+            w.z += part[h][e][s].z;
+            w.w += part[h][e][s].w;
+          }
+        v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
+      }
+      const int c = u >> 4, r0 = ((u >> 2) & 3) * 32 + (u & 3) * 4;
+      if (r0 < t.rows) gated_col_units<EPI, 4>(p, t.out_j0 + c, t.out_i0 + r0, v[0], v[1], a0, a1);
+    }
+  }
+}
+
 // Arrive on `bar` once the calling thread's tcgen05 operations so far are complete; for a CTA
 // pair, on the barrier at that offset in both CTAs.
 template <class C>
@@ -679,8 +828,9 @@ __device__ __forceinline__ void commit_to(uint32_t bar) {
 }
 
 // FUSED (swap-AB configurations only): operand B is quantised in the kernel (GemmArgs::xq); a
-// separate instantiation, so the other kernels carry none of that code.
-template <class C, bool GROUPED, bool FUSED = false>
+// separate instantiation, so the other kernels carry none of that code.  EPI: the gated epilogues are
+// instantiations of their own too (dense plans only).
+template <class C, bool GROUPED, bool FUSED = false, int EPI = kEpiPlain>
 __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
     bs_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmB3, const GemmArgs p) {
@@ -703,6 +853,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
   volatile int *sk_last = consumed + 2;       // stream-K: epilogue decision broadcast
   volatile float *alpha_s = reinterpret_cast<volatile float *>(sk_last + 1);  // alpha, read once
   volatile int *sf_issued = reinterpret_cast<volatile int *>(alpha_s + 1);   // pair: scale stages issued
+  volatile float *alpha1_s = reinterpret_cast<volatile float *>(sf_issued + 1);  // gated: alpha of the up rows
   int *tables = reinterpret_cast<int *>(ctrl + C::CTRL_BYTES);
   Tables<C, GROUPED> tb{tables, tables + (C::MAX_EXPERTS + 1), tables + 2 * (C::MAX_EXPERTS + 1)};
 
@@ -713,6 +864,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
   // units and reading the partials remotely was measured faster); the same on every CTA
   const bool push_red = C::PUSH_RED && p.splits > 1 && p.n >= 16;
   static_assert(!FUSED || (C::SWAP_ONLY && !GROUPED), "fused quantisation serves the swap-AB plans");
+  static_assert(EPI == kEpiPlain || (!FUSED && !GROUPED), "the gated epilogues serve the dense plans");
   const WaitCtl wc{p.wait_limit, abort_flag, p.status};
   // The next kernel may launch now: it waits (griddepcontrol.wait) for this grid to complete
   // before it reads our output, and its CTAs can meanwhile take the SM space we leave free.
@@ -1218,6 +1370,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
     // alpha is read by one thread and shared: a load left to each thread's first use was
     // scheduled there, putting a full memory latency (~1400 cycles) in front of the stores.
     if (tid == 0) *alpha_s = p.alpha ? *p.alpha : 1.0f;
+    if (EPI != kEpiPlain && tid == 1) *alpha1_s = p.alpha[1];
     {
       // Touch the output lines of this CTA's first tile now: the first store to a cold page
       // otherwise waits for its address translation at the very end of the kernel.
@@ -1225,18 +1378,21 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
       Seg sg{};
       if (w.next(p, sg)) {
         const TileInfo t = tile_info<C, GROUPED>(p, tb, sg.tile, crank);
+        // (h is half as wide as the product)
+        constexpr int HALF = EPI == kEpiGated ? 1 : 0;
         if (row < t.rows) {
           if (p.swap) {
-            prefetch_l2(p.d + t.out_j0 * p.ldd + t.out_i0 + row);
-            prefetch_l2(p.d + (t.out_j0 + t.cols - 1) * p.ldd + t.out_i0 + row);
+            prefetch_l2(p.d + t.out_j0 * p.ldd + ((t.out_i0 + row) >> HALF));
+            prefetch_l2(p.d + (t.out_j0 + t.cols - 1) * p.ldd + ((t.out_i0 + row) >> HALF));
           } else {
-            prefetch_l2(p.d + (t.out_i0 + row) * p.ldd + t.out_j0);
+            prefetch_l2(p.d + (t.out_i0 + row) * p.ldd + (t.out_j0 >> HALF));
           }
         }
       }
     }
     named_barrier_sync(2, 128);
     const float alpha = *alpha_s;
+    const float alpha1 = EPI != kEpiPlain ? *alpha1_s : 0.0f;
     int acc = 0;
     uint32_t acc_phase = 0;
     Work w = work0;
@@ -1275,7 +1431,14 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
             st_global_v8(dst + 8 * q, v);
           }
         } else if (!C::SWAP_ONLY) {
-          if (row < t.rows && 32 * c < t.cols) {
+          if constexpr (EPI != kEpiPlain) {
+            if (row < t.rows && 32 * c < t.cols) {
+              float v[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+              gated_row_chunk<EPI>(p, t.out_i0 + row, t.out_j0 + 32 * c, v, alpha, alpha1);
+            }
+          } else if (row < t.rows && 32 * c < t.cols) {
             __nv_bfloat16 *out = p.d + (t.out_i0 + row) * p.ldd + t.out_j0 + 32 * c;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1289,6 +1452,18 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
           }
         } else if (row < t.rows) {
           // operand A is the weight: TMEM lane = output column, TMEM column = output row
+          if constexpr (EPI != kEpiPlain) {
+            // lanes 0..15 hold gate rows, lanes 16..31 the up rows (valid rows come in whole warps)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float o = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(r[i]), 16);
+              if (32 * c + i < t.cols && lane < 16) {
+                const float g1[1] = {__uint_as_float(r[i])}, u1[1] = {o};
+                gated_col_units<EPI, 1>(p, t.out_j0 + 32 * c + i, t.out_i0 + row, g1, u1, alpha, alpha1);
+              }
+            }
+            continue;
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int j = 32 * c + i;
@@ -1331,7 +1506,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
           Work rest = w;
           Seg more;
           if (!rest.next(p, more)) {
-            sk_fixup<C>(p, t, sg, alpha, tid, smem);
+            sk_fixup<C, EPI>(p, t, sg, alpha, alpha1, tid, smem);
           } else {
             pending = sg;
             has_pending = true;
@@ -1343,7 +1518,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
       named_barrier_sync(2, 128);
       if (tid == 0) *sk_last = *abort_flag ? -1 : 1;  // after a time-out copies may still land in the ring
       named_barrier_sync(2, 128);
-      if (*sk_last == 1) sk_fixup<C>(p, tile_info<C, GROUPED>(p, tb, pending.tile, crank), pending, alpha, tid, smem);
+      if (*sk_last == 1) sk_fixup<C, EPI>(p, tile_info<C, GROUPED>(p, tb, pending.tile, crank), pending, alpha, alpha1,
+                                              tid, smem);
     }
   }
 
@@ -1398,14 +1574,16 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
         w.next(p, sg);
         const TileInfo t = tile_info<C, GROUPED>(p, tb, sg.tile, crank);
         const float alpha = *alpha_s;
-        const int units = min(t.cols, C::BN) * 32;
-        const int slot = (units + S - 1) / S;  // units of the largest slice
-        const int u0 = rank * units / S, u1 = (rank + 1) * units / S;
+        // (the gated epilogues cut the units in whole groups of 8: the gate and up units of a column's 32 rows)
+        constexpr int GRP = EPI != kEpiPlain ? 8 : 1;
+        const int units = min(t.cols, C::BN) * 32 / GRP;  // in groups
+        const int slot = (units + S - 1) / S * GRP;  // units of the largest slice
+        const int u0 = rank * units / S * GRP, u1 = (rank + 1) * units / S * GRP;
         const uint32_t red0 = smem_u32(smem), rcv0 = smem_u32(ctrl + C::CTRL_BYTES);
         if (threadIdx.x == 0) {
           mbar_arrive_expect_tx(smem_u32(rbar), static_cast<uint32_t>((S - 1) * (u1 - u0) * 16));
           for (int r = 0; r < S; ++r) {
-            const int a0 = r * units / S, a1 = (r + 1) * units / S;
+            const int a0 = r * units / S * GRP, a1 = (r + 1) * units / S * GRP;
             if (r != rank && a1 > a0)
               bulk_copy_to_peer(map_to_rank(rcv0 + static_cast<uint32_t>((rank < r ? rank : rank - 1) * slot * 16), r),
                                 red0 + a0 * 16,
@@ -1415,7 +1593,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
         if (mbar_wait(smem_u32(rbar), 0, wc, kSiteEpilogue)) {
           const float4 *own = reinterpret_cast<const float4 *>(smem);
           const float4 *rcv = reinterpret_cast<const float4 *>(ctrl + C::CTRL_BYTES);
-          for (int u = u0 + static_cast<int>(threadIdx.x); u < u1; u += C::THREADS) {
+          auto sum_ranks = [&](int u) {
             float4 v = rank == 0 ? own[u] : rcv[u - u0];  // (source 0 sits in slot 0)
             for (int s2 = 1; s2 < S; ++s2) {
               const float4 q = s2 == rank ? own[u] : rcv[(s2 < rank ? s2 : s2 - 1) * slot + (u - u0)];
@@ -1424,6 +1602,23 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
               v.z += q.z;
               v.w += q.w;
             }
+            return v;
+          };
+          if constexpr (EPI != kEpiPlain) {
+            // unit i of four h rows in a group: its gate unit and the up unit four after it
+            const float alpha1 = *alpha1_s;
+            for (int i = static_cast<int>(threadIdx.x); i < (u1 - u0) / 2; i += C::THREADS) {
+              const int u = u0 + (i >> 2) * 8 + (i & 3);
+              const float4 g = sum_ranks(u), x = sum_ranks(u + 4);
+              const int c = u / 32, r0 = (u % 32) * 4;
+              if (r0 < t.rows) {
+                const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {x.x, x.y, x.z, x.w};
+                gated_col_units<EPI, 4>(p, t.out_j0 + c, t.out_i0 + r0, gv, uv, alpha, alpha1);
+              }
+            }
+          } else
+          for (int u = u0 + static_cast<int>(threadIdx.x); u < u1; u += C::THREADS) {
+            const float4 v = sum_ranks(u);
             const int c = (u * 4) / 128, r0 = (u * 4) % 128;
             if (r0 < t.rows) {
               uint2 pk;  // (swap-AB: the output row is the token, the 4 values are weight rows)
@@ -1452,6 +1647,11 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
         const int units = min(t.cols, C::BN) * 32;  // float4 groups of the valid columns
         const int u0 = rank * units / p.splits, u1 = (rank + 1) * units / p.splits;
         const uint32_t red0 = smem_u32(smem);
+        if constexpr (EPI != kEpiPlain) {
+          const int pairs = min(t.cols, C::BN) * 16;  // units of four h rows
+          const int p0 = rank * pairs / p.splits, p1 = (rank + 1) * pairs / p.splits;
+          reduce_read_gated<EPI, 1, 8>(p, t, red0, p0, p1, alpha, *alpha1_s, static_cast<int>(threadIdx.x), C::THREADS);
+        } else {
         // Two ranks of a 128- or 256-wide tile: four units per thread in flight, else two.  (More
         // loads in flight per thread were measured slower with four ranks: the distributed
         // shared-memory reads congest.  The narrower tiles keep one form, whose code measured
@@ -1464,6 +1664,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
           }
         }
         if (!done) reduce_read<2, 8>(p, t, red0, u0, u1, alpha, static_cast<int>(threadIdx.x), C::THREADS);
+        }
       }
       // no CTA leaves while another may still read its partial; those reads are complete here
       // (their sums are stored), so the arrive publishes nothing
