@@ -17,6 +17,7 @@
  *                       one kernel; nvfp4_gated_gemm_backward: the gradients of both projections
  *   decoder block       block_norm, block_norm_quantize, block_norm_backward (the norms before and
  *                       after a block with its gate and residual sum)
+ *   sample_tokens       one token per row of logits: temperature, top-k, top-p, min-p
  *   sizes and status    nvfp4_sf_bytes, mxfp4_grouped_sf_bytes, moe_sort_workspace_size,
  *                       nvfp4_check_status, nvfp4_last_error
  *
@@ -420,8 +421,8 @@ nvfp4_status_t moe_combine(const void *y, int64_t rows, const int32_t *pos, cons
  *   gate    bf16 [m, n] with row stride ldg, or [n] shared by all rows with ldg = 0
  *   x_out   x's type [m, n], row stride ldxo; may be x itself (same stride); no other overlap
  *   h       bf16 [m, n], row stride ldh
- *   1 <= n <= 32768.  Any strides and alignments of whole elements are taken; rows that all start
- *   on 16 bytes (and n % 8 == 0) are moved with 16-byte accesses.
+ *   1 <= n <= 32768.  Any strides (of an input also 0: one row for all) and alignments of whole
+ *   elements are taken; rows that all start on 16 bytes (and n % 8 == 0) are moved with 16-byte accesses.
  * Every input is read and every output written after the PDL wait. */
 enum { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_F32 = 1 };
 nvfp4_status_t block_norm(const void *x, int x_type, int64_t ldx, const void *y, int64_t ldy, const void *w_post,
@@ -458,6 +459,35 @@ nvfp4_status_t block_norm_backward(const void *dh, int64_t lddh, const void *dx_
                                    float weight_offset, void *dx, int64_t lddx, void *dy, int64_t lddy, float *dw_pre,
                                    float *dw_post, void *dgate, int64_t lddg, int64_t m, int64_t n, void *workspace,
                                    size_t workspace_bytes, uint32_t flags, nvfp4_stream_t stream);
+
+/* ---------------------------------------------------------------- draw of the next token
+ * One token per row of logits, from a random number given per row.  Not an operation of the pages:
+ * it is what a decoder does with the last product's rows.  For a row z with largest logit m (fp32,
+ * each step rounded to nearest):
+ *   x_i = (z_i - m) * (log2(e) / temperature),  e_i = 2^x_i,  w_i = rint(e_i * 2^30)
+ * (2^x by the hardware's approximation, within 2^-22).  Tokens are ordered by x, largest first, ties by
+ * index; each filter keeps a beginning of that order, and the first token always stays:
+ *   top_k   the first top_k (<= 0: all)
+ *   top_p   those before which the top_k weigh less than top_p * their total (>= 1: all)
+ *   min_p   those with e_i >= min_p (<= 0: all)
+ * The token is the first, by index, at which the kept tokens' cumulative weight exceeds
+ * floor(uniform * total).  The weights are whole numbers and their sums exact, so the result depends
+ * neither on timing nor on how a row is split.
+ *   logits       bf16 or fp32 (logits_type: NVFP4_DTYPE_*) [rows, vocab], row stride ld >= vocab or
+ *                0 (one row for all), any alignment of whole elements.  NaN and -inf weigh nothing;
+ *                with +inf only the +inf tokens weigh.  A row with nothing else than NaN and -inf gives token -1.
+ *   uniform      fp32 [rows], in [0, 1) (values outside draw the first or the last kept token)
+ *   temperature  fp32 [rows] or NULL for 1; <= 0 (or NaN): the largest logit, lowest index
+ *   top_k        int32 [rows] or NULL;  top_p, min_p  fp32 [rows] or NULL
+ *   tokens       int32 [rows]
+ *   logprobs     fp32 [rows] or NULL: log of the token's probability among the kept ones (-inf for
+ *                token -1)
+ *   1 <= vocab <= 2^21, rows < 2^28.  One launch, no workspace.
+ * Every input is read and every output written after the PDL wait. */
+nvfp4_status_t sample_tokens(const void *logits, int logits_type, int64_t ld, const float *uniform,
+                             const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                             int32_t *tokens, float *logprobs, int64_t rows, int64_t vocab, uint32_t flags,
+                             nvfp4_stream_t stream);
 
 /* Scale layout conversion between a row-major scale matrix [rows, cols] (bytes) and the
  * 128x4 swizzled layout of nvfp4_sf_bytes size (swizzle writes the zero padding).

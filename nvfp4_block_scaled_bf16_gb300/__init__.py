@@ -70,6 +70,7 @@ _SIGS = {
     "block_norm_backward_workspace_size": (_sz, [_i64, _i64]),
     "block_norm_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _f32, _f32,
                                    _f32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _u32, _vp]),
+    "sample_tokens": (_int, [_vp, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _u32, _vp]),
     "nvfp4_check_status": (_int, [_vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -629,8 +630,8 @@ def _channels(t, name, n):
         raise ValueError(f"{name} must be a contiguous vector of {n}")
 
 
-def _block_operands(x, w_pre, y, w_post, gate):
-    """Checks what the forward and backward norms share: (x_type, m, n, row strides of x, y and gate)."""
+def _block_operands(x, w_pre, y, w_post, gate, stream):
+    """Checks what the forward and backward norms share: (x_type, m, n, row strides of x, y and gate, gate)."""
     _check_device(x, "x")
     if x.dtype not in _STREAM_TYPES:
         raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
@@ -642,16 +643,19 @@ def _block_operands(x, w_pre, y, w_post, gate):
     if y is None:
         if w_post is not None or gate is not None:
             raise ValueError("w_post and gate belong to y")
-        return _STREAM_TYPES[x.dtype], m, n, ldx, 0, 0
+        return _STREAM_TYPES[x.dtype], m, n, ldx, 0, 0, None
     ldy = _rows(y, torch.bfloat16, "y", m, n)
     _channels(w_post, "w_post", n)
     ldg = 0
     if gate is not None:
         if gate.dim() == 2:
             ldg = _rows(gate, torch.bfloat16, "gate", m, n)
+            if ldg < n:      # rows expanded from one: a gate per token still, with a gradient per token
+                gate = _contig(gate, stream)
+                ldg = n
         else:
             _channels(gate, "gate", n)
-    return _STREAM_TYPES[x.dtype], m, n, ldx, ldy, ldg
+    return _STREAM_TYPES[x.dtype], m, n, ldx, ldy, ldg, gate
 
 
 def block_norm(x, w_pre=None, y=None, w_post=None, gate=None, residual_scale: float = 1.0, eps: float = 1e-6,
@@ -662,7 +666,7 @@ def block_norm(x, w_pre=None, y=None, w_post=None, gate=None, residual_scale: fl
     x bf16 or fp32 [m, n], y bf16 [m, n] or None (h = norm(x) only), weights bf16 [n] or None, gate
     bf16 [n] or [m, n] or None.  Returns (x_out, h): the stream in x's type (x itself without y) and
     bf16 [m, n] (None without w_pre).  x_out may be x."""
-    xt, m, n, ldx, ldy, ldg = _block_operands(x, w_pre, y, w_post, gate)
+    xt, m, n, ldx, ldy, ldg, gate = _block_operands(x, w_pre, y, w_post, gate, stream)
     ldo = ldh = 0
     if y is not None:
         if x_out is None:
@@ -685,7 +689,7 @@ def block_norm_quantize(x, w_pre, gs, y=None, w_post=None, gate=None, residual_s
                         weight_offset: float = 0.0, x_out=None, q=None, sf=None, flags: int = 0, stream=None):
     """block_norm whose h is quantised on the way out: (x_out, q, sf) with q and sf equal to
     nvfp4_quantize(h, gs)."""
-    xt, m, n, ldx, ldy, ldg = _block_operands(x, w_pre, y, w_post, gate)
+    xt, m, n, ldx, ldy, ldg, gate = _block_operands(x, w_pre, y, w_post, gate, stream)
     if w_pre is None:
         raise ValueError("w_pre is needed")
     _room(gs, torch.float32, "gs", 1)
@@ -719,7 +723,7 @@ def block_norm_backward(dh, dx_out, x_out, w_pre=None, y=None, w_post=None, gate
 
     Returns (dx, dy, dw_pre, dw_post, dgate): dx in x_out's type, dy bf16, the weights' gradients fp32 [n],
     dgate fp32 [n] for a gate per channel or bf16 [m, n] for a gate per token; None for what was absent."""
-    xt, m, n, ldr, ldy, ldg = _block_operands(x_out, w_pre, y, w_post, gate)
+    xt, m, n, ldr, ldy, ldg, gate = _block_operands(x_out, w_pre, y, w_post, gate, stream)
     if (dh is None) != (w_pre is None):
         raise ValueError("dh and w_pre: give both or neither")
     lddh = 0 if dh is None else _rows(dh, torch.bfloat16, "dh", m, n)
@@ -743,6 +747,42 @@ def block_norm_backward(dh, dx_out, x_out, w_pre=None, y=None, w_post=None, gate
                                     _ptr(dy), n, _ptr(dw_pre), _ptr(dw_post), _ptr(dgate), n if ldg else 0, m, n,
                                     _ptr(workspace), workspace.numel(), flags, _stream(stream)))
     return dx, dy, dw_pre, dw_post, dgate
+
+
+# ---------------------------------------------------------------- draw of the next token
+def sample_tokens(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logprobs=None,
+                  flags: int = 0, stream=None):
+    """One token per row of logits (bf16 or fp32 [rows, vocab], any row stride) from uniform, fp32 [rows]
+    in [0, 1).  temperature, top_p, min_p fp32 [rows] and top_k int32 [rows], each None for off; a
+    temperature <= 0 takes the largest logit.  Ties go to the lowest index; the result does not depend on
+    how the work is split.
+
+    Returns (tokens int32 [rows], logprobs fp32 [rows]): -1 where a row holds nothing but -inf and NaN;
+    the log-probability is the one among the tokens the filters kept."""
+    _check_device(logits, "logits")
+    if logits.dtype not in _STREAM_TYPES:
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must have 2 dimensions")
+    rows, vocab = logits.shape
+    ld = _rows(logits, logits.dtype, "logits", rows, vocab)
+    for t_, dtype, name in ((uniform, torch.float32, "uniform"), (temperature, torch.float32, "temperature"),
+                            (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p")):
+        if t_ is not None:
+            _need(t_, dtype, name, 1)
+            if t_.numel() != rows or not t_.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous vector of {rows}")
+    if uniform is None:
+        raise TypeError("uniform is needed")
+    if tokens is None:
+        tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    if logprobs is None:
+        logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _room(tokens, torch.int32, "tokens", rows)
+    _room(logprobs, torch.float32, "logprobs", rows)
+    _check(_lib.sample_tokens(_ptr(logits), _STREAM_TYPES[logits.dtype], ld, _ptr(uniform), _ptr(temperature), _ptr(top_k),
+                              _ptr(top_p), _ptr(min_p), _ptr(tokens), _ptr(logprobs), rows, vocab, flags, _stream(stream)))
+    return tokens, logprobs
 
 
 def check_status(stream=None) -> None:

@@ -485,6 +485,8 @@ int grad_teams(int64_t m, const Shape &s, int sm_count) {
 }
 
 bool rows_aligned(const void *p, int64_t ld, int elem) { return !p || (aligned(p, 16) && ld * elem % 16 == 0); }
+// Row stride of an input: 0 (one row for all) or at least a row.
+bool in_stride(int64_t ld, int64_t n) { return ld == 0 || ld >= n; }
 int elem_of(int type) { return type == NVFP4_DTYPE_F32 ? 4 : 2; }
 
 // The checks that the forward entry points share.
@@ -499,7 +501,7 @@ nvfp4_status_t check_norm(const char *name, const void *x, int x_type, int64_t l
   if (!y && (w_post || gate || x_out))
     return fail(NVFP4_ERR_INVALID_ARG, "%s: w_post, gate and x_out belong to y, which is NULL", name);
   if (!y && !w_pre) return fail(NVFP4_ERR_INVALID_ARG, "%s: neither y nor w_pre: nothing to compute", name);
-  if (ldx < n || (y && ldy < n) || (gate && ldg != 0 && ldg < n) || (x_out && ldxo < n))
+  if (!in_stride(ldx, n) || (y && !in_stride(ldy, n)) || (gate && !in_stride(ldg, n)) || (x_out && ldxo < n))
     return fail(NVFP4_ERR_INVALID_ARG, "%s: row strides ldx=%lld ldy=%lld ldg=%lld ldxo=%lld are shorter than n=%lld", name,
                 (long long)ldx, (long long)ldy, (long long)ldg, (long long)ldxo, (long long)n);
   if (!x || (y && !x_out)) return fail(NVFP4_ERR_INVALID_ARG, "%s: null pointer", name);
@@ -606,8 +608,8 @@ extern "C" nvfp4_status_t block_norm_backward(const void *dh, int64_t lddh, cons
     return fail(NVFP4_ERR_INVALID_ARG, "%s: w_post, gate, dy, dw_post and dgate belong to y, which is NULL", name);
   if ((dh != nullptr) != (w_pre != nullptr) && m > 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: dh and w_pre: give both or neither", name);
   const bool token_gate = gate && ldg != 0;
-  if (ldxo < n || lddx < n || (dh && lddh < n) || (dx_out && lddxo < n) || (y && (ldy < n || lddy < n)) ||
-      (token_gate && (ldg < n || lddg < n)))
+  if (!in_stride(ldxo, n) || lddx < n || (dh && !in_stride(lddh, n)) || (dx_out && !in_stride(lddxo, n)) ||
+      (y && (!in_stride(ldy, n) || lddy < n)) || (token_gate && (ldg < n || lddg < n)))
     return fail(NVFP4_ERR_INVALID_ARG, "%s: a row stride is shorter than n=%lld", name, (long long)n);
   if ((w_pre != nullptr) != (dw_pre != nullptr) || (w_post != nullptr) != (dw_post != nullptr) ||
       (gate != nullptr) != (dgate != nullptr))

@@ -267,3 +267,20 @@ def test_another_stream(nv):
         g = nv.block_norm_backward(d["dh"], d["dr"], d["x"], d["w_pre"], y=d["y"], w_post=d["w_post"])
     s.synchronize()
     assert torch.equal(h, want) and all(a is b or torch.equal(a, b) for a, b in zip(g, g_want))
+
+
+def test_broadcast_inputs(nv):
+    """Rows expanded from one row are read as they are; the gradients come for every row."""
+    m, n = 7, 264
+    d = inputs(m, n, gate="token")
+    for k in ("x", "y", "gate", "dh", "dr"):
+        d[k] = d[k][:1].expand(m, n)
+    full = {k: (v.contiguous() if v is not None else None) for k, v in d.items()}
+    for a, b in zip(nv.block_norm(d["x"], d["w_pre"], y=d["y"], w_post=d["w_post"], gate=d["gate"]),
+                    nv.block_norm(full["x"], full["w_pre"], y=full["y"], w_post=full["w_post"], gate=full["gate"])):
+        assert torch.equal(a, b)
+    got = check_backward(nv, d, 0.7, 0.0)
+    want = check_backward(nv, full, 0.7, 0.0)
+    assert got[4].shape == (m, n)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
