@@ -97,23 +97,29 @@ def _check(code: int) -> None:
         raise NVFP4Error(code, last_error())
 
 
+# The pointers and the stream go to ctypes as plain integers (its argument types make them void *), and
+# the device and stream are asked of torch's C layer: a small call spends its time here, not on the GPU.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _check_device(t, name):
     """The library launches on the current CUDA device; every tensor must live there."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    cur = torch.cuda.current_device()
+    cur = _current_device()
     if t.get_device() != cur:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{cur}")
 
@@ -339,14 +345,13 @@ def _gated_operands(a, sfa, b, sfb, alpha, activation, workspace):
     _need(a, torch.uint8, "a", 2)
     _need(b, torch.uint8, "b", 2)
     m, kh = a.shape
-    n = b.shape[0]
-    if b.shape[1] != kh:
+    n, kb = b.shape
+    if kb != kh:
         raise ValueError("a and b disagree on K")
     if n % 2:
         raise ValueError("b must hold as many gate rows as up rows")
-    for t_, name in ((a, "a"), (b, "b")):
-        if not t_.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    if not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("a and b must be contiguous")
     _room(sfa, torch.uint8, "sfa", sf_bytes(m, 2 * kh))
     _room(sfb, torch.uint8, "sfb", sf_bytes(n, 2 * kh))
     _room(alpha, torch.float32, "alpha", 2)
@@ -370,8 +375,9 @@ def nvfp4_gated_gemm(a, sfa, b, sfb, alpha, activation: str = "silu", h=None, fl
     (interleave_gate_up), alpha fp32 [2], activation "silu" or "gelu_tanh"; workspace as nvfp4_gemm."""
     m, inter, k, act, workspace = _gated_operands(a, sfa, b, sfb, alpha, activation, workspace)
     if h is None:
-        h = torch.empty((m, inter), dtype=torch.bfloat16, device=a.device)
-    _room(h, torch.bfloat16, "h", m * inter)
+        h = a.new_empty((m, inter), dtype=torch.bfloat16)
+    else:
+        _room(h, torch.bfloat16, "h", m * inter)
     _check(_lib.nvfp4_gated_gemm(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(alpha), act, _ptr(h), m, inter, k,
                                  _ptr(workspace), 0 if workspace is None else workspace.numel(), flags, _stream(stream)))
     return h
@@ -611,51 +617,70 @@ def moe_combine(y, pos, weights, out=None, flags: int = 0, stream=None):
 _STREAM_TYPES = {torch.bfloat16: 0, torch.float32: 1}   # NVFP4_DTYPE_*
 
 
-def _rows(t, dtype, name, m, n):
-    """A [m, n] operand with contiguous rows at any row stride; returns the stride."""
-    _need(t, dtype, name, 2)
-    if tuple(t.shape) != (m, n):
+def _rows(t, dtype, name, m, n, dev):
+    """A [m, n] operand on device `dev` with contiguous rows at any row stride; returns the stride."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == 2):
+        _need(t, dtype, name, 2)
+        raise ValueError(f"{name} is on another device")
+    ld, step = t.stride()
+    if t.shape != (m, n):
         raise ValueError(f"{name} must have shape {(m, n)}, got {tuple(t.shape)}")
-    if n > 1 and t.stride(1) != 1:
+    if step != 1 and n > 1:
         raise ValueError(f"{name} rows must be contiguous")
-    return t.stride(0) if m > 1 else max(n, t.stride(0))
+    return ld if m > 1 else max(n, ld)
 
 
-def _channels(t, name, n):
-    """A bf16 [n] vector (None: absent)."""
+def _vector(t, dtype, name, n, dev):
+    """A contiguous [n] vector on device `dev` (None: absent)."""
     if t is None:
         return
-    _need(t, torch.bfloat16, name, 1)
-    if t.numel() != n or not t.is_contiguous():
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == 1):
+        _need(t, dtype, name, 1)
+        raise ValueError(f"{name} is on another device")
+    if t.numel() != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {n}")
 
 
 def _block_operands(x, w_pre, y, w_post, gate, stream):
-    """Checks what the forward and backward norms share: (x_type, m, n, row strides of x, y and gate, gate)."""
+    """Checks what the forward and backward norms share:
+    (x_type, m, n, device index, row strides of x, y and gate, gate)."""
     _check_device(x, "x")
-    if x.dtype not in _STREAM_TYPES:
+    xt = _STREAM_TYPES.get(x.dtype)
+    if xt is None:
         raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
     if x.dim() != 2:
         raise ValueError("x must have 2 dimensions")
     m, n = x.shape
-    ldx = _rows(x, x.dtype, "x", m, n)
-    _channels(w_pre, "w_pre", n)
+    dev = x.get_device()
+    ldx = _rows(x, x.dtype, "x", m, n, dev)
+    _vector(w_pre, torch.bfloat16, "w_pre", n, dev)
     if y is None:
         if w_post is not None or gate is not None:
             raise ValueError("w_post and gate belong to y")
-        return _STREAM_TYPES[x.dtype], m, n, ldx, 0, 0, None
-    ldy = _rows(y, torch.bfloat16, "y", m, n)
-    _channels(w_post, "w_post", n)
+        return xt, m, n, dev, ldx, 0, 0, None
+    ldy = _rows(y, torch.bfloat16, "y", m, n, dev)
+    _vector(w_post, torch.bfloat16, "w_post", n, dev)
     ldg = 0
     if gate is not None:
-        if gate.dim() == 2:
-            ldg = _rows(gate, torch.bfloat16, "gate", m, n)
+        if isinstance(gate, torch.Tensor) and gate.dim() == 2:
+            ldg = _rows(gate, torch.bfloat16, "gate", m, n, dev)
             if ldg < n:      # rows expanded from one: a gate per token still, with a gradient per token
                 gate = _contig(gate, stream)
                 ldg = n
         else:
-            _channels(gate, "gate", n)
-    return _STREAM_TYPES[x.dtype], m, n, ldx, ldy, ldg, gate
+            _vector(gate, torch.bfloat16, "gate", n, dev)
+    return xt, m, n, dev, ldx, ldy, ldg, gate
+
+
+def _stream_out(x, y, x_out, m, n, dev):
+    """x_out (made where it is missing) and its row stride."""
+    if y is None:
+        if x_out is not None:
+            raise ValueError("x_out belongs to y")
+        return None, 0
+    if x_out is None:
+        return x.new_empty((m, n)), n
+    return x_out, _rows(x_out, x.dtype, "x_out", m, n, dev)
 
 
 def block_norm(x, w_pre=None, y=None, w_post=None, gate=None, residual_scale: float = 1.0, eps: float = 1e-6,
@@ -666,20 +691,16 @@ def block_norm(x, w_pre=None, y=None, w_post=None, gate=None, residual_scale: fl
     x bf16 or fp32 [m, n], y bf16 [m, n] or None (h = norm(x) only), weights bf16 [n] or None, gate
     bf16 [n] or [m, n] or None.  Returns (x_out, h): the stream in x's type (x itself without y) and
     bf16 [m, n] (None without w_pre).  x_out may be x."""
-    xt, m, n, ldx, ldy, ldg, gate = _block_operands(x, w_pre, y, w_post, gate, stream)
-    ldo = ldh = 0
-    if y is not None:
-        if x_out is None:
-            x_out = torch.empty((m, n), dtype=x.dtype, device=x.device)
-        ldo = _rows(x_out, x.dtype, "x_out", m, n)
-    elif x_out is not None:
-        raise ValueError("x_out belongs to y")
-    if w_pre is not None:
-        if h is None:
-            h = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
-        ldh = _rows(h, torch.bfloat16, "h", m, n)
-    elif h is not None:
-        raise ValueError("h belongs to w_pre")
+    xt, m, n, dev, ldx, ldy, ldg, gate = _block_operands(x, w_pre, y, w_post, gate, stream)
+    x_out, ldo = _stream_out(x, y, x_out, m, n, dev)
+    ldh = n
+    if w_pre is None:
+        if h is not None:
+            raise ValueError("h belongs to w_pre")
+    elif h is None:
+        h = x.new_empty((m, n), dtype=torch.bfloat16)
+    else:
+        ldh = _rows(h, torch.bfloat16, "h", m, n, dev)
     _check(_lib.block_norm(_ptr(x), xt, ldx, _ptr(y), ldy, _ptr(w_post), _ptr(gate), ldg, _ptr(w_pre), residual_scale,
                            eps, weight_offset, _ptr(x_out), ldo, _ptr(h), ldh, m, n, flags, _stream(stream)))
     return (x if y is None else x_out), h
@@ -689,23 +710,20 @@ def block_norm_quantize(x, w_pre, gs, y=None, w_post=None, gate=None, residual_s
                         weight_offset: float = 0.0, x_out=None, q=None, sf=None, flags: int = 0, stream=None):
     """block_norm whose h is quantised on the way out: (x_out, q, sf) with q and sf equal to
     nvfp4_quantize(h, gs)."""
-    xt, m, n, ldx, ldy, ldg, gate = _block_operands(x, w_pre, y, w_post, gate, stream)
+    xt, m, n, dev, ldx, ldy, ldg, gate = _block_operands(x, w_pre, y, w_post, gate, stream)
     if w_pre is None:
         raise ValueError("w_pre is needed")
     _room(gs, torch.float32, "gs", 1)
-    ldo = 0
-    if y is not None:
-        if x_out is None:
-            x_out = torch.empty((m, n), dtype=x.dtype, device=x.device)
-        ldo = _rows(x_out, x.dtype, "x_out", m, n)
-    elif x_out is not None:
-        raise ValueError("x_out belongs to y")
+    x_out, ldo = _stream_out(x, y, x_out, m, n, dev)
+    need = sf_bytes(m, n // 16 * 16, 16)
     if q is None:
-        q = torch.empty((m, n // 2), dtype=torch.uint8, device=x.device)
+        q = x.new_empty((m, n // 2), dtype=torch.uint8)
+    else:
+        _room(q, torch.uint8, "q", m * (n // 2))
     if sf is None:
-        sf = torch.empty(sf_bytes(m, n // 16 * 16, 16), dtype=torch.uint8, device=x.device)
-    _room(q, torch.uint8, "q", m * (n // 2))
-    _room(sf, torch.uint8, "sf", sf_bytes(m, n // 16 * 16, 16))
+        sf = x.new_empty(need, dtype=torch.uint8)
+    else:
+        _room(sf, torch.uint8, "sf", need)
     _check(_lib.block_norm_quantize(_ptr(x), xt, ldx, _ptr(y), ldy, _ptr(w_post), _ptr(gate), ldg, _ptr(w_pre),
                                     residual_scale, eps, weight_offset, _ptr(x_out), ldo, _ptr(gs), _ptr(q), _ptr(sf),
                                     m, n, flags, _stream(stream)))
@@ -723,24 +741,23 @@ def block_norm_backward(dh, dx_out, x_out, w_pre=None, y=None, w_post=None, gate
 
     Returns (dx, dy, dw_pre, dw_post, dgate): dx in x_out's type, dy bf16, the weights' gradients fp32 [n],
     dgate fp32 [n] for a gate per channel or bf16 [m, n] for a gate per token; None for what was absent."""
-    xt, m, n, ldr, ldy, ldg, gate = _block_operands(x_out, w_pre, y, w_post, gate, stream)
+    xt, m, n, dev, ldr, ldy, ldg, gate = _block_operands(x_out, w_pre, y, w_post, gate, stream)
     if (dh is None) != (w_pre is None):
         raise ValueError("dh and w_pre: give both or neither")
-    lddh = 0 if dh is None else _rows(dh, torch.bfloat16, "dh", m, n)
-    lddr = 0 if dx_out is None else _rows(dx_out, x_out.dtype, "dx_out", m, n)
-    dev = x_out.device
+    lddh = 0 if dh is None else _rows(dh, torch.bfloat16, "dh", m, n, dev)
+    lddr = 0 if dx_out is None else _rows(dx_out, x_out.dtype, "dx_out", m, n, dev)
 
     def new(shape, dtype, wanted):
-        return torch.empty(shape, dtype=dtype, device=dev) if wanted else None
+        return x_out.new_empty(shape, dtype=dtype) if wanted else None
 
-    dx = new((m, n), x_out.dtype, True)
+    dx = x_out.new_empty((m, n))
     dy = new((m, n), torch.bfloat16, y is not None)
     dw_pre = new(n, torch.float32, w_pre is not None)
     dw_post = new(n, torch.float32, w_post is not None)
     dgate = new((m, n), torch.bfloat16, True) if ldg else new(n, torch.float32, gate is not None)
     if workspace is None:
         # made on the launch stream, so that its memory is not handed out before that stream is done with it
-        workspace = _scratch(block_norm_backward_workspace_size(m, n), dev, stream)
+        workspace = _scratch(block_norm_backward_workspace_size(m, n), x_out.device, stream)
     _room(workspace, torch.uint8, "workspace", 0)      # the library checks its size
     _check(_lib.block_norm_backward(_ptr(dh), lddh, _ptr(dx_out), lddr, _ptr(x_out), xt, ldr, _ptr(y), ldy, _ptr(w_post),
                                     _ptr(gate), ldg, _ptr(w_pre), residual_scale, eps, weight_offset, _ptr(dx), n,
@@ -760,27 +777,30 @@ def sample_tokens(logits, uniform, temperature=None, top_k=None, top_p=None, min
     Returns (tokens int32 [rows], logprobs fp32 [rows]): -1 where a row holds nothing but -inf and NaN;
     the log-probability is the one among the tokens the filters kept."""
     _check_device(logits, "logits")
-    if logits.dtype not in _STREAM_TYPES:
+    lt = _STREAM_TYPES.get(logits.dtype)
+    if lt is None:
         raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
     if logits.dim() != 2:
         raise ValueError("logits must have 2 dimensions")
     rows, vocab = logits.shape
-    ld = _rows(logits, logits.dtype, "logits", rows, vocab)
-    for t_, dtype, name in ((uniform, torch.float32, "uniform"), (temperature, torch.float32, "temperature"),
-                            (top_k, torch.int32, "top_k"), (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p")):
-        if t_ is not None:
-            _need(t_, dtype, name, 1)
-            if t_.numel() != rows or not t_.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous vector of {rows}")
+    dev = logits.get_device()
+    ld = _rows(logits, logits.dtype, "logits", rows, vocab, dev)
     if uniform is None:
         raise TypeError("uniform is needed")
+    _vector(uniform, torch.float32, "uniform", rows, dev)
+    _vector(temperature, torch.float32, "temperature", rows, dev)
+    _vector(top_k, torch.int32, "top_k", rows, dev)
+    _vector(top_p, torch.float32, "top_p", rows, dev)
+    _vector(min_p, torch.float32, "min_p", rows, dev)
     if tokens is None:
-        tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        tokens = logits.new_empty(rows, dtype=torch.int32)
+    else:
+        _vector(tokens, torch.int32, "tokens", rows, dev)
     if logprobs is None:
-        logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _room(tokens, torch.int32, "tokens", rows)
-    _room(logprobs, torch.float32, "logprobs", rows)
-    _check(_lib.sample_tokens(_ptr(logits), _STREAM_TYPES[logits.dtype], ld, _ptr(uniform), _ptr(temperature), _ptr(top_k),
+        logprobs = logits.new_empty(rows, dtype=torch.float32)
+    else:
+        _vector(logprobs, torch.float32, "logprobs", rows, dev)
+    _check(_lib.sample_tokens(_ptr(logits), lt, ld, _ptr(uniform), _ptr(temperature), _ptr(top_k),
                               _ptr(top_p), _ptr(min_p), _ptr(tokens), _ptr(logprobs), rows, vocab, flags, _stream(stream)))
     return tokens, logprobs
 

@@ -13,18 +13,29 @@
 // atomics.  (A weight below 2^-31 of the largest is zero; 2^21 tokens of weight 2^30 stay below 2^53,
 // so the products with p and u are taken in fp64 without losing a unit.)
 //
-// No sort.  A cluster of 1 to 8 CTAs owns a row; each of its warps owns a contiguous piece:
-//   1. the row's maximum;
-//   2. (top-k, top-p) counts and weights of 1024 classes of -x, each 1/32 wide, in shared memory; the
-//      first CTA adds the others' and finds the class in which the k-th token, then p times the
-//      total, is reached;
-//   3. (top-k, top-p) that class's keys (the bits of -x, which order as -x does) go to a list in the first
-//      CTA, which sorts it and reads off the cut: the last kept key and how many tokens that share
-//      it are kept.  A class with more than kList tokens is first split again, by 256, down to a
-//      single key if it must be (a row of equal logits needs no list at all);
-//   4. the kept weight and the ties of every piece; then the piece that the random number falls in
-//      is walked once more to the token.
-// Without top-k and top-p only 1 and 4 run.  The row is read from memory once and then from L2.
+// No sort of the row.  A cluster of 1 to 8 CTAs owns a row; each of its warps owns a contiguous piece:
+//   1. the row's maximum (and each thread's own);
+//   2. (top-k, top-p) a bracket of -x that the cut must fall in:
+//      top-k  the threads' maxima are tokens, so the k-th largest of them bounds the k-th token
+//             from below: everything from there up is the bracket;
+//      top-p  a histogram of every eighth vector estimates where the mass reaches p; the bracket is
+//             4.5 standard deviations either way;
+//   3. one pass that adds up the weight above the bracket (top-p; with top-k nothing is above) and
+//      keeps the logits inside it in a list per thread;
+//   4. the cut: the last kept key (the bits of -x, which order as -x does) and how many tokens that share
+//      it are kept.  The bracket is split by 256 until at most kFew keys are left; the first CTA compares
+//      those with one another;
+//   5. the kept weight and the ties of every piece, from the weight above and the lists; then the piece
+//      that the random number falls in is split over its CTA's warps, and one of them walks its
+//      part to the token.
+// Where the bracket is missed or a list overflows (equal logits, k or p near the end of a flat row) the
+// cut is found from the row itself: counts and weights of 1024 classes of -x, then splits of the class
+// down to a single key if need be (a row of equal logits), with a pass over the row each, and one more
+// pass for 5.  Both ways give the same cut.  Without top-k and top-p only 1 and 5 run, from the row.
+//
+// The row is read from memory once, then from L2.  What bounds it: a large batch is bound by
+// instruction issue (the top-p pass takes 2^x of every token), a small one by the latency of its passes and
+// cluster barriers.
 #include <cuda_bf16.h>
 
 #include "host.h"
@@ -38,7 +49,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;       // CTAs per row: the portable cluster size
 constexpr int kClasses = 1024;    // classes of -x in [0, 32)
 constexpr int kSplit = 256;       // parts of a class that is split again
-constexpr int kList = 4096;       // keys sorted at once
+constexpr int kFew = 256;         // keys compared with one another
+constexpr int kListBytes = 128;   // a thread's list of the bracket's logits: 64 of bf16, 32 of fp32
+constexpr int kSampled = 8;       // the top-p bracket is estimated from every eighth group of vectors
 constexpr int64_t kMaxVocab = 1 << 21;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kNoCut = 0xFFFFFFFFu;
@@ -54,6 +67,12 @@ struct SampleArgs {
   float *logprobs;
 };
 
+// Weight that top-p's tokens must reach: those before a kept token weigh less than top_p * total.
+__device__ __forceinline__ uint64_t mass_target(float top_p, uint64_t total) {
+  const double want = ceil(static_cast<double>(top_p) * static_cast<double>(total));
+  return want < 1.0 ? 1 : static_cast<uint64_t>(want);
+}
+
 // Where a sum reaches a target: class (or part) `bin`, with what the ones before it hold.
 struct Found {
   uint32_t ok, bin, n, key, r;
@@ -61,14 +80,19 @@ struct Found {
 };
 
 struct Smem {
+  uint32_t kept[kListBytes / 4 * kThreads];
   uint64_t mass[kClasses];
   uint64_t part_mass[2][kSplit];
   uint32_t count[kClasses];
   uint32_t part_count[2][kSplit];
-  uint32_t list[kList];
-  uint32_t list_n[2];
+  uint32_t part_lo[kSplit], part_hi[kSplit];
+  uint2 few[kFew];  // key, weight
+  uint32_t few_n[2];
   uint32_t base;
   Found found;
+  // the bracket's edges in classes, and what the cluster found of it
+  uint32_t edge_lo, edge_hi, bracket_n, overflow;
+  uint64_t bracket_mass, above, total;
   float cta_max[kMaxCtas];
   uint64_t cta_mass[kMaxCtas];
   uint32_t cta_ties[kMaxCtas];
@@ -83,30 +107,54 @@ struct Smem {
 template <typename T>
 struct Row {
   static constexpr int EV = 16 / sizeof(T);
+  static constexpr int kList = kListBytes / sizeof(T);
   const T *p;
   int off, v, vecs;
   __device__ __forceinline__ Row(const T *row, int n) : p(row), v(n) {
     off = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     vecs = (off + n + EV - 1) / EV;
   }
-  __device__ __forceinline__ void load(int vec, float (&f)[EV]) const {
+  // Vector `vec` as it lies in memory; places outside the row hold -inf.
+  __device__ __forceinline__ uint4 load(int vec) const {
     const int i0 = vec * EV - off;
-    if (i0 >= 0 && i0 + EV <= v) {
-      const uint4 q = *reinterpret_cast<const uint4 *>(p + i0);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if (i0 >= 0 && i0 + EV <= v) return *reinterpret_cast<const uint4 *>(p + i0);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 2) {
-          f[2 * i] = __uint_as_float(w[i] << 16);
-          f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        } else {
-          f[i] = __uint_as_float(w[i]);
-        }
+    for (int i = 0; i < EV; ++i) {
+      const bool in = i0 + i >= 0 && i0 + i < v;
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t h = in ? __bfloat16_as_ushort(p[i0 + i]) : 0xFF80u;
+        w[i / 2] |= h << (16 * (i & 1));
+      } else {
+        w[i] = in ? __float_as_uint(p[i0 + i]) : 0xFF800000u;
       }
-    } else {
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ void unpack(const uint4 &q, float (&f)[EV]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < EV; ++i)
-        f[i] = i0 + i >= 0 && i0 + i < v ? static_cast<float>(p[i0 + i]) : __uint_as_float(0xFF800000u);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        f[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+  // Largest value of a vector (NaN passed over).
+  static __device__ __forceinline__ float max_of(const uint4 &q) {
+    if constexpr (sizeof(T) == 2) {
+      auto max2 = [](uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+      };
+      const uint32_t m = max2(max2(q.x, q.y), max2(q.z, q.w));
+      return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    } else {
+      return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
     }
   }
 };
@@ -114,12 +162,9 @@ struct Row {
 // What turns a logit into its place in the order.
 struct Scale {
   float m, c;
-  bool only_max;  // only the logits equal to m have weight (m or c is infinite, or the row is greedy)
-  // -x; tokens that weigh nothing (NaN included) come out at 32 or more, or as NaN
-  __device__ __forceinline__ float neg_x(float z) const {
-    if (only_max) return z == m ? 0.0f : 64.0f;
-    return __fsub_rn(0.0f, __fmul_rn(__fsub_rn(z, m), c));
-  }
+  // -x = (m - z) c, which is the exact negative of (z - m) c and never -0.  A token whose -x is 32 or
+  // more, or NaN, weighs nothing (exp2_neg and weight_of give 0 for those too).
+  __device__ __forceinline__ float neg_x(float z) const { return __fmul_rn(__fsub_rn(m, z), c); }
 };
 __device__ __forceinline__ float exp2_neg(float nx) {
   float e;
@@ -128,18 +173,18 @@ __device__ __forceinline__ float exp2_neg(float nx) {
 }
 __device__ __forceinline__ uint32_t weight_of(float e) { return __float2uint_rn(e * 1073741824.0f); }
 
-// f(values of one vector) over the vectors [b, e) of a warp's piece, U vectors a lane in flight.
-template <typename T, typename F>
+// f(vector) over the vectors b + lane, b + lane + 32 * STEP, ... of [b, e), U of them in flight.
+template <int STEP, typename T, typename F>
 __device__ __forceinline__ void walk(const Row<T> &row, int b, int e, int lane, F &&f) {
   constexpr int U = 4;
-  for (int s = b + lane; s < e; s += 32 * U) {
-    float z[U][Row<T>::EV];
+  for (int s = b + lane; s < e; s += 32 * STEP * U) {
+    uint4 q[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (s + 32 * u < e) row.load(s + 32 * u, z[u]);
+      if (s + 32 * STEP * u < e) q[u] = row.load(s + 32 * STEP * u);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (s + 32 * u < e) f(z[u]);
+      if (s + 32 * STEP * u < e) f(q[u]);
   }
 }
 
@@ -195,46 +240,40 @@ __device__ void find_bin(Smem &s, const uint32_t *count, const uint64_t *mass, i
     }
 }
 
-// Sorts the first CTA's list of n keys and finds the key at which the count (or mass) reaches
-// `target`, how many of the tokens that share it are kept, and the mass up to there.
-__device__ void find_key(Smem &s, int n, bool by_mass, uint64_t target) {
-  int n2 = 32;
-  while (n2 < n) n2 <<= 1;
-  for (int i = n + threadIdx.x; i < n2; i += kThreads) s.list[i] = 0xFFFFFFFFu;
+// The cut among the first CTA's n <= kFew keys, each compared with all others (fewer instructions than
+// sorting them, and no barriers): the key at which the count reaches `k` (0: no such target), then
+// the one at which the mass reaches `target`, or with top_p < 1 that share of the mass up to the first cut.
+// Run by every thread of the first CTA.
+__device__ void find_key(Smem &s, int n, uint64_t k, uint64_t target, float top_p) {
+  uint32_t key = 0, w = 0, eq = 0;
+  uint64_t less = s.found.count, mass = s.found.mass;
+  const bool in = static_cast<int>(threadIdx.x) < n;
+  if (in) {
+    key = s.few[threadIdx.x].x;
+    w = weight_of(exp2_neg(__uint_as_float(key)));
+    s.few[threadIdx.x].y = w;
+  }
   __syncthreads();
-  for (int k = 2; k <= n2; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < n2 / 2; i += kThreads) {
-        const int a = 2 * i - (i & (j - 1)), b = a + j;
-        const uint32_t x = s.list[a], y = s.list[b];
-        if ((x > y) == ((a & k) == 0)) s.list[a] = y, s.list[b] = x;
-      }
-      __syncthreads();
+  if (in)
+    for (int j = 0; j < n; ++j) {
+      const uint2 o = s.few[j];
+      if (o.x < key) ++less, mass += o.y;
+      eq += o.x == key;
     }
-  const int per = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * per;
-  auto weight = [&](int i) { return static_cast<uint64_t>(weight_of(exp2_neg(__uint_as_float(s.list[i])))); };
-  uint64_t c = 0, m = 0;
-  for (int i = i0; i < i0 + per && i < n; ++i) ++c, m += weight(i);
-  const uint64_t c0 = s.found.count, m0 = s.found.mass;
-  block_prefix(s.scan, c, m);
-  c += c0;
-  m += m0;
-  for (int i = i0; i < i0 + per && i < n; ++i) {
-    const uint64_t w = weight(i), before = by_mass ? m : c;
-    if (before < target && target <= before + (by_mass ? w : 1)) {
-      const uint32_t key = s.list[i];
-      int lo = 0, hi = i;  // first place of the key
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s.list[mid] < key) lo = mid + 1;
-        else hi = mid;
-      }
+  if (k > 0) {
+    if (in && less < k && k <= less + eq) {  // (tokens that share the key write the same)
       s.found.key = key;
-      s.found.r = i - lo + 1;
-      s.found.mass = m + w;
+      s.found.r = static_cast<uint32_t>(k - less);
+      s.found.mass = mass + (k - less) * w;
     }
-    ++c;
-    m += w;
+    __syncthreads();
+    if (top_p >= 1.0f) return;
+    target = mass_target(top_p, s.found.mass);
+    __syncthreads();
+  }
+  if (in && mass < target && target <= mass + static_cast<uint64_t>(eq) * w) {
+    s.found.key = key;
+    s.found.r = static_cast<uint32_t>((target - mass + w - 1) / w);
   }
 }
 
@@ -243,9 +282,66 @@ struct Cut {
   uint32_t key, r;
 };
 
+// The bracket of a top-p cut from the classes' counts of a sample, run by every thread of the first CTA:
+// classes below edge_lo lie above the cut, classes from edge_hi on below it, to 4.5 standard deviations.
+// The sampled share of the mass above a cut at share p has variance
+//   ((1 - p)^2 sum of w^2 above + p^2 sum of w^2 below) / (sum of w)^2
+// times the share not sampled: a few heavy tokens above the cut hardly blur it.
+// `most`: keys that the lists should have to hold at most.
+__device__ void sample_bracket(Smem &s, float top_p, float unsampled, float scale, float most) {
+  constexpr int PER = kClasses / kThreads;
+  const int b0 = threadIdx.x * PER;
+  uint64_t c = 0, m = 0, sq = 0, zero = 0;
+  auto weight = [&](int b) { return static_cast<uint64_t>(weight_of(exp2_neg((b + 0.5f) / 32.0f))); };
+  auto square = [&](int b) { return (weight(b) >> 15) * (weight(b) >> 15); };  // in units of 2^30
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c += s.count[b0 + i];
+    m += s.count[b0 + i] * weight(b0 + i);
+    sq += s.count[b0 + i] * square(b0 + i);
+  }
+  const uint64_t own_m = m, own_sq = sq;
+  block_prefix(s.scan, c, m);
+  block_prefix(s.scan, sq, zero);
+  __syncthreads();
+  if (threadIdx.x == kThreads - 1) s.total = m + own_m, s.above = sq + own_sq;
+  if (threadIdx.x == 0) s.edge_lo = 0, s.edge_hi = kClasses, s.bracket_n = 0, s.bracket_mass = 0;
+  __syncthreads();
+  const float total = static_cast<float>(s.total), all_sq = static_cast<float>(s.above);
+  // the first class of this thread's that ends past `x`: f(class, tokens before it, squares up to its end)
+  auto crossing = [&](float x, auto &&f) {
+    uint64_t ci = c, mi = m, si = sq;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float before = static_cast<float>(mi);
+      mi += s.count[b0 + i] * weight(b0 + i);
+      si += s.count[b0 + i] * square(b0 + i);
+      if (before <= x && static_cast<float>(mi) > x) f(b0 + i, ci, si);
+      ci += s.count[b0 + i];
+    }
+  };
+  crossing(top_p * total, [&](int, uint64_t, uint64_t si) { s.bracket_mass = si; });
+  __syncthreads();
+  const float up = static_cast<float>(s.bracket_mass), q = 1.0f - top_p;
+  const float var = (q * q * up + top_p * top_p * fmaxf(all_sq - up, 0.0f)) * 1073741824.0f / (total * total);
+  const float width = 4.5f * sqrtf(fmaxf(var * unsampled, 0.0f)) + 0.0005f * fminf(q, top_p);
+  crossing((top_p - width) * total, [&](int b, uint64_t ci, uint64_t) { s.edge_lo = b, s.bracket_n = static_cast<uint32_t>(ci); });
+  __syncthreads();
+  const int lo = static_cast<int>(s.edge_lo);
+  const float to = (top_p + width) * total, n0 = static_cast<float>(s.bracket_n);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {  // the last class it needs, or the last that fits
+    m += s.count[b0 + i] * weight(b0 + i);
+    c += s.count[b0 + i];
+    if (b0 + i >= lo && (static_cast<float>(m) >= to || (static_cast<float>(c) - n0) * scale >= most))
+      atomicMin(&s.edge_hi, static_cast<uint32_t>(b0 + i + 1));
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p) {
-  __shared__ Smem s;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Smem &s = *reinterpret_cast<Smem *>(smem_raw);
   if (p.ctas > 1) cluster_arrive_relaxed();
   pdl_trigger();
   pdl_wait();
@@ -254,10 +350,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Row<T> row(static_cast<const T *>(p.logits) + r * p.ld, p.v);
   constexpr int EV = Row<T>::EV;
+  const float inf = __uint_as_float(0x7F800000u);
   // this warp's vectors: pieces of equal length, in order over the cluster's warps
-  const int piece = rank * kWarps + warp, pieces = ctas * kWarps;
-  const int vb = static_cast<int>(static_cast<int64_t>(piece) * row.vecs / pieces);
-  const int ve = static_cast<int>(static_cast<int64_t>(piece + 1) * row.vecs / pieces);
+  const int pieces = ctas * kWarps;
+  auto piece_at = [&](int i) { return static_cast<int>(static_cast<int64_t>(i) * row.vecs / pieces); };
+  const int vb = piece_at(rank * kWarps + warp), ve = piece_at(rank * kWarps + warp + 1);
 
   const float t = p.temperature ? p.temperature[r] : 1.0f;
   const bool greedy = !(t > 0.0f);
@@ -266,21 +363,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   const float min_p = p.min_p && !greedy ? p.min_p[r] : 0.0f;
   const bool use_k = k > 0 && k < p.v, use_p = top_p < 1.0f;
 
-  // 1. maximum (fmaxf passes over NaN)
-  float mx = __uint_as_float(0xFF800000u);
-  walk(row, vb, ve, lane, [&](const float(&z)[EV]) {
-#pragma unroll
-    for (int i = 0; i < EV; ++i) mx = fmaxf(mx, z[i]);
-  });
+  // 1. maximum
+  float mx = -inf;
+  walk<1>(row, vb, ve, lane, [&](const uint4 &q) { mx = fmaxf(mx, Row<T>::max_of(q)); });
+  const float own_max = mx;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
   if (lane == 0) s.warp_max[warp] = mx;
-  if (use_k || use_p) {
+  auto clear_classes = [&]() {
     for (int i = threadIdx.x; i < kClasses; i += kThreads) s.count[i] = 0, s.mass[i] = 0;
+  };
+  if (use_k || use_p) {
+    clear_classes();
     for (int i = threadIdx.x; i < 2 * kSplit; i += kThreads) (&s.part_count[0][0])[i] = 0, (&s.part_mass[0][0])[i] = 0;
   }
+  if (threadIdx.x < kSplit) s.part_lo[threadIdx.x] = s.part_hi[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
-    s.list_n[0] = s.list_n[1] = 0;
+    s.few_n[0] = s.few_n[1] = 0;
     s.found.count = s.found.mass = 0;
   }
   __syncthreads();
@@ -295,170 +394,354 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     mx = s.cta_max[0];
     for (int i = 1; i < ctas; ++i) mx = fmaxf(mx, s.cta_max[i]);
   }
-  if (mx == __uint_as_float(0xFF800000u)) {  // nothing but -inf and NaN (the same on every CTA of the row)
+  if (mx == -inf) {  // nothing but -inf and NaN (the same on every CTA of the row)
     if (rank == 0 && threadIdx.x == 0) {
       p.tokens[r] = -1;
       if (p.logprobs) p.logprobs[r] = mx;
     }
     return;
   }
-  const float c = greedy ? 1.0f : __fdiv_rn(kLog2e, t);
-  const float inf = __uint_as_float(0x7F800000u);
-  const Scale sc{mx, c, greedy || mx == inf || c == inf};
-  Cut cut{kNoCut, 0};
-
-  // 2. and 3. the cut of top-k and top-p
-  if (use_k || use_p) {
-    walk(row, vb, ve, lane, [&](const float(&z)[EV]) {
+  // Only the logits equal to the largest have weight where that or the factor is infinite, or the row is
+  // greedy: they become 0 and the others -inf.
+  const float c0 = greedy ? 1.0f : __fdiv_rn(kLog2e, t);
+  const bool only_max = greedy || mx == inf || c0 == inf;
+  const Scale sc{only_max ? 0.0f : mx, only_max ? 1.0f : c0};
+  auto unpack = [&](const uint4 &q, float(&z)[EV]) {
+    Row<T>::unpack(q, z);
+    if (only_max)
 #pragma unroll
-      for (int i = 0; i < EV; ++i) {
-        const float nx = sc.neg_x(z[i]);
-        if (nx < 32.0f) {
-          const int b = static_cast<int>(nx * 32.0f);
-          atomicAdd(&s.count[b], 1u);
-          if (use_p) atomicAdd(reinterpret_cast<unsigned long long *>(&s.mass[b]),
-                               static_cast<unsigned long long>(weight_of(exp2_neg(nx))));
+      for (int i = 0; i < EV; ++i) z[i] = z[i] == mx ? 0.0f : -inf;
+  };
+  Cut cut{kNoCut, 0};
+  // What this thread saw above the bracket, and how many keys it keeps of the bracket itself.
+  uint64_t above = 0;
+  int mine = 0;
+  bool listed = false;
+  T *const list = reinterpret_cast<T *>(s.kept) + threadIdx.x;  // entry i at i * kThreads
+
+  if (use_k || use_p) {
+    auto to_first = [&](const void *q) { return map_to_rank(smem_u32(q), 0); };
+    // Adds this CTA's bins to the first CTA's.
+    auto add_to_first = [&](uint32_t *count, uint64_t *mass, int n) {
+      if (rank != 0)
+        for (int i = threadIdx.x; i < n; i += kThreads)
+          if (count[i]) {
+            red_add_cluster_u32(to_first(&count[i]), count[i]);
+            if (mass) red_add_cluster_u64(to_first(&mass[i]), mass[i]);
+          }
+    };
+    auto class_edge = [](uint32_t b) { return static_cast<float>(b) / 32.0f; };
+    // Reads a field of the first CTA's shared memory.
+    auto first_u32 = [&](const uint32_t &f) { return ctas > 1 ? ld_cluster_u32(to_first(&f)) : f; };
+    auto first_u64 = [&](const uint64_t &f) { return ctas > 1 ? ld_cluster_u64(to_first(&f)) : f; };
+
+    // 2. the bracket
+    if (use_k) {
+      const float nx = sc.neg_x(only_max ? (own_max == mx ? 0.0f : -inf) : own_max);
+      if (nx < 32.0f) atomicAdd(&s.count[static_cast<int>(nx * 32.0f)], 1u);
+    } else {
+      walk<kSampled>(row, vb, ve, lane, [&](const uint4 &q) {
+        float z[EV];
+        unpack(q, z);
+#pragma unroll
+        for (int i = 0; i < EV; ++i) {
+          const float nx = sc.neg_x(z[i]);
+          if (nx < 32.0f) atomicAdd(&s.count[static_cast<int>(nx * 32.0f)], 1u);
         }
-      }
-    });
+      });
+    }
     __syncthreads();
-    if (rank != 0)
-      for (int i = threadIdx.x; i < kClasses; i += kThreads)
-        if (s.count[i]) {
-          red_add_cluster_u32(map_to_rank(smem_u32(&s.count[i]), 0), s.count[i]);
-          if (use_p) red_add_cluster_u64(map_to_rank(smem_u32(&s.mass[i]), 0), s.mass[i]);
-        }
+    add_to_first(s.count, nullptr, kClasses);
     row_sync(ctas);
-    int level = 0;  // splits made so far: they alternate between two sets of bins
-    const uint32_t found0 = map_to_rank(smem_u32(&s.found), 0);
-    auto found_u32 = [&](size_t off) { return ld_cluster_u32(found0 + static_cast<uint32_t>(off)); };
-    auto found_u64 = [&](size_t off) { return ld_cluster_u64(found0 + static_cast<uint32_t>(off)); };
-    // Keeps the shortest beginning of the order whose count (or mass) reaches target; returns its mass.
-    // Every branch goes by what the first CTA found, so all CTAs of the row take it alike.
-    auto keep = [&](bool by_mass, uint64_t target, int which) -> uint64_t {
-      if (rank == 0) {
-        if (threadIdx.x == 0) s.found.count = s.found.mass = 0;
+    if (rank == 0) {
+      if (use_k) {
+        find_bin(s, s.count, s.mass, kClasses, false, static_cast<uint64_t>(k));
         __syncthreads();
-        find_bin(s, s.count, s.mass, kClasses, by_mass, target);
+        if (threadIdx.x == 0) s.edge_lo = 0, s.edge_hi = s.found.ok ? s.found.bin + 1 : 0;
+      } else {
+        sample_bracket(s, top_p, 1.0f - 1.0f / kSampled, kSampled, 0.5f * Row<T>::kList * kThreads * ctas);
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        s.bracket_n = s.overflow = 0;
+        s.bracket_mass = s.above = s.total = 0;
+      }
+    }
+    row_sync(ctas);
+    const uint32_t edge_lo = first_u32(s.edge_lo), edge_hi = first_u32(s.edge_hi);
+    uint32_t n = 0;        // keys in the bracket
+    uint64_t total = 0;    // top-p without top-k: the row's mass
+    if (edge_hi > edge_lo) {
+      // 3. what is above the bracket, and the keys inside it
+      const float lo = class_edge(edge_lo), hi = class_edge(edge_hi);
+      uint64_t all = 0;
+      // `mine` past the list's end says that it overflowed
+      T *at = list;
+      auto room = [&]() {
+        if (mine > Row<T>::kList - EV) at = list, mine = Row<T>::kList + 1;
+      };
+      if (use_k) {
+        // a vector whose largest logit lies below the bracket is skipped; the bound allows for the
+        // roundings of -x
+        const float reach = hi / sc.c;
+        float floor = mx - reach - (fabsf(mx) + reach) * 9.5367431640625e-7f;
+        if (only_max || !(floor > -inf)) floor = -inf;
+        walk<1>(row, vb, ve, lane, [&](const uint4 &q) {
+          if (!(Row<T>::max_of(q) >= floor)) return;
+          room();
+          float z[EV];
+          unpack(q, z);
+#pragma unroll
+          for (int i = 0; i < EV; ++i)
+            if (sc.neg_x(z[i]) < hi) {
+              *at = static_cast<T>(z[i]);
+              at += kThreads;
+              ++mine;
+            }
+        });
+      } else {
+        const uint32_t lo_key = __float_as_uint(lo), span = __float_as_uint(hi) - lo_key;
+        walk<1>(row, vb, ve, lane, [&](const uint4 &q) {
+          room();
+          float z[EV];
+          unpack(q, z);
+#pragma unroll
+          for (int i = 0; i < EV; ++i) {
+            const float nx = sc.neg_x(z[i]);
+            const uint32_t w = weight_of(exp2_neg(nx));
+            all += w;
+            if (nx < lo) above += w;
+            if (__float_as_uint(nx) - lo_key < span) {
+              *at = static_cast<T>(z[i]);
+              at += kThreads;
+              ++mine;
+            }
+          }
+        });
+      }
+      uint32_t cnt = static_cast<uint32_t>(mine), over = mine > Row<T>::kList ? 1u : 0u;
+      uint64_t ab = above, in_mass = 0;
+      if (over) mine = 0;
+      else if (!use_k)
+        for (int i = 0; i < mine; ++i) in_mass += weight_of(exp2_neg(sc.neg_x(static_cast<float>(list[i * kThreads]))));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        cnt += __shfl_xor_sync(0xFFFFFFFFu, cnt, o);
+        over |= __shfl_xor_sync(0xFFFFFFFFu, over, o);
+        ab += __shfl_xor_sync(0xFFFFFFFFu, ab, o);
+        in_mass += __shfl_xor_sync(0xFFFFFFFFu, in_mass, o);
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+      }
+      if (lane == 0) {
+        red_add_cluster_u32(to_first(&s.bracket_n), cnt);
+        if (over) red_add_cluster_u32(to_first(&s.overflow), 1u);
+        if (use_p) {
+          red_add_cluster_u64(to_first(&s.above), ab);
+          red_add_cluster_u64(to_first(&s.bracket_mass), in_mass);
+          red_add_cluster_u64(to_first(&s.total), all);
+        }
       }
       row_sync(ctas);
-      if (!found_u32(offsetof(Found, ok))) return 0;  // fewer tokens have weight: nothing to cut
-      const uint32_t bin = found_u32(offsetof(Found, bin));
-      uint32_t lo = __float_as_uint(static_cast<float>(bin) / 32.0f), hi = __float_as_uint(static_cast<float>(bin + 1) / 32.0f);
-      uint32_t n = found_u32(offsetof(Found, n));
-      while (n > kList && hi - lo > 1) {
-        const int buf = level++ & 1;
-        int shift = 0;
-        while (((hi - lo - 1) >> shift) >= kSplit) ++shift;
-        walk(row, vb, ve, lane, [&](const float(&z)[EV]) {
+      n = first_u32(s.bracket_n);
+      listed = first_u32(s.overflow) == 0;
+      if (!use_k) {
+        total = first_u64(s.total);
+        const uint64_t upto = first_u64(s.above);
+        const uint64_t target = mass_target(top_p, total);
+        // (and min-p must not reach above the bracket, whose mass is not looked at token by token)
+        listed = listed && upto < target && target <= upto + first_u64(s.bracket_mass) &&
+                 (edge_lo == 0 || exp2_neg(lo) >= min_p);
+      }
+    }
+
+    // The keys of the bracket, or of the row.
+    auto each_key = [&](uint32_t lo, uint32_t hi, auto &&f) {
+      if (listed) {
+        for (int i = 0; i < mine; ++i) {
+          const uint32_t key = __float_as_uint(sc.neg_x(static_cast<float>(list[i * kThreads])));
+          if (key >= lo && key < hi) f(key);
+        }
+      } else {
+        walk<1>(row, vb, ve, lane, [&](const uint4 &q) {
+          float z[EV];
+          unpack(q, z);
 #pragma unroll
           for (int i = 0; i < EV; ++i) {
             const float nx = sc.neg_x(z[i]);
             const uint32_t key = __float_as_uint(nx);
-            if (nx < 32.0f && key >= lo && key < hi) {
-              atomicAdd(&s.part_count[buf][(key - lo) >> shift], 1u);
-              atomicAdd(reinterpret_cast<unsigned long long *>(&s.part_mass[buf][(key - lo) >> shift]),
-                        static_cast<unsigned long long>(weight_of(exp2_neg(nx))));
-            }
+            if (nx < 32.0f && key >= lo && key < hi) f(key);
+          }
+        });
+      }
+    };
+    auto add_key = [&](uint32_t *count, uint64_t *mass, uint32_t key) {
+      atomicAdd(count, 1u);
+      atomicAdd(reinterpret_cast<unsigned long long *>(mass),
+                static_cast<unsigned long long>(weight_of(exp2_neg(__uint_as_float(key)))));
+    };
+    if (!listed) {  // counts and masses of the classes of the whole row
+      row_sync(ctas);  // (the first CTA's bins have been read)
+      clear_classes();
+      row_sync(ctas);
+      each_key(0u, kNoCut, [&](uint32_t key) {
+        const int b = static_cast<int>(__uint_as_float(key) * 32.0f);
+        add_key(&s.count[b], &s.mass[b], key);
+      });
+      __syncthreads();
+      add_to_first(s.count, s.mass, kClasses);
+      row_sync(ctas);
+    }
+
+    // 4. Keeps the shortest beginning of the order whose count (or mass) reaches target, with then_p also
+    // top-p of what that keeps; returns the mass of the first.  Every branch goes by what the first CTA
+    // holds, so all CTAs of the row take it alike.
+    int level = 0;  // splits made so far: they alternate between two sets of bins
+    auto keep = [&](bool by_mass, uint64_t target, int which, bool then_p) -> uint64_t {
+      uint32_t lo, hi, left = n;
+      if (listed) {
+        lo = __float_as_uint(class_edge(edge_lo));
+        hi = __float_as_uint(class_edge(edge_hi));
+        if (rank == 0) {
+          if (threadIdx.x == 0) s.found.count = 0, s.found.mass = s.above;
+          __syncthreads();
+        }
+      } else {
+        if (rank == 0) {
+          if (threadIdx.x == 0) s.found.count = s.found.mass = 0;
+          __syncthreads();
+          find_bin(s, s.count, s.mass, kClasses, by_mass, target);
+        }
+        row_sync(ctas);
+        if (!first_u32(s.found.ok)) return 0;  // fewer tokens have weight: nothing to cut
+        const uint32_t bin = first_u32(s.found.bin);
+        lo = __float_as_uint(class_edge(bin));
+        hi = __float_as_uint(class_edge(bin + 1));
+        left = first_u32(s.found.n);
+      }
+      while (left > kFew && hi - lo > 1) {
+        const int buf = level++ & 1;
+        int shift = 0;
+        while (((hi - lo - 1) >> shift) >= kSplit) ++shift;
+        each_key(lo, hi, [&](uint32_t key) {
+          const uint32_t b = (key - lo) >> shift;
+          if (listed) {
+            // (a CTA's lists hold at most 2^15 keys: neither half of the weights' sum can overflow)
+            const uint32_t w = weight_of(exp2_neg(__uint_as_float(key)));
+            atomicAdd(&s.part_count[buf][b], 1u);
+            atomicAdd(&s.part_lo[b], w & 0xFFFFu);
+            atomicAdd(&s.part_hi[b], w >> 16);
+          } else {
+            add_key(&s.part_count[buf][b], &s.part_mass[buf][b], key);
           }
         });
         __syncthreads();
         for (int i = threadIdx.x; i < kSplit; i += kThreads) {
-          if (rank != 0 && s.part_count[buf][i]) {
-            red_add_cluster_u32(map_to_rank(smem_u32(&s.part_count[buf][i]), 0), s.part_count[buf][i]);
-            red_add_cluster_u64(map_to_rank(smem_u32(&s.part_mass[buf][i]), 0), s.part_mass[buf][i]);
+          if (listed && s.part_count[buf][i]) {
+            // (added, not stored: in the first CTA other CTAs' masses arrive at the same time)
+            red_add_cluster_u64(map_to_rank(smem_u32(&s.part_mass[buf][i]), rank),
+                                (static_cast<uint64_t>(s.part_hi[i]) << 16) + s.part_lo[i]);
+            s.part_lo[i] = s.part_hi[i] = 0;
           }
-          s.part_count[buf ^ 1][i] = 0;  // (nobody adds to it before the next barrier)
-          s.part_mass[buf ^ 1][i] = 0;
+          // (nobody adds to the other set before the next barrier)
+          s.part_count[buf ^ 1][i] = 0, s.part_mass[buf ^ 1][i] = 0;
         }
+        __syncthreads();
+        add_to_first(s.part_count[buf], s.part_mass[buf], kSplit);
         row_sync(ctas);
         if (rank == 0) find_bin(s, s.part_count[buf], s.part_mass[buf], kSplit, by_mass, target);
         row_sync(ctas);
-        lo += found_u32(offsetof(Found, bin)) << shift;
+        lo += first_u32(s.found.bin) << shift;
         hi = min(hi, lo + (1u << shift));
-        n = found_u32(offsetof(Found, n));
+        left = first_u32(s.found.n);
       }
       Cut got;
       uint64_t mass;
       if (hi - lo == 1) {
-        const uint64_t w = weight_of(exp2_neg(__uint_as_float(lo))), m0 = found_u64(offsetof(Found, mass));
-        const uint64_t before = by_mass ? m0 : found_u64(offsetof(Found, count)), each = by_mass ? w : 1;
+        const uint64_t w = weight_of(exp2_neg(__uint_as_float(lo))), m0 = first_u64(s.found.mass);
+        const uint64_t before = by_mass ? m0 : first_u64(s.found.count), each = by_mass ? w : 1;
         got = Cut{lo, static_cast<uint32_t>((target - before + each - 1) / each)};
         mass = m0 + got.r * w;
-        row_sync(ctas);  // everyone has read found
       } else {
-        walk(row, vb, ve, lane, [&](const float(&z)[EV]) {
-#pragma unroll
-          for (int i = 0; i < EV; ++i) {
-            const float nx = sc.neg_x(z[i]);
-            const uint32_t key = __float_as_uint(nx);
-            if (nx < 32.0f && key >= lo && key < hi) s.list[atomicAdd(&s.list_n[which], 1u)] = key;
-          }
-        });
+        each_key(lo, hi, [&](uint32_t key) { s.few[atomicAdd(&s.few_n[which], 1u)].x = key; });
         __syncthreads();
         if (rank != 0) {
-          const uint32_t mine = s.list_n[which];
-          if (threadIdx.x == 0 && mine) s.base = atom_add_cluster_u32(map_to_rank(smem_u32(&s.list_n[which]), 0), mine);
+          const uint32_t have = s.few_n[which];
+          if (threadIdx.x == 0 && have) s.base = atom_add_cluster_u32(to_first(&s.few_n[which]), have);
           __syncthreads();
-          for (uint32_t i = threadIdx.x; i < mine; i += kThreads)
-            st_cluster_u32(map_to_rank(smem_u32(&s.list[s.base + i]), 0), s.list[i]);
+          for (uint32_t i = threadIdx.x; i < have; i += kThreads) st_cluster_u32(to_first(&s.few[s.base + i].x), s.few[i].x);
         }
         row_sync(ctas);
-        if (rank == 0) find_key(s, static_cast<int>(n), by_mass, target);
+        if (rank == 0) find_key(s, static_cast<int>(left), by_mass ? 0 : target, target, then_p ? top_p : 1.0f);
         row_sync(ctas);
-        got = Cut{found_u32(offsetof(Found, key)), found_u32(offsetof(Found, r))};
-        mass = found_u64(offsetof(Found, mass));
-        row_sync(ctas);  // everyone has read found
+        got = Cut{first_u32(s.found.key), first_u32(s.found.r)};
+        mass = first_u64(s.found.mass);
       }
+      row_sync(ctas);  // everyone has read found
       if (got.key < cut.key || (got.key == cut.key && got.r < cut.r)) cut = got;
       return mass;
     };
-    uint64_t total = 0;
-    if (use_k) total = keep(false, static_cast<uint64_t>(k), 0);
-    if (use_p) {
-      if (total == 0) {  // no top-k, or fewer than k tokens have weight: the whole row's mass
+    // (few keys in the bracket of top-k: both cuts are among them)
+    const bool both = use_k && use_p && listed && n <= kFew;
+    if (use_k) total = keep(false, static_cast<uint64_t>(k), 0, both);
+    if (use_p && !both) {
+      if (total == 0) {  // no top-k and no bracket, or fewer than k tokens have weight: the whole row's mass
         if (rank == 0) {
           uint64_t a = 0, b = 0;
           for (int i = threadIdx.x; i < kClasses; i += kThreads) a += s.mass[i];
           const uint64_t own = a;
           block_prefix(s.scan, a, b);
-          if (threadIdx.x == kThreads - 1) s.found.mass = a + own;
+          if (threadIdx.x == kThreads - 1) s.total = a + own;
         }
         row_sync(ctas);
-        total = found_u64(offsetof(Found, mass));
+        total = first_u64(s.total);
         row_sync(ctas);
       }
-      const double want = ceil(static_cast<double>(top_p) * static_cast<double>(total));
-      keep(true, want < 1.0 ? 1 : static_cast<uint64_t>(want), 1);
+      keep(true, mass_target(top_p, total), 1, false);
     }
   }
   // the first of the order stays whatever the filters say
   if (greedy || min_p > 1.0f || min_p != min_p) cut = Cut{0, 1};
 
-  // 4. kept weight and ties of every piece
+  // 5. kept weight and ties, of a key and of a stretch of the row
   uint64_t mass = 0;
   uint32_t ties = 0;
-  walk(row, vb, ve, lane, [&](const float(&z)[EV]) {
-#pragma unroll
-    for (int i = 0; i < EV; ++i) {
-      const float nx = sc.neg_x(z[i]);
-      const uint32_t key = __float_as_uint(nx);
-      if (nx < 32.0f && key <= cut.key) {
-        const float e = exp2_neg(nx);
-        if (e >= min_p) {
-          if (key == cut.key) ++ties;
-          else mass += weight_of(e);
-        }
+  auto add = [&](uint32_t key) {
+    if (key <= cut.key) {
+      const float e = exp2_neg(__uint_as_float(key));
+      if (e >= min_p) {
+        if (key == cut.key) ++ties;
+        else mass += weight_of(e);
       }
     }
-  });
+  };
+  auto add_row = [&](int b, int e) {
+    walk<1>(row, b, e, lane, [&](const uint4 &q) {
+      float z[EV];
+      unpack(q, z);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mass += __shfl_xor_sync(0xFFFFFFFFu, mass, o);
-    ties += __shfl_xor_sync(0xFFFFFFFFu, ties, o);
+      for (int i = 0; i < EV; ++i) {
+        const float nx = sc.neg_x(z[i]);
+        if (nx < 32.0f) add(__float_as_uint(nx));
+      }
+    });
+  };
+  auto to_warps = [&]() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mass += __shfl_xor_sync(0xFFFFFFFFu, mass, o);
+      ties += __shfl_xor_sync(0xFFFFFFFFu, ties, o);
+    }
+    if (lane == 0) s.warp_mass[warp] = mass, s.warp_ties[warp] = ties;
+    __syncthreads();
+  };
+  if (listed) {
+    // (all that is above the bracket is kept: neither the cut nor min-p reaches there)
+    for (int i = 0; i < mine; ++i) add(__float_as_uint(sc.neg_x(static_cast<float>(list[i * kThreads]))));
+    mass += above;
+  } else {
+    add_row(vb, ve);
   }
-  if (lane == 0) s.warp_mass[warp] = mass, s.warp_ties[warp] = ties;
-  __syncthreads();
+  to_warps();
   uint64_t cta_mass = 0;
   uint32_t cta_ties = 0;
 #pragma unroll
@@ -469,11 +752,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
       st_cluster_u32(map_to_rank(smem_u32(&s.cta_ties[rank]), threadIdx.x), cta_ties);
     }
     cluster_sync();  // (the last access to another CTA's shared memory: a CTA may leave after it)
-  } else if (threadIdx.x == 0) {
-    s.cta_mass[0] = cta_mass;
-    s.cta_ties[0] = cta_ties;
+  } else {
+    if (threadIdx.x == 0) s.cta_mass[0] = cta_mass, s.cta_ties[0] = cta_ties;
+    __syncthreads();
   }
-  if (ctas == 1) __syncthreads();
   const uint64_t wc = cut.key == kNoCut ? 0 : weight_of(exp2_neg(__uint_as_float(cut.key)));
   uint64_t total = 0;
   uint32_t all_ties = 0;
@@ -482,39 +764,38 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   const double want = static_cast<double>(p.uniform[r]) * static_cast<double>(total);
   uint64_t target = want > 0.0 ? static_cast<uint64_t>(want) : 0;
   if (target >= total) target = total - 1;
-  // the piece that holds it: ties are kept by index until r of them are
-  uint32_t left = cut.r;  // ties still to keep
+  // Which of n consecutive stretches holds the target (-1: none); `before` and `left`, the mass before the
+  // stretch and the ties still to keep from it on, go by index: ties are kept until r of them are.
   uint64_t before = 0;
-  bool mine = false;
-  for (int i = 0; i <= rank; ++i) {
-    const uint32_t kept = min(left, s.cta_ties[i]);
-    const uint64_t held = s.cta_mass[i] + wc * kept;
-    if (i == rank) {
-      mine = target >= before && target < before + held;
-    } else {
+  uint32_t left = cut.r;
+  auto find = [&](const uint64_t *m, const uint32_t *ti, int n) {
+    for (int i = 0; i < n; ++i) {
+      const uint32_t kept = min(left, ti[i]);
+      const uint64_t held = m[i] + wc * kept;
+      if (target < before + held) return i;
       before += held;
       left -= kept;
     }
-  }
-  if (!mine) return;
-  for (int w = 0; w <= warp; ++w) {
-    const uint32_t kept = min(left, s.warp_ties[w]);
-    const uint64_t held = s.warp_mass[w] + wc * kept;
-    if (w == warp) {
-      mine = target >= before && target < before + held;
-    } else {
-      before += held;
-      left -= kept;
-    }
-  }
-  if (!mine) return;
-  // (one warp of the row is left) walk its piece to the token
-  for (int v0 = vb; v0 < ve; v0 += 32) {
+    return -1;
+  };
+  if (find(s.cta_mass, s.cta_ties, ctas) != rank) return;
+  const int w0 = find(s.warp_mass, s.warp_ties, kWarps);
+  __syncthreads();  // (everyone has read the warps' sums)
+  // the CTA's warps share the piece, then the one whose part holds the target walks it to the token
+  const int pb = piece_at(rank * kWarps + w0), pe = piece_at(rank * kWarps + w0 + 1);
+  auto part_at = [&](int i) { return pb + static_cast<int>(static_cast<int64_t>(i) * (pe - pb) / kWarps); };
+  mass = 0;
+  ties = 0;
+  add_row(part_at(warp), part_at(warp + 1));
+  to_warps();
+  if (find(s.warp_mass, s.warp_ties, kWarps) != warp) return;
+  const int qe = part_at(warp + 1);
+  for (int v0 = part_at(warp); v0 < qe; v0 += 32) {
     float z[EV];
     uint32_t wt[EV];
     uint32_t n_ties = 0;
-    const bool in = v0 + lane < ve;
-    if (in) row.load(v0 + lane, z);
+    const bool in = v0 + lane < qe;
+    if (in) unpack(row.load(v0 + lane), z);
     uint32_t tie_mask = 0;
 #pragma unroll
     for (int i = 0; i < EV; ++i) {
@@ -609,6 +890,8 @@ extern "C" nvfp4_status_t sample_tokens(const void *logits, int logits_type, int
   while (ctas < kMaxCtas && rows * ctas * 2 <= 2LL * dev.sm_count && vocab >= 2048LL * 2 * ctas) ctas *= 2;
   SampleArgs a{logits, ld, static_cast<int>(vocab), ctas, uniform, temperature, top_k, top_p, min_p, tokens, logprobs};
   auto kern = f32 ? sample_kernel<float> : sample_kernel<__nv_bfloat16>;
-  return check_launch(launch(kern, dim3(static_cast<unsigned>(rows * ctas)), dim3(kThreads), 0, (cudaStream_t)stream,
+  st = allow_smem(reinterpret_cast<const void *>(kern), sizeof(Smem), dev.device);
+  if (st != NVFP4_OK) return st;
+  return check_launch(launch(kern, dim3(static_cast<unsigned>(rows * ctas)), dim3(kThreads), sizeof(Smem), (cudaStream_t)stream,
                              (flags & NVFP4_FLAG_PDL) != 0, ctas, a), name);
 }
