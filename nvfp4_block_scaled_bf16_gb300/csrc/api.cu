@@ -267,10 +267,10 @@ extern "C" nvfp4_status_t nvfp4_check_status(nvfp4_stream_t stream) {
       return fail(NVFP4_ERR_INVALID_ARG, "a MoE step found an expert id or row index out of range and skipped it (status 0x%x)", word);
     if (word & 4u)
       return fail(NVFP4_ERR_CUDA, "internal: a split tile had more partials than the fix-up buffer holds (status 0x%x)", word);
-    static const char *const kSites[7] = {"load/free-slot", "mma/accumulator", "mma/stage", "mma/scales",
-                                          "scales/slot", "scales/stage", "epilogue/accumulator"};
+    static const char *const kSites[8] = {"load/free-slot", "mma/accumulator", "mma/stage", "mma/scales",
+                                          "scales/slot", "scales/stage", "epilogue/accumulator", "norm/row"};
     char sites[160] = "";
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < 8; ++i)
       if (word & (1u << (8 + i))) {
         strncat(sites, sites[0] ? ", " : "", sizeof(sites) - strlen(sites) - 1);
         strncat(sites, kSites[i], sizeof(sites) - strlen(sites) - 1);

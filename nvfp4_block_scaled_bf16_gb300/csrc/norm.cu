@@ -17,10 +17,15 @@
 //   b    = scale * g * gate;  dw_post = sum over rows of b * yn
 //   e    = b * (offset + w_post);  dy = rstd_y * (e - yn * mean(e * yn))
 //
-// Every kernel reads each input once and keeps the row in registers between the two reductions:
-// they are bound by memory for many rows and by latency for few.  A team (a warp up to 512
-// channels, otherwise a block) owns a row; a thread holds 8 * VPT of its channels.
+// Every kernel reads each input once: they are bound by memory for many rows and by latency for few.
+// A team (a warp up to 512 channels, otherwise a block) owns a row; a thread holds 8 * VPT of its channels.
+//   - norm_kernel, norm_grad_kernel: the row's loads go straight to registers, one team per row;
+//   - norm_ring_kernel, norm_grad_ring_kernel, for many aligned rows of more than 512 channels: resident
+//     blocks walk the rows, which bulk copies bring ahead into a ring of shared memory, with one barrier a
+//     row; registers alone cannot hold enough loads in flight across a row's reductions.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "host.h"
 #include "ptx.cuh"
@@ -28,6 +33,7 @@
 namespace nvfp4 {
 namespace {
 
+constexpr int kSiteRing = 7;  // wait site recorded in the status word (after the GEMM's, gemm.cuh)
 constexpr int kMaxChannels = 32768;  // 1024 threads x 8 channels x 4
 constexpr int kWarpTeams = 8;        // rows per block where a warp owns a row
 
@@ -157,32 +163,42 @@ struct TeamSum {
   }
 };
 
-// NVFP4 of a row already rounded to bf16: a 16-channel block is the 8 channels of two neighbouring
+// NVFP4 of channels already rounded to bf16, eight from c on in each lane: a 16-channel block is the 8 channels of two neighbouring
 // threads, and eight threads gather the four scale bytes of a 32-bit word of the 128x4 layout.
 // Every lane of the warp takes part; channels past n (whole blocks) get zero scales.
+__device__ __forceinline__ void quantize8(const NormArgs &p, const float *f, float gs, int64_t row, int c) {
+  float amax = 0.0f, y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+  amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  uint32_t code = 0;
+  const float inv = nvfp4_block_scale(amax, gs, code);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(f[i], inv);
+  if (c < p.n) *reinterpret_cast<uint32_t *>(p.q + row * (p.n >> 1) + (c >> 1)) = e2m1x8(y);
+  else code = 0;
+  const uint32_t b1 = __shfl_down_sync(0xFFFFFFFFu, code, 2);
+  const uint32_t b2 = __shfl_down_sync(0xFFFFFFFFu, code, 4);
+  const uint32_t b3 = __shfl_down_sync(0xFFFFFFFFu, code, 6);
+  const int j = c >> 4;  // scale column
+  if ((threadIdx.x & 7) == 0 && j < p.cp)
+    *reinterpret_cast<uint32_t *>(p.sf + ((row >> 7) * (p.cp >> 2) + (j >> 2)) * 512 + (row & 31) * 16 +
+                                  ((row >> 5) & 3) * 4) = code | (b1 << 8) | (b2 << 16) | (b3 << 24);
+}
 template <int VPT>
 __device__ __forceinline__ void quantize_row(const NormArgs &p, const float (&f)[8 * VPT], int64_t row, int t, int ts) {
   const float gs = __ldg(p.gs);
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int c = (v * ts + t) * 8;
-    float amax = 0.0f, y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[8 * v + i]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    uint32_t code = 0;
-    const float inv = nvfp4_block_scale(amax, gs, code);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(f[8 * v + i], inv);
-    if (c < p.n) *reinterpret_cast<uint32_t *>(p.q + row * (p.n >> 1) + (c >> 1)) = e2m1x8(y);
-    else code = 0;
-    const uint32_t b1 = __shfl_down_sync(0xFFFFFFFFu, code, 2);
-    const uint32_t b2 = __shfl_down_sync(0xFFFFFFFFu, code, 4);
-    const uint32_t b3 = __shfl_down_sync(0xFFFFFFFFu, code, 6);
-    const int j = c >> 4;  // scale column
-    if ((t & 7) == 0 && j < p.cp)
-      *reinterpret_cast<uint32_t *>(p.sf + ((row >> 7) * (p.cp >> 2) + (j >> 2)) * 512 + (row & 31) * 16 +
-                                    ((row >> 5) & 3) * 4) = code | (b1 << 8) | (b2 << 16) | (b3 << 24);
+  for (int v = 0; v < VPT; ++v) quantize8(p, f + 8 * v, gs, row, (v * ts + t) * 8);
+}
+
+// Zeroes the scale rows between m and the next multiple of 128 (block `block` of `blocks`).
+__device__ __forceinline__ void zero_pad_rows(const NormArgs &p, unsigned int block, unsigned int blocks) {
+  const int64_t words = ((p.m + 127) / 128 * 128 - p.m) * (p.cp >> 2);
+  const int64_t stride = static_cast<int64_t>(blocks) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(block) * blockDim.x + threadIdx.x; i < words; i += stride) {
+    const int64_t row = p.m + i / (p.cp >> 2), jt = i % (p.cp >> 2);
+    *reinterpret_cast<uint32_t *>(p.sf + ((row >> 7) * (p.cp >> 2) + jt) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4) = 0u;
   }
 }
 
@@ -197,13 +213,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT)
   pdl_trigger();
   pdl_wait();
   if (QUANT && blockIdx.x >= row_blocks) {
-    const int64_t words = ((p.m + 127) / 128 * 128 - p.m) * (p.cp >> 2);
-    const int64_t stride = static_cast<int64_t>(gridDim.x - row_blocks) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x - row_blocks) * blockDim.x + threadIdx.x; i < words; i += stride) {
-      const int64_t row = p.m + i / (p.cp >> 2), jt = i % (p.cp >> 2);
-      *reinterpret_cast<uint32_t *>(p.sf + ((row >> 7) * (p.cp >> 2) + jt) * 512 + (row & 31) * 16 +
-                                    ((row >> 5) & 3) * 4) = 0u;
-    }
+    zero_pad_rows(p, blockIdx.x - row_blocks, gridDim.x - row_blocks);
     return;
   }
   const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpTeams + (threadIdx.x >> 5) : blockIdx.x;
@@ -256,6 +266,315 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT)
   } else {
     store_row<VPT, VEC>(p.h + row * p.ldh, r, t, ts, p.n);
   }
+}
+
+// Two fp32 values in a register pair: Blackwell's packed arithmetic rounds each half as the scalar
+// instruction would, at half the instructions.  The ring kernels are written in it: with scalar
+// arithmetic the 4096 x 7168 forward pass spent 36 instructions a channel and was bound by their issue.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void halves(F2 a, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float sum(F2 a) {
+  float lo, hi;
+  halves(a, lo, hi);
+  return lo + hi;
+}
+// Pair i of eight bf16 channels.
+__device__ __forceinline__ F2 pair(const uint4 &q, int i) {
+  const uint32_t w = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// Eight channels as four pairs, from and to memory.
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, F2 *f) {
+  const uint4 q = *reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pair(q, i);
+}
+__device__ __forceinline__ void load4(const float *p, F2 *f) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(p)[0], b = reinterpret_cast<const ulonglong2 *>(p)[1];
+  f[0].v = a.x, f[1].v = a.y, f[2].v = b.x, f[3].v = b.y;
+}
+__device__ __forceinline__ uint32_t pack(F2 a) {
+  float lo, hi;
+  halves(a, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const F2 *f) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(pack(f[0]), pack(f[1]), pack(f[2]), pack(f[3]));
+}
+__device__ __forceinline__ void store4(float *p, const F2 *f) {
+  reinterpret_cast<ulonglong2 *>(p)[0] = make_ulonglong2(f[0].v, f[1].v);
+  reinterpret_cast<ulonglong2 *>(p)[1] = make_ulonglong2(f[2].v, f[3].v);
+}
+
+// A row's operands as they land in one slot of the ring, each 16-byte aligned; 0 bytes: absent.
+struct Slot {
+  int bytes[5], offset[5], size;
+};
+template <int N>
+Slot slot_of(const int (&bytes)[N]) {
+  Slot s{};
+  for (int i = 0; i < N; ++i) {
+    s.bytes[i] = bytes[i];
+    s.offset[i] = s.size;
+    s.size += bytes[i];
+  }
+  return s;
+}
+struct RingArgs {
+  int slots;
+  Slot slot;
+  unsigned int *status;
+  long long wait_limit;
+};
+
+constexpr int kMaxSlots = 4;
+constexpr int kRingHead = 128;  // shared memory ahead of the slots: a barrier per slot, the abort flag
+
+// The ring of one block: its rows are first, first + step, ..., row i of them in slot i % slots.  An operand's
+// copy goes out from lane 0 of a warp of its own (a copy costs the thread that issues it about 100 cycles,
+// which the block's next barrier would wait for); a slot's barrier collects one arrival per operand.
+struct Ring {
+  uint64_t *full;
+  volatile int *abort;
+  uint8_t *data;
+  const RingArgs &a;
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ Ring(uint8_t *smem, const RingArgs &args)
+      : full(reinterpret_cast<uint64_t *>(smem)), abort(reinterpret_cast<volatile int *>(smem + 8 * kMaxSlots)),
+        data(smem + kRingHead), a(args) {
+    if (threadIdx.x == 0) {
+      int operands = 0;
+      for (int o = 0; o < 5; ++o) operands += a.slot.bytes[o] > 0;
+      for (int i = 0; i < a.slots; ++i) mbar_init(smem_u32(&full[i]), operands);
+      *abort = 0;
+      fence_barrier_init();
+    }
+    __syncthreads();
+  }
+  // src(operand): where the row begins
+  template <class Src>
+  __device__ __forceinline__ void fill(int to, Src &&src) const {
+    if ((threadIdx.x & 31) != 0) return;
+    for (int o = threadIdx.x >> 5; o < 5; o += blockDim.x >> 5) {
+      const int bytes = a.slot.bytes[o];
+      if (!bytes) continue;
+      mbar_arrive_expect_tx(smem_u32(&full[to]), bytes);
+      bulk_load(smem_u32(data + to * a.slot.size) + a.slot.offset[o], src(o), bytes, smem_u32(&full[to]));
+    }
+  }
+  // Waits for the slot; one that gives up sets the abort flag, which the block reads behind its next barrier.
+  __device__ __forceinline__ void wait(int i, uint32_t parity) const {
+    const WaitCtl wc{a.wait_limit, abort, a.status};
+    mbar_wait(smem_u32(&full[i]), parity, wc, kSiteRing);
+  }
+  template <typename T>
+  __device__ __forceinline__ const T *operand(int i, int o) const {
+    return reinterpret_cast<const T *>(data + i * a.slot.size + a.slot.offset[o]);
+  }
+  __device__ __forceinline__ int next_slot() const { return slot + 1 == a.slots ? 0 : slot + 1; }
+  __device__ __forceinline__ uint32_t next_phase() const { return slot + 1 == a.slots ? phase ^ 1 : phase; }
+  __device__ __forceinline__ void advance() {
+    phase = next_phase();
+    slot = next_slot();
+  }
+  // After a wait gave up: thread 0 waits, again with a limit, for the copies still in flight, so that
+  // none lands after the block is gone.
+  __device__ void drain() {
+    if (threadIdx.x != 0) return;
+    for (int n = 0; n < a.slots; ++n) {
+      const long long t0 = clock64();
+      while (!mbar_try_wait(smem_u32(&full[slot]), phase) && clock64() - t0 < a.wait_limit) {
+      }
+      advance();
+    }
+  }
+};
+
+// norm_kernel for many rows (see the head of this file).  The sums of r^2 of a row
+// and of y^2 of the row after it share a barrier.  A thread keeps its channels' factors in fp32:
+// scale * gate * (offset + w_post) of y and offset + w_pre.
+// Measured at 4096 x 7168, cold L2: 47.6 us for 235 MB, where 34.9 us is the measured copy rate and 37 us
+// what a kernel takes that only reads two such arrays and writes two.  Against it, the same ring with two
+// barriers a row and the copies issued by one computing thread took 54 us, a warp per row 74 us (too few
+// warps fit beside the rows), plain loads 59 us, one more warp for the copies 52 us.  What is left is
+// the latency of a row's chain (slot, sums, barrier, stores) that two blocks do not hide entirely: without
+// the stores of x_out it takes 43.5 us, with 2 slots instead of 3 49.7 us.
+template <typename XT, int VPT, bool QUANT, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_ring_kernel(const NormArgs p, const RingArgs ra) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_sum[2][2][32];  // [value][warp]; warps that are not there add zero
+  pdl_trigger();
+  pdl_wait();
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, ts = blockDim.x;
+  for (int i = t; i < 2 * 2 * 32; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
+  Ring ring(smem, ra);
+  const int64_t first = blockIdx.x, step = gridDim.x;
+  auto fill = [&](int to, int64_t row) {
+    ring.fill(to, [&](int o) -> const void * {
+      if (o == 0) return static_cast<const XT *>(p.x) + row * p.ldx;
+      return o == 1 ? p.y + row * p.ldy : p.gate + row * p.ldg;
+    });
+  };
+  for (int i = 0; i < ra.slots && first + i * step < p.m; ++i) fill(i, first + i * step);
+  const bool token_gate = p.gate && p.ldg != 0;
+  const F2 zero = f2(0.0f), offset = f2(p.offset);
+  constexpr int P = 4 * VPT;  // pairs a thread holds
+  F2 factor[P], pre[P];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = (v * ts + t) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) factor[4 * v + i] = f2(p.scale), pre[4 * v + i] = zero;
+    if (c >= p.n) continue;
+    F2 w[4];
+    if (p.w_post) {
+      load4(p.w_post + c, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) factor[4 * v + i] = factor[4 * v + i] * (offset + w[i]);
+    }
+    if (p.gate && !token_gate) {
+      load4(p.gate + c, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) factor[4 * v + i] = factor[4 * v + i] * w[i];
+    }
+    if (p.w_pre) {
+      load4(p.w_pre + c, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pre[4 * v + i] = offset + w[i];
+    }
+  }
+  const float inv_n = 1.0f / static_cast<float>(p.n), gs = QUANT ? __ldg(p.gs) : 0.0f;
+  const bool norm_y = p.y && p.w_post;
+  // sum of y^2 of the row in slot i
+  auto squares = [&](int i) {
+    F2 q = zero, y[4];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (v * ts + t) * 8;
+      if (c >= p.n) continue;
+      load4(ring.operand<__nv_bfloat16>(i, 1) + c, y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q = fma(y[k], y[k], q);
+    }
+    return sum(q);
+  };
+  int buf = 0;
+  // block sums of a and b, in a fixed order: the first shuffle leaves a to the lower half warp and b to the
+  // upper.  False: a wait gave up.
+  auto block_sums = [&](float &a, float &b) {
+    float s = lane < 16 ? a : b;
+    s += __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    s_sum[buf][lane >> 4][warp] = s;  // (by every lane of the half: under a test of lane & 15 the compiler takes
+                                      // lane >> 4 for lane / 16 without its remainder further down, too)
+    __syncthreads();
+    s = s_sum[buf][lane >> 4][lane & 15] + s_sum[buf][lane >> 4][(lane & 15) + 16];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    a = __shfl_sync(0xFFFFFFFFu, s, 0);
+    b = __shfl_sync(0xFFFFFFFFu, s, 16);
+    buf ^= 1;  // (written again only after the next sums' barrier)
+    return *ring.abort == 0;
+  };
+  float ry = 1.0f;
+  bool ok = true;
+  if (norm_y && first < p.m) {
+    ring.wait(0, 0);
+    float a = 0.0f, b = squares(0);
+    ok = block_sums(a, b);
+    ry = rsqrtf(b * inv_n + p.eps);
+  }
+  for (int64_t row = first; ok && row < p.m; row += step) {
+    ring.wait(ring.slot, ring.phase);
+    F2 r[P], q = zero;
+    const F2 f = f2(ry);
+    float yy = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (v * ts + t) * 8;
+      if (c >= p.n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[4 * v + i] = zero;
+        continue;
+      }
+      load4(ring.operand<XT>(ring.slot, 0) + c, r + 4 * v);
+      if (p.y) {
+        F2 y[4];
+        load4(ring.operand<__nv_bfloat16>(ring.slot, 1) + c, y);
+        if (token_gate) {
+          F2 g[4];
+          load4(ring.operand<__nv_bfloat16>(ring.slot, 2) + c, g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = y[i] * g[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[4 * v + i] = fma(y[i] * factor[4 * v + i], f, r[4 * v + i]);
+        store4(static_cast<XT *>(p.x_out) + row * p.ldxo + c, r + 4 * v);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q = fma(r[4 * v + i], r[4 * v + i], q);
+    }
+    float rr = sum(q);
+    if (norm_y && row + step < p.m) {
+      ring.wait(ring.next_slot(), ring.next_phase());
+      yy = squares(ring.next_slot());
+    }
+    ok = block_sums(rr, yy);
+    if (!ok) break;
+    // every thread has read this row's slot
+    if (row + ra.slots * step < p.m) fill(ring.slot, row + ra.slots * step);
+    ry = norm_y ? rsqrtf(yy * inv_n + p.eps) : 1.0f;
+    if (p.w_pre) {
+      const F2 rstd = f2(rsqrtf(rr * inv_n + p.eps));
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (v * ts + t) * 8;
+        F2 *h = r + 4 * v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = h[i] * rstd * pre[4 * v + i];
+        if constexpr (QUANT) {
+          float q8[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = pack(h[i]);  // rounded to bf16, then widened again
+            q8[2 * i] = __uint_as_float(w << 16);
+            q8[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+          }
+          quantize8(p, q8, gs, row, c);
+        } else if (c < p.n) {
+          store4(p.h + row * p.ldh + c, h);
+        }
+      }
+    }
+    ring.advance();
+  }
+  if (!ok) ring.drain();
+  if constexpr (QUANT) zero_pad_rows(p, blockIdx.x, gridDim.x);
 }
 
 // ------------------------------------------------------------------ backward
@@ -410,6 +729,216 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT)
   if (p.y && p.gate && p.ldg == 0) store_row<VPT, VEC>(part, ag, t, ts, p.n);
 }
 
+// norm_grad_kernel for many rows (see the head of this file).  A row needs one reduction only: dy's mean is
+// linear in the gradient of r, so with u = gate * (offset + w_post) the sums
+//   r^2, (dh w) r, y^2,  A = u y dr,  B = u y dh w,  C = u y r       (w = offset + w_pre)
+// give it as scale * rstd_y / n * (A + rstd_r B - rstd_r^2 mean C), mean = rstd_r sum((dh w) r) / n.
+// Warp shuffles that halve the values a lane carries, then the lanes, take 9 shuffles for all six.  A row
+// is read from its slot twice, before and after the block's barrier; the barrier of row i also says that
+// row i - 1 is done with, so its slot is filled again behind it.
+template <typename XT, int VPT, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_grad_ring_kernel(const NormGradArgs p, const RingArgs ra) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float s_sum[2][8][32];  // [value][warp]; warps that are not there add zero
+  pdl_trigger();
+  pdl_wait();
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, ts = blockDim.x;
+  for (int i = t; i < 2 * 8 * 32; i += ts) (&s_sum[0][0][0])[i] = 0.0f;
+  Ring ring(smem, ra);
+  const int64_t first = blockIdx.x, step = gridDim.x;
+  auto fill = [&](int to, int64_t row) {
+    ring.fill(to, [&](int o) -> const void * {
+      if (o == 0) return static_cast<const XT *>(p.r) + row * p.ldr;
+      if (o == 1) return p.dh + row * p.lddh;
+      if (o == 2) return static_cast<const XT *>(p.dr) + row * p.lddr;
+      return o == 3 ? p.y + row * p.ldy : p.gate + row * p.ldg;
+    });
+  };
+  for (int i = 0; i < ra.slots && first + i * step < p.m; ++i) fill(i, first + i * step);
+  const float inv_n = 1.0f / static_cast<float>(p.n);
+  uint4 w_pre[VPT], w_post[VPT], gate[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = (v * ts + t) * 8;
+    w_pre[v] = w_post[v] = gate[v] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < p.n) {
+      if (p.w_pre) w_pre[v] = *reinterpret_cast<const uint4 *>(p.w_pre + c);
+      if (p.w_post) w_post[v] = *reinterpret_cast<const uint4 *>(p.w_post + c);
+      if (p.gate && p.ldg == 0) gate[v] = *reinterpret_cast<const uint4 *>(p.gate + c);
+    }
+  }
+  const F2 offset = f2(p.offset), zero = f2(0.0f), one = f2(1.0f);
+  const bool token_gate = p.gate && p.ldg != 0;
+  constexpr int P = 4 * VPT;  // pairs a thread holds
+  F2 aw[P], ap[P], ag[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) aw[i] = ap[i] = ag[i] = zero;
+  int buf = 0;
+  bool gone = false;
+  for (int64_t row = first; row < p.m; row += step) {
+    ring.wait(ring.slot, ring.phase);
+    const XT *in_r = ring.operand<XT>(ring.slot, 0), *in_g = ring.operand<XT>(ring.slot, 2);
+    const __nv_bfloat16 *in_d = ring.operand<__nv_bfloat16>(ring.slot, 1), *in_y = ring.operand<__nv_bfloat16>(ring.slot, 3),
+                        *in_gate = ring.operand<__nv_bfloat16>(ring.slot, 4);
+    F2 q[6] = {zero, zero, zero, zero, zero, zero};
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (v * ts + t) * 8;
+      if (c >= p.n) continue;
+      F2 r[4], dw[4], u[4];
+      load4(in_r + c, r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dw[i] = zero;
+      if (p.dh) {
+        load4(in_d + c, dw);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dw[i] = dw[i] * (offset + pair(w_pre[v], i));
+          q[0] = fma(r[i], r[i], q[0]);
+          q[1] = fma(dw[i], r[i], q[1]);
+        }
+      }
+      if (p.w_post) {
+        load4(in_y + c, u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          q[2] = fma(u[i], u[i], q[2]);
+          u[i] = u[i] * (offset + pair(w_post[v], i));
+        }
+        if (p.gate) {
+          if (token_gate) gate[v] = *reinterpret_cast<const uint4 *>(in_gate + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[i] = u[i] * pair(gate[v], i);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          q[4] = fma(u[i], dw[i], q[4]);
+          q[5] = fma(u[i], r[i], q[5]);
+        }
+        if (p.dr) {
+          load4(in_g + c, r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[3] = fma(u[i], r[i], q[3]);
+        }
+      }
+    }
+    // six sums over the warp: each step halves the values a lane carries (then the lanes)
+    float s[8] = {sum(q[0]), sum(q[1]), sum(q[2]), sum(q[3]), sum(q[4]), sum(q[5]), 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 4, o = 16; k > 0; k >>= 1, o >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < k; ++i) {
+        const float keep = up ? s[i + k] : s[i], give = up ? s[i] : s[i + k];
+        s[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+      }
+    }
+    s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], 2);
+    s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], 1);
+    // lanes 4 i .. 4 i + 3 hold value ((i >> 2) & 1) * 4 + ((i >> 1) & 1) * 2 + (i & 1)  =  i
+    s_sum[buf][lane >> 2][warp] = s[0];  // (by all four: see norm_ring_kernel)
+    __syncthreads();
+    if (*ring.abort) {
+      gone = true;
+      break;
+    }
+    // every thread has done with the row before this one: its slot is free
+    if (row != first && row + (ra.slots - 1) * step < p.m)
+      fill(ring.slot == 0 ? ra.slots - 1 : ring.slot - 1, row + (ra.slots - 1) * step);
+    float tot;
+    {
+      const float4 a = *reinterpret_cast<const float4 *>(&s_sum[buf][lane >> 2][(lane & 3) * 8]);
+      const float4 b = *reinterpret_cast<const float4 *>(&s_sum[buf][lane >> 2][(lane & 3) * 8 + 4]);
+      tot = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+      tot += __shfl_xor_sync(0xFFFFFFFFu, tot, 2);
+      tot += __shfl_xor_sync(0xFFFFFFFFu, tot, 1);
+    }
+    buf ^= 1;  // (written again only after the next row's barrier)
+    float v6[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v6[i] = __shfl_sync(0xFFFFFFFFu, tot, 4 * i);
+    const float rx1 = rsqrtf(v6[0] * inv_n + p.eps), mean1 = v6[1] * rx1 * inv_n;
+    const float ry1 = p.w_post ? rsqrtf(v6[2] * inv_n + p.eps) : 1.0f;
+    // without w_post dy has no mean, without dh v6[4] and mean1 are zero
+    const float e1 = p.w_post ? p.scale * ry1 * inv_n * (v6[3] + rx1 * v6[4] - rx1 * rx1 * mean1 * v6[5]) : 0.0f;
+    const F2 rx = f2(rx1), neg_mean = f2(-mean1), ry = f2(ry1), neg_e = f2(-e1), scale = f2(p.scale);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (v * ts + t) * 8;
+      if (c >= p.n) continue;
+      F2 g[4], a[4], b[4];
+      if (p.dr) {
+        load4(in_g + c, g);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = zero;
+      }
+      if (p.dh) {
+        load4(in_r + c, a);
+        load4(in_d + c, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 xn = a[i] * rx;
+          aw[4 * v + i] = fma(b[i], xn, aw[4 * v + i]);
+          g[i] = fma(rx, fma(xn, neg_mean, b[i] * (offset + pair(w_pre[v], i))), g[i]);
+        }
+      }
+      store4(static_cast<XT *>(p.dx) + row * p.lddx + c, g);
+      if (!p.y) continue;
+      load4(in_y + c, a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = a[i] * ry;      // yn
+        g[i] = g[i] * scale;
+        b[i] = p.w_post ? offset + pair(w_post[v], i) : one;
+      }
+      if (p.gate) {
+        F2 d[4];
+        if (token_gate) gate[v] = *reinterpret_cast<const uint4 *>(in_gate + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d[i] = g[i] * a[i] * b[i];
+          g[i] = g[i] * pair(gate[v], i);
+        }
+        if (token_gate) {
+          store4(p.dgate + row * p.lddg + c, d);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ag[4 * v + i] = ag[4 * v + i] + d[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ap[4 * v + i] = fma(g[i], a[i], ap[4 * v + i]);
+        g[i] = ry * fma(a[i], neg_e, g[i] * b[i]);
+      }
+      store4(p.dy + row * p.lddy + c, g);
+    }
+    ring.advance();
+  }
+  if (gone) {
+    ring.drain();
+    return;
+  }
+  auto store_sums = [&](float *part, const F2 *f) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (v * ts + t) * 8;
+      if (c < p.n) store4(part + c, f + 4 * v);
+    }
+  };
+  float *part = p.part + static_cast<int64_t>(blockIdx.x) * p.planes * p.n;
+  if (p.dh) {
+    store_sums(part, aw);
+    part += p.n;
+  }
+  if (p.y && p.w_post) {
+    store_sums(part, ap);
+    part += p.n;
+  }
+  if (p.y && p.gate && p.ldg == 0) store_sums(part, ag);
+}
+
 // out[plane][c] = sum over teams of part[team][plane][c]: 32 columns a block, each of its 32 warps
 // sums every 32nd team, then the warps' sums are added in warp order.
 __global__ void __launch_bounds__(1024) norm_colsum_kernel(const float *__restrict__ part, int teams, int planes, int n,
@@ -484,6 +1013,42 @@ int grad_teams(int64_t m, const Shape &s, int sm_count) {
   return static_cast<int>(m < cap ? m : cap);
 }
 
+constexpr int kSmemBudget = 226 * 1024;  // dynamic shared memory of all blocks of an SM together
+
+// Ring launches: blocks of `threads` threads of `vpt` vectors each, per_sm of them an SM.  Taken from four
+// rows an SM on (fewer: the plain kernels start sooner), for 513 to 8192 channels.
+struct RingShape {
+  bool use;
+  int vpt, threads, per_sm, slots;
+};
+RingShape ring_slots(RingShape s, int slot) {
+  s.slots = (kSmemBudget / s.per_sm - kRingHead - 3072) / slot;
+  if (s.slots > kMaxSlots) s.slots = kMaxSlots;
+  s.use = s.slots >= 2;
+  return s;
+}
+// n_pad: channels the NVFP4 scale columns need.  One vector a thread up to 4096 channels (64 registers), two
+// above (half the warps share a row's fixed costs: 4096 x 7168 49.6 -> 47.6 us), two blocks an SM up to 7168.
+RingShape forward_ring_shape(int64_t m, int64_t n_pad, int slot, int sm_count) {
+  RingShape s{};
+  const int nv = static_cast<int>(ceil_div(n_pad, 8));
+  if (m < 4LL * sm_count || nv <= 64 || nv > 1024) return s;
+  s.vpt = nv > 512 ? 2 : 1;
+  s.threads = static_cast<int>(round_up(ceil_div(nv, s.vpt), 32));
+  s.per_sm = s.vpt == 2 ? (s.threads <= 448 ? 2 : 1) : s.threads <= 256 ? 4 : 2;
+  return ring_slots(s, slot);
+}
+// One vector a thread up to 4096 channels, two above; 128 registers a thread.
+RingShape backward_ring_shape(int64_t m, int64_t n, int slot, int sm_count) {
+  RingShape s{};
+  const int nv = static_cast<int>(ceil_div(n, 8));
+  if (m < 4LL * sm_count || nv <= 64 || nv > 1024) return s;
+  s.vpt = nv > 512 ? 2 : 1;
+  s.threads = static_cast<int>(round_up(ceil_div(nv, s.vpt), 32));
+  s.per_sm = s.threads <= 128 ? 4 : s.threads <= 256 ? 2 : 1;
+  return ring_slots(s, slot);
+}
+
 bool rows_aligned(const void *p, int64_t ld, int elem) { return !p || (aligned(p, 16) && ld * elem % 16 == 0); }
 // Row stride of an input: 0 (one row for all) or at least a row.
 bool in_stride(int64_t ld, int64_t n) { return ld == 0 || ld >= n; }
@@ -496,7 +1061,7 @@ nvfp4_status_t check_norm(const char *name, const void *x, int x_type, int64_t l
   if (m < 0 || n <= 0 || m >= (1LL << 31)) return fail(NVFP4_ERR_INVALID_ARG, "%s: m=%lld n=%lld", name, (long long)m, (long long)n);
   if (n > kMaxChannels) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: n=%lld (at most %d)", name, (long long)n, kMaxChannels);
   if (x_type != NVFP4_DTYPE_BF16 && x_type != NVFP4_DTYPE_F32) return fail(NVFP4_ERR_INVALID_ARG, "%s: x_type=%d", name, x_type);
-  if (flags & ~(uint32_t)NVFP4_FLAG_PDL) return fail(NVFP4_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name, flags);
+  if (flags & ~(uint32_t)(NVFP4_FLAG_PDL | NVFP4_FLAG_DEBUG_TIMEOUT)) return fail(NVFP4_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name, flags);
   if (m == 0) return NVFP4_OK;  // (an empty operand may come without an address)
   if (!y && (w_post || gate || x_out))
     return fail(NVFP4_ERR_INVALID_ARG, "%s: w_post, gate and x_out belong to y, which is NULL", name);
@@ -515,6 +1080,30 @@ nvfp4_status_t check_norm(const char *name, const void *x, int x_type, int64_t l
 }  // namespace nvfp4
 
 using namespace nvfp4;
+
+// Launches the forward pass as a ring where that pays; false: it does not.
+template <bool QUANT>
+static bool forward_ring(const NormArgs &a, bool f32, bool pdl, cudaStream_t stream, const DeviceInfo &dev, uint32_t flags,
+                         nvfp4_status_t *st, const char *name) {
+  const int n = a.n, xe = f32 ? 4 : 2;
+  const int bytes[3] = {n * xe, a.y ? n * 2 : 0, a.y && a.gate && a.ldg != 0 ? n * 2 : 0};
+  const Slot slot = slot_of(bytes);
+  const RingShape s = forward_ring_shape(a.m, QUANT ? a.cp * 16 : n, slot.size, dev.sm_count);
+  if (!s.use) return false;
+  const RingArgs ra{s.slots, slot, dev.status, wait_limit(flags)};
+  auto pick = [&](auto *x) {
+    using XT = std::remove_pointer_t<decltype(x)>;
+    if (s.vpt == 2) return s.threads <= 448 ? norm_ring_kernel<XT, 2, QUANT, 448, 2> : norm_ring_kernel<XT, 2, QUANT, 512, 1>;
+    return s.threads <= 256 ? norm_ring_kernel<XT, 1, QUANT, 256, 4> : norm_ring_kernel<XT, 1, QUANT, 512, 2>;
+  };
+  auto kern = f32 ? pick(static_cast<float *>(nullptr)) : pick(static_cast<__nv_bfloat16 *>(nullptr));
+  const int smem = kRingHead + s.slots * slot.size;
+  *st = allow_smem(reinterpret_cast<const void *>(kern), smem, dev.device);
+  if (*st != NVFP4_OK) return true;
+  const int64_t cap = static_cast<int64_t>(s.per_sm) * dev.sm_count;
+  *st = check_launch(launch(kern, dim3(static_cast<unsigned>(a.m < cap ? a.m : cap)), dim3(s.threads), smem, stream, pdl, 1, a, ra), name);
+  return true;
+}
 
 // One vector a thread while the rows are few (the call waits for one row's latency: 7168 channels,
 // one row), two from four rows an SM on (fewer, wider threads: more bytes in flight per warp).
@@ -544,6 +1133,7 @@ extern "C" nvfp4_status_t block_norm(const void *x, int x_type, int64_t ldx, con
              (const __nv_bfloat16 *)gate, ldg, residual_scale, eps, weight_offset, x_out, ldxo, (__nv_bfloat16 *)h, ldh,
              nullptr, nullptr, nullptr, m, static_cast<int>(n), 0};
   const bool f32 = x_type == NVFP4_DTYPE_F32;
+  if (vec && forward_ring<false>(a, f32, (flags & NVFP4_FLAG_PDL) != 0, (cudaStream_t)stream, dev, flags, &st, "block_norm")) return st;
   auto kern = f32 ? (vec ? forward_kernel<float, true, false>(s) : forward_kernel<float, false, false>(s))
                   : (vec ? forward_kernel<__nv_bfloat16, true, false>(s) : forward_kernel<__nv_bfloat16, false, false>(s));
   const unsigned int rows = static_cast<unsigned int>(s.warp ? ceil_div(m, kWarpTeams) : m);
@@ -576,6 +1166,9 @@ extern "C" nvfp4_status_t block_norm_quantize(const void *x, int x_type, int64_t
   NormArgs a{x, ldx, (const __nv_bfloat16 *)y, ldy, (const __nv_bfloat16 *)w_post, (const __nv_bfloat16 *)w_pre,
              (const __nv_bfloat16 *)gate, ldg, residual_scale, eps, weight_offset, x_out, ldxo, nullptr, 0,
              gs, q, sf, m, static_cast<int>(n), static_cast<int>(cp)};
+  if (forward_ring<true>(a, x_type == NVFP4_DTYPE_F32, (flags & NVFP4_FLAG_PDL) != 0, (cudaStream_t)stream, dev, flags, &st,
+                         name))
+    return st;
   auto kern = x_type == NVFP4_DTYPE_F32 ? forward_kernel<float, true, true>(s) : forward_kernel<__nv_bfloat16, true, true>(s);
   const unsigned int rows = static_cast<unsigned int>(s.warp ? ceil_div(m, kWarpTeams) : m);
   const int64_t words = (round_up(m, 128) - m) * (cp / 4);
@@ -587,8 +1180,14 @@ extern "C" nvfp4_status_t block_norm_quantize(const void *x, int x_type, int64_t
 
 extern "C" size_t block_norm_backward_workspace_size(int64_t m, int64_t n) {
   if (m < 0 || n <= 0 || n > kMaxChannels) return 0;
-  // (the largest number of teams on any GPU this library runs on; sized without a device)
-  return static_cast<size_t>(grad_teams(m, shape_of(n, 1), 160)) * 3 * static_cast<size_t>(n) * 4;
+  // (the most teams of either kernel on any GPU this library runs on; sized without a device)
+  const Shape s = shape_of(n, 1);
+  int64_t teams = grad_teams(m, s, 160);
+  if (!s.warp && teams < m) {
+    const int64_t ring = 160LL * 4;
+    teams = ring > teams ? (ring < m ? ring : m) : teams;
+  }
+  return static_cast<size_t>(teams) * 3 * static_cast<size_t>(n) * 4;
 }
 
 extern "C" nvfp4_status_t block_norm_backward(const void *dh, int64_t lddh, const void *dx_out, int64_t lddxo,
@@ -603,7 +1202,7 @@ extern "C" nvfp4_status_t block_norm_backward(const void *dh, int64_t lddh, cons
   if (m < 0 || n <= 0 || m >= (1LL << 31)) return fail(NVFP4_ERR_INVALID_ARG, "%s: m=%lld n=%lld", name, (long long)m, (long long)n);
   if (n > kMaxChannels) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: n=%lld (at most %d)", name, (long long)n, kMaxChannels);
   if (x_type != NVFP4_DTYPE_BF16 && x_type != NVFP4_DTYPE_F32) return fail(NVFP4_ERR_INVALID_ARG, "%s: x_type=%d", name, x_type);
-  if (flags & ~(uint32_t)NVFP4_FLAG_PDL) return fail(NVFP4_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name, flags);
+  if (flags & ~(uint32_t)(NVFP4_FLAG_PDL | NVFP4_FLAG_DEBUG_TIMEOUT)) return fail(NVFP4_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name, flags);
   if (m > 0 && !y && (w_post || gate || dy || dw_post || dgate))  // (an empty y may come without an address)
     return fail(NVFP4_ERR_INVALID_ARG, "%s: w_post, gate, dy, dw_post and dgate belong to y, which is NULL", name);
   if ((dh != nullptr) != (w_pre != nullptr) && m > 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: dh and w_pre: give both or neither", name);
@@ -636,7 +1235,13 @@ extern "C" nvfp4_status_t block_norm_backward(const void *dh, int64_t lddh, cons
                    rows_aligned(dy, lddy, 2) && (!token_gate || rows_aligned(dgate, lddg, 2)) && aligned(w_post, 16) &&
                    aligned(w_pre, 16);
   const Shape s = shape_of(n, 1);
-  const int teams = grad_teams(m, s, dev.sm_count < 160 ? dev.sm_count : 160);
+  const int sms = dev.sm_count < 160 ? dev.sm_count : 160;
+  const int bytes[5] = {static_cast<int>(n) * xe, dh ? static_cast<int>(n) * 2 : 0, dx_out ? static_cast<int>(n) * xe : 0,
+                        y ? static_cast<int>(n) * 2 : 0, token_gate ? static_cast<int>(n) * 2 : 0};
+  const Slot slot = slot_of(bytes);
+  const RingShape rs = vec ? backward_ring_shape(m, n, slot.size, sms) : RingShape{};
+  const int64_t ring_teams = static_cast<int64_t>(rs.per_sm) * sms;
+  const int teams = rs.use ? static_cast<int>(m < ring_teams ? m : ring_teams) : grad_teams(m, s, sms);
   NormGradArgs a{(const __nv_bfloat16 *)dh, lddh, dx_out, lddxo, x_out, ldxo, (const __nv_bfloat16 *)y, ldy,
                  (const __nv_bfloat16 *)w_post, (const __nv_bfloat16 *)w_pre, (const __nv_bfloat16 *)gate, ldg,
                  residual_scale, eps, weight_offset, dx, lddx, (__nv_bfloat16 *)dy, lddy,
@@ -644,7 +1249,20 @@ extern "C" nvfp4_status_t block_norm_backward(const void *dh, int64_t lddh, cons
                  static_cast<int>(n), planes, teams};
   const bool pdl = (flags & NVFP4_FLAG_PDL) != 0, f32 = x_type == NVFP4_DTYPE_F32;
   cudaError_t e = cudaSuccess;
-  if (m > 0) {
+  if (rs.use) {
+    const RingArgs ra{rs.slots, slot, dev.status, wait_limit(flags)};
+    auto pick = [&](auto *x) {
+      using XT = std::remove_pointer_t<decltype(x)>;
+      if (rs.vpt == 2) return norm_grad_ring_kernel<XT, 2, 512, 1>;
+      return rs.threads <= 128 ? norm_grad_ring_kernel<XT, 1, 128, 4>
+                               : (rs.threads <= 256 ? norm_grad_ring_kernel<XT, 1, 256, 2> : norm_grad_ring_kernel<XT, 1, 512, 1>);
+    };
+    auto kern = f32 ? pick(static_cast<float *>(nullptr)) : pick(static_cast<__nv_bfloat16 *>(nullptr));
+    const int smem = kRingHead + rs.slots * slot.size;
+    st = allow_smem(reinterpret_cast<const void *>(kern), smem, dev.device);
+    if (st != NVFP4_OK) return st;
+    e = launch(kern, dim3(static_cast<unsigned>(teams)), dim3(rs.threads), smem, (cudaStream_t)stream, pdl, 1, a, ra);
+  } else if (m > 0) {
     auto kern = f32 ? (vec ? backward_kernel<float, true>(s) : backward_kernel<float, false>(s))
                     : (vec ? backward_kernel<__nv_bfloat16, true>(s) : backward_kernel<__nv_bfloat16, false>(s));
     e = launch(kern, dim3(static_cast<unsigned>(s.warp ? ceil_div(teams, kWarpTeams) : teams)), dim3(s.threads), 0,

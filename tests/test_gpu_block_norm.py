@@ -70,7 +70,9 @@ def forward_terms(d, scale, offset):
 
 
 SHAPES = [(1, 1), (1, 7), (3, 8), (1, 16), (5, 255), (9, 256), (4, 257), (2, 512), (3, 520), (700, 96), (1, 2047),
-          (6, 2048), (77, 2047), (1, 7168), (700, 4096), (2, 8200), (2, 12296), (3, 20000), (2, 32768)]
+          (6, 2048), (77, 2047), (1, 7168), (700, 4096), (2, 8200), (2, 12296), (3, 20000), (2, 32768),
+          # from 4 rows an SM on, aligned rows are copied ahead
+          (608, 520), (700, 1032), (613, 2056), (1300, 4104), (620, 7168), (609, 8192), (640, 10248), (650, 7177)]
 
 
 @pytest.mark.parametrize("m,n", SHAPES)
@@ -86,7 +88,7 @@ def test_forward(nv, m, n):
 @pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("post,gate", [(True, "none"), (True, "channel"), (True, "token"), (False, "none"), (False, "channel"),
                                        (False, "token"), (None, "none")])
-@pytest.mark.parametrize("m,n,pad", [(6, 200, 0), (6, 200, 3), (5, 1032, 8), (3, 333, 1)])
+@pytest.mark.parametrize("m,n,pad", [(6, 200, 0), (6, 200, 3), (5, 1032, 8), (3, 333, 1), (620, 1032, 8)])
 def test_forward_forms(nv, stream, post, gate, m, n, pad):
     """Every combination of what may be absent, both stream types, rows of a wider buffer."""
     d = inputs(m, n, stream, post, gate, pad=pad)
@@ -111,6 +113,17 @@ def test_forward_in_place_and_without_the_second_norm(nv):
     assert out is x and torch.equal(x, want) and torch.equal(h, h2)
 
 
+def test_forward_in_place_with_rows_copied_ahead(nv):
+    d = inputs(1300, 2048, gate="token")
+    kw = dict(y=d["y"], w_post=d["w_post"], gate=d["gate"])
+    want, h = nv.block_norm(d["x"], d["w_pre"], **kw)
+    x = d["x"].clone()
+    out, h2 = nv.block_norm(x, d["w_pre"], x_out=x, **kw)
+    assert out is x and torch.equal(x, want) and torch.equal(h, h2)
+    none, h3 = nv.block_norm(want, d["w_pre"])
+    assert none is want and h3.shape == h.shape
+
+
 def test_zero_rows_and_special_values(nv):
     d = inputs(4, 64)
     for t in ("x", "y"):
@@ -125,7 +138,8 @@ def test_zero_rows_and_special_values(nv):
     assert x_out.shape == (0, 64) and h.shape == (0, 64)
 
 
-@pytest.mark.parametrize("m,n", [(1, 16), (1, 7168), (3, 48), (130, 1024), (128, 4096), (5, 496), (300, 528), (2, 20480)])
+@pytest.mark.parametrize("m,n", [(1, 16), (1, 7168), (3, 48), (130, 1024), (128, 4096), (5, 496), (300, 528), (2, 20480), (610, 528),
+                                 (650, 2080), (640, 4096)])
 @pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
 def test_quantized_output_equals_the_two_calls(nv, m, n, stream):
     d = inputs(m, n, stream, gate="token")
@@ -194,7 +208,7 @@ def test_backward(nv, m, n):
 @pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("post,gate", [(True, "none"), (True, "channel"), (True, "token"), (False, "none"), (False, "channel"),
                                        (False, "token"), (None, "none")])
-@pytest.mark.parametrize("m,n,pad", [(6, 200, 0), (700, 200, 3), (5, 1032, 8), (3, 333, 1)])
+@pytest.mark.parametrize("m,n,pad", [(6, 200, 0), (700, 200, 3), (5, 1032, 8), (3, 333, 1), (620, 1032, 8)])
 def test_backward_forms(nv, stream, post, gate, m, n, pad):
     d = inputs(m, n, stream, post, gate, pad=pad)
     check_backward(nv, d, 1.3, 1.0)
