@@ -254,9 +254,10 @@ __device__ __forceinline__ void gate_act(const GemmArgs &p, float g, float &f, f
 
 // The gated epilogue of 32 columns of one row (16 gate, then 16 up) held by one thread: column
 // 32 j of the product is column 16 j of h.
+// dv: the 16 dh of the chunk (kEpiGatedGrad).
 template <int EPI>
 __device__ __forceinline__ void gated_row_chunk(const GemmArgs &p, int64_t row, int64_t col, const float (&c)[32],
-                                                float a0, float a1) {
+                                                float a0, float a1, const uint32_t (&dv)[8]) {
   const int64_t hc = col >> 1;
   uint32_t hv[8];
   if constexpr (EPI == kEpiGated) {
@@ -272,8 +273,7 @@ __device__ __forceinline__ void gated_row_chunk(const GemmArgs &p, int64_t row, 
     }
     st_global_v8(p.d + row * p.ldd + hc, hv);
   } else {
-    uint32_t dv[8], gv[8], uv[8];
-    ld_global_nc_v8(p.dh + row * p.ldh + hc, dv);
+    uint32_t gv[8], uv[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float f[2], df[2], u[2];
@@ -290,6 +290,36 @@ __device__ __forceinline__ void gated_row_chunk(const GemmArgs &p, int64_t row, 
     st_global_v8(p.d + row * p.ldd + col, gv);
     st_global_v8(p.d + row * p.ldd + col + 16, uv);
     if (p.h) st_global_v8(p.h + row * p.ldh + hc, hv);
+  }
+}
+
+// Chunks [c0, c1) of one row of a whole tile (row: the thread's lane of the accumulator at t_base).  dh is
+// loaded a chunk ahead.
+template <class C, int EPI, class Tile>
+__device__ __forceinline__ void gated_chunks(const GemmArgs &p, const Tile &t, uint32_t t_base, int row, int c0, int c1,
+                                             float a0, float a1) {
+  const bool in = row < t.rows;
+  const __nv_bfloat16 *dh = p.dh + (t.out_i0 + row) * p.ldh + (t.out_j0 >> 1);
+  uint32_t next[8] = {};
+  if constexpr (EPI == kEpiGatedGrad) {
+    if (in && 32 * c0 < t.cols) ld_global_nc_v8(dh + 16 * c0, next);
+  }
+#pragma unroll 1
+  for (int c = c0; c < c1; ++c) {
+    uint32_t r[32], now[8];
+    tmem_ld_32x32b_x32(t_base + 32 * c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) now[i] = next[i];
+    if constexpr (EPI == kEpiGatedGrad) {
+      if (in && c + 1 < c1 && 32 * (c + 1) < t.cols) ld_global_nc_v8(dh + 16 * (c + 1), next);
+    }
+    if (in && 32 * c < t.cols) {
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+      gated_row_chunk<EPI>(p, t.out_i0 + row, t.out_j0 + 32 * c, v, a0, a1, now);
+    }
   }
 }
 
@@ -614,7 +644,10 @@ __device__ __forceinline__ void sk_fixup(const GemmArgs &p, const TileInfo &t, c
         }
       }
       if constexpr (EPI != kEpiPlain) {
-        gated_row_chunk<EPI>(p, t.out_i0 + row, t.out_j0 + 32 * c, acc, alpha, alpha1);
+        uint32_t dv[8] = {};
+        if constexpr (EPI == kEpiGatedGrad)
+          ld_global_nc_v8(p.dh + (t.out_i0 + row) * p.ldh + ((t.out_j0 + 32 * c) >> 1), dv);
+        gated_row_chunk<EPI>(p, t.out_i0 + row, t.out_j0 + 32 * c, acc, alpha, alpha1, dv);
         continue;
       }
       __nv_bfloat16 *out = p.d + (t.out_i0 + row) * p.ldd + t.out_j0 + 32 * c;
@@ -865,6 +898,10 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
   const bool push_red = C::PUSH_RED && p.splits > 1 && p.n >= 16;
   static_assert(!FUSED || (C::SWAP_ONLY && !GROUPED), "fused quantisation serves the swap-AB plans");
   static_assert(EPI == kEpiPlain || (!FUSED && !GROUPED), "the gated epilogues serve the dense plans");
+  // The scale writers take the upper half of every tile's columns: the gradient's arithmetic (an exponential, a
+  // reciprocal and about 25 more instructions an element, on one warp per scheduler) bounds the boundary
+  // between tiles.
+  constexpr bool HELP = EPI == kEpiGatedGrad && C::PAIR;
   const WaitCtl wc{p.wait_limit, abort_flag, p.status};
   // The next kernel may launch now: it waits (griddepcontrol.wait) for this grid to complete
   // before it reads our output, and its CTAs can meanwhile take the SM space we leave free.
@@ -877,7 +914,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&accf[a]), 1);
-      mbar_init(smem_u32(&acce[a]), C::ACC_ARRIVALS);
+      mbar_init(smem_u32(&acce[a]), HELP ? 2 * C::ACC_ARRIVALS : C::ACC_ARRIVALS);
     }
     for (int q = 0; q < C::SF_GROUPS; ++q) {
       mbar_init(smem_u32(&sff[q]), C::SLOT_ARRIVALS);
@@ -1239,6 +1276,9 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
       }
     } else {
       uint32_t sit = 0;  // ring stages (the scale ring of a pair is indexed by stage)
+      int acc = 0;         // HELP: the tile's accumulator
+      uint32_t acc_phase = 0;
+      if constexpr (HELP) pdl_wait();  // (alpha and dh are read here too)
       for (Seg sg; w.next(p, sg);) {
         for (int kt = sg.kt0; kt < sg.kt1; ++kt, ++sit) {
           // The stage's scales land with its operands, or (pair) in the scale ring ahead of them.
@@ -1302,6 +1342,20 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1;
+          }
+        }
+        if constexpr (HELP) {
+          if (!mbar_wait<C::PAIR>(smem_u32(&accf[acc]), acc_phase, wc, kSiteEpilogue)) goto scale_done;
+          tc_fence_after();
+          const TileInfo t = tile_info<C, GROUPED>(p, tb, sg.tile, crank);
+          gated_chunks<C, EPI>(p, t, tmem + lane_base + acc * C::BN, (warp & 3) * 32 + lane, C::BN / 64, C::BN / 32,
+                               __ldg(p.alpha), __ldg(p.alpha + 1));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&acce[acc]), 0));
+          if (++acc == C::NACC) {
+            acc = 0;
+            acc_phase ^= 1;
           }
         }
       }
@@ -1403,6 +1457,14 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
     for (Seg sg; w.next(p, sg);) {
       const TileInfo t = tile_info<C, GROUPED>(p, tb, sg.tile, crank);
       const bool sk_part = C::MULTI_TILE && !GROUPED && p.splits == 1 && sg.n > 1;
+      if constexpr (EPI == kEpiGatedGrad && !C::SWAP_ONLY) {
+        // dh of the tile comes to L2 while its MMAs run
+        if (row < t.rows) {
+          const __nv_bfloat16 *dh_row = p.dh + (t.out_i0 + row) * p.ldh + (t.out_j0 >> 1);
+          for (int c = 0; c < t.cols / 2; c += 64) prefetch_l2(dh_row + c);
+          prefetch_l2(dh_row + t.cols / 2 - 1);
+        }
+      }
       const bool ok = mbar_wait<C::PAIR>(smem_u32(&accf[acc]), acc_phase, wc, kSiteEpilogue);
       tc_fence_after();
       const uint32_t t_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * C::BN;
@@ -1411,8 +1473,15 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
       float *slot = sk_part ? sk_slot<C>(p, blockIdx.x, sg.j) : nullptr;
       // (a split swap-AB tile of 64 or more columns: the scale writers take the upper half)
       const int c_end = (!GROUPED && C::SWAP_ONLY && C::BN >= 64 && p.splits > 1) ? C::BN / 64 : C::BN / 32;
+      bool drained = false;
+      if constexpr (EPI != kEpiPlain && !C::SWAP_ONLY) {
+        if (!sk_part) {
+          if (ok) gated_chunks<C, EPI>(p, t, t_base, row, 0, HELP ? C::BN / 64 : C::BN / 32, tile_alpha, alpha1);
+          drained = true;
+        }
+      }
 #pragma unroll 1
-      for (int c = 0; ok && c < c_end; ++c) {
+      for (int c = 0; ok && !drained && c < c_end; ++c) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(t_base + 32 * c, r);
         tmem_ld_wait();
@@ -1431,14 +1500,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
             st_global_v8(dst + 8 * q, v);
           }
         } else if (!C::SWAP_ONLY) {
-          if constexpr (EPI != kEpiPlain) {
-            if (row < t.rows && 32 * c < t.cols) {
-              float v[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-              gated_row_chunk<EPI>(p, t.out_i0 + row, t.out_j0 + 32 * c, v, alpha, alpha1);
-            }
-          } else if (row < t.rows && 32 * c < t.cols) {
+          if (row < t.rows && 32 * c < t.cols) {
             __nv_bfloat16 *out = p.d + (t.out_i0 + row) * p.ldd + t.out_j0 + 32 * c;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1453,14 +1515,23 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
         } else if (row < t.rows) {
           // operand A is the weight: TMEM lane = output column, TMEM column = output row
           if constexpr (EPI != kEpiPlain) {
-            // lanes 0..15 hold gate rows, lanes 16..31 the up rows (valid rows come in whole warps)
+            // 32 weight rows (16 gate, 16 up) x 32 tokens: turned around through this warp's 4 KB of the
+            // idle ring, so that a lane holds a token's 32 columns and stores whole vectors (valid rows
+            // come in whole warps).  With single elements instead, two bytes a store, 128 x 14336 x 4096
+            // took 26.1 us, its backward pass 78.9.
+            float *turn = reinterpret_cast<float *>(smem) + quad * (32 * 33);
+            float v[32];
+            __syncwarp();  // (the chunk before has been read)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float o = __shfl_xor_sync(0xFFFFFFFFu, __uint_as_float(r[i]), 16);
-              if (32 * c + i < t.cols && lane < 16) {
-                const float g1[1] = {__uint_as_float(r[i])}, u1[1] = {o};
-                gated_col_units<EPI, 1>(p, t.out_j0 + 32 * c + i, t.out_i0 + row, g1, u1, alpha, alpha1);
-              }
+            for (int i = 0; i < 32; ++i) turn[i * 33 + lane] = __uint_as_float(r[i]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = turn[lane * 33 + i];
+            if (32 * c + lane < t.cols) {
+              const int64_t token = t.out_j0 + 32 * c + lane, wr = t.out_i0 + quad * 32;
+              uint32_t dv[8] = {};
+              if constexpr (EPI == kEpiGatedGrad) ld_global_nc_v8(p.dh + token * p.ldh + (wr >> 1), dv);
+              gated_row_chunk<EPI>(p, token, wr, v, alpha, alpha1, dv);
             }
             continue;
           }
