@@ -14,12 +14,13 @@
 // so the products with p and u are taken in fp64 without losing a unit.)
 //
 // No sort of the row.  A cluster of 1 to 8 CTAs owns a row; each of its warps owns a contiguous piece:
-//   1. the row's maximum (and each thread's own);
+//   1. the row's maximum (and the largest logits of each thread's two heaviest vectors);
 //   2. (top-k, top-p) a bracket of -x that the cut must fall in:
 //      top-k  the threads' maxima are tokens, so the k-th largest of them bounds the k-th token
 //             from below: everything from there up is the bracket;
-//      top-p  a histogram of every eighth vector estimates where the mass reaches p; the bracket is
-//             4.5 standard deviations either way;
+//      top-p  the threads' maxima, which hold the heavy tokens, and a histogram of every eighth vector
+//             of the rest estimate where the mass reaches p; the bracket is 4.5 standard deviations
+//             either way;
 //   3. one pass that adds up the weight above the bracket (top-p; with top-k nothing is above) and
 //      keeps the logits inside it in a list per thread;
 //   4. the cut: the last kept key (the bits of -x, which order as -x does) and how many tokens that share
@@ -33,9 +34,15 @@
 // down to a single key if need be (a row of equal logits), with a pass over the row each, and one more
 // pass for 5.  Both ways give the same cut.  Without top-k and top-p only 1 and 5 run, from the row.
 //
-// The row is read from memory once, then from L2.  What bounds it: a large batch is bound by
-// instruction issue (the top-p pass takes 2^x of every token), a small one by the latency of its passes and
-// cluster barriers.
+// The row is read from memory once, then from L2.  What bounds it, measured on device: 256 rows of 131072
+// bf16 with top-p take 72 us (floor 10 us, the logits read once), of them 6 the maximum, 8 the bracket, 18 to
+// 26 the pass (issue: about 15 instructions a token on the SMs that hold two rows), 10 the cut; 64 rows with
+// every filter 28 us (floor 2.5) and one row of 32000 fp32 7.6 us, which is latency: seven passes or
+// cluster barriers of one to three microseconds each.
+// Measured and not kept: classes and 64-bit masses of the whole row with shared-memory atomics, two of
+// them a token (328 and 83 us: a 64-bit one costs several 32-bit ones), which is now only the fallback;
+// a sample of every fourth vector with p (1 - p) for the variance, which overflowed lists (206 us); a
+// sorted list instead of keys compared with one another (33 -> 26 us at 64 rows).
 #include <cuda_bf16.h>
 
 #include "host.h"
@@ -92,6 +99,7 @@ struct Smem {
   Found found;
   // the bracket's edges in classes, and what the cluster found of it
   uint32_t edge_lo, edge_hi, bracket_n, overflow;
+  uint32_t vectors, sampled;  // of the row, and in the sample
   uint64_t bracket_mass, above, total;
   float cta_max[kMaxCtas];
   uint64_t cta_mass[kMaxCtas];
@@ -165,6 +173,13 @@ struct Scale {
   // -x = (m - z) c, which is the exact negative of (z - m) c and never -0.  A token whose -x is 32 or
   // more, or NaN, weighs nothing (exp2_neg and weight_of give 0 for those too).
   __device__ __forceinline__ float neg_x(float z) const { return __fmul_rn(__fsub_rn(m, z), c); }
+  // Two at once: z * -1 + m rounds as m - z does.
+  __device__ __forceinline__ void neg_x2(float z0, float z1, float (&nx)[2]) const {
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 d, {%5, %5};\n"
+        " fma.rn.f32x2 a, a, b, d;\n mov.b64 b, {%6, %6};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+        : "=f"(nx[0]), "=f"(nx[1])
+        : "f"(z0), "f"(z1), "f"(-1.0f), "f"(m), "f"(c));
+  }
 };
 __device__ __forceinline__ float exp2_neg(float nx) {
   float e;
@@ -173,7 +188,7 @@ __device__ __forceinline__ float exp2_neg(float nx) {
 }
 __device__ __forceinline__ uint32_t weight_of(float e) { return __float2uint_rn(e * 1073741824.0f); }
 
-// f(vector) over the vectors b + lane, b + lane + 32 * STEP, ... of [b, e), U of them in flight.
+// f(vector, its index) over the vectors b + lane, b + lane + 32 * STEP, ... of [b, e), U of them in flight.
 template <int STEP, typename T, typename F>
 __device__ __forceinline__ void walk(const Row<T> &row, int b, int e, int lane, F &&f) {
   constexpr int U = 4;
@@ -184,7 +199,7 @@ __device__ __forceinline__ void walk(const Row<T> &row, int b, int e, int lane, 
       if (s + 32 * STEP * u < e) q[u] = row.load(s + 32 * STEP * u);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (s + 32 * STEP * u < e) f(q[u]);
+      if (s + 32 * STEP * u < e) f(q[u], s + 32 * STEP * u);
   }
 }
 
@@ -282,23 +297,28 @@ struct Cut {
   uint32_t key, r;
 };
 
-// The bracket of a top-p cut from the classes' counts of a sample, run by every thread of the first CTA:
-// classes below edge_lo lie above the cut, classes from edge_hi on below it, to 4.5 standard deviations.
-// The sampled share of the mass above a cut at share p has variance
-//   ((1 - p)^2 sum of w^2 above + p^2 sum of w^2 below) / (sum of w)^2
-// times the share not sampled: a few heavy tokens above the cut hardly blur it.
+// The bracket of a top-p cut, run by every thread of the first CTA: classes below edge_lo lie above the
+// cut, classes from edge_hi on below it, to 4.5 standard deviations.  s.count holds the sampled tokens
+// (taken at their class's middle; one stands for k = s.vectors / s.sampled), s.mass the weights of the
+// thread maxima, which the sample leaves out: a heavy token that one sample holds and the next does not
+// would blur everything.  The estimated share of the mass above a cut at share p has variance
+//   ((1 - p)^2 sum of w^2 above + p^2 sum of w^2 below) k (k - 1) / (sum of w)^2
+// over the tokens that were sampled.  The classes' own width adds a little (0.01 p (1 - p)).
 // `most`: keys that the lists should have to hold at most.
-__device__ void sample_bracket(Smem &s, float top_p, float unsampled, float scale, float most) {
+__device__ void sample_bracket(Smem &s, float top_p, float most) {
   constexpr int PER = kClasses / kThreads;
   const int b0 = threadIdx.x * PER;
   uint64_t c = 0, m = 0, sq = 0, zero = 0;
+  const float k = static_cast<float>(s.vectors) / static_cast<float>(s.sampled);
+  const uint64_t k256 = static_cast<uint64_t>(k * 256.0f + 0.5f);
   auto weight = [&](int b) { return static_cast<uint64_t>(weight_of(exp2_neg((b + 0.5f) / 32.0f))); };
-  auto square = [&](int b) { return (weight(b) >> 15) * (weight(b) >> 15); };  // in units of 2^30
+  auto mass = [&](int b) { return (s.count[b] * weight(b) * k256 >> 8) + s.mass[b]; };
+  auto square = [&](int b) { return s.count[b] * (weight(b) * weight(b) >> 14); };  // in units of 2^14
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     c += s.count[b0 + i];
-    m += s.count[b0 + i] * weight(b0 + i);
-    sq += s.count[b0 + i] * square(b0 + i);
+    m += mass(b0 + i);
+    sq += square(b0 + i);
   }
   const uint64_t own_m = m, own_sq = sq;
   block_prefix(s.scan, c, m);
@@ -314,8 +334,8 @@ __device__ void sample_bracket(Smem &s, float top_p, float unsampled, float scal
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const float before = static_cast<float>(mi);
-      mi += s.count[b0 + i] * weight(b0 + i);
-      si += s.count[b0 + i] * square(b0 + i);
+      mi += mass(b0 + i);
+      si += square(b0 + i);
       if (before <= x && static_cast<float>(mi) > x) f(b0 + i, ci, si);
       ci += s.count[b0 + i];
     }
@@ -323,17 +343,17 @@ __device__ void sample_bracket(Smem &s, float top_p, float unsampled, float scal
   crossing(top_p * total, [&](int, uint64_t, uint64_t si) { s.bracket_mass = si; });
   __syncthreads();
   const float up = static_cast<float>(s.bracket_mass), q = 1.0f - top_p;
-  const float var = (q * q * up + top_p * top_p * fmaxf(all_sq - up, 0.0f)) * 1073741824.0f / (total * total);
-  const float width = 4.5f * sqrtf(fmaxf(var * unsampled, 0.0f)) + 0.0005f * fminf(q, top_p);
+  const float var = (q * q * up + top_p * top_p * fmaxf(all_sq - up, 0.0f)) * 16384.0f / (total * total);
+  const float width = 4.5f * sqrtf(fmaxf(var * k * (k - 1.0f), 0.0f)) + 0.01f * q * top_p;
   crossing((top_p - width) * total, [&](int b, uint64_t ci, uint64_t) { s.edge_lo = b, s.bracket_n = static_cast<uint32_t>(ci); });
   __syncthreads();
   const int lo = static_cast<int>(s.edge_lo);
   const float to = (top_p + width) * total, n0 = static_cast<float>(s.bracket_n);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {  // the last class it needs, or the last that fits
-    m += s.count[b0 + i] * weight(b0 + i);
+    m += mass(b0 + i);
     c += s.count[b0 + i];
-    if (b0 + i >= lo && (static_cast<float>(m) >= to || (static_cast<float>(c) - n0) * scale >= most))
+    if (b0 + i >= lo && (static_cast<float>(m) >= to || (static_cast<float>(c) - n0) * k >= most))
       atomicMin(&s.edge_hi, static_cast<uint32_t>(b0 + i + 1));
   }
 }
@@ -363,10 +383,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   const float min_p = p.min_p && !greedy ? p.min_p[r] : 0.0f;
   const bool use_k = k > 0 && k < p.v, use_p = top_p < 1.0f;
 
-  // 1. maximum
-  float mx = -inf;
-  walk<1>(row, vb, ve, lane, [&](const uint4 &q) { mx = fmaxf(mx, Row<T>::max_of(q)); });
-  const float own_max = mx;
+  // 1. maximum; m1 and m2: the largest logits of this thread's two heaviest vectors, i1 and i2
+  float m1 = -inf, m2 = -inf;
+  int i1 = 0, i2 = 0;
+  walk<1>(row, vb, ve, lane, [&](const uint4 &q, int i) {
+    const float v = Row<T>::max_of(q);
+    const bool first = v > m1, second = v > m2;
+    m2 = first ? m1 : second ? v : m2;
+    i2 = first ? i1 : second ? i : i2;
+    m1 = first ? v : m1;
+    i1 = first ? i : i1;
+  });
+  float mx = m1;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
   if (lane == 0) s.warp_max[warp] = mx;
@@ -381,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   if (threadIdx.x == 0) {
     s.few_n[0] = s.few_n[1] = 0;
     s.found.count = s.found.mass = 0;
+    s.vectors = s.sampled = 0;
   }
   __syncthreads();
   mx = s.warp_max[0];
@@ -424,11 +453,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     // Adds this CTA's bins to the first CTA's.
     auto add_to_first = [&](uint32_t *count, uint64_t *mass, int n) {
       if (rank != 0)
-        for (int i = threadIdx.x; i < n; i += kThreads)
-          if (count[i]) {
-            red_add_cluster_u32(to_first(&count[i]), count[i]);
-            if (mass) red_add_cluster_u64(to_first(&mass[i]), mass[i]);
-          }
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+          if (count[i]) red_add_cluster_u32(to_first(&count[i]), count[i]);
+          if (mass[i]) red_add_cluster_u64(to_first(&mass[i]), mass[i]);
+        }
     };
     auto class_edge = [](uint32_t b) { return static_cast<float>(b) / 32.0f; };
     // Reads a field of the first CTA's shared memory.
@@ -436,11 +464,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     auto first_u64 = [&](const uint64_t &f) { return ctas > 1 ? ld_cluster_u64(to_first(&f)) : f; };
 
     // 2. the bracket
-    if (use_k) {
-      const float nx = sc.neg_x(only_max ? (own_max == mx ? 0.0f : -inf) : own_max);
-      if (nx < 32.0f) atomicAdd(&s.count[static_cast<int>(nx * 32.0f)], 1u);
-    } else {
-      walk<kSampled>(row, vb, ve, lane, [&](const uint4 &q) {
+    // a thread maximum is one token, counted for top-k and weighed for top-p (the halves of the weights' sums
+    // in the lists' room, which is not in use yet: 1024 maxima a CTA cannot overflow them)
+    uint32_t *const half = s.kept;
+    if (!use_k) {
+      for (int i = threadIdx.x; i < 2 * kClasses; i += kThreads) half[i] = 0;
+      __syncthreads();
+    }
+    auto count_max = [&](float z, int i) {
+      const float nx = sc.neg_x(only_max ? (z == mx ? 0.0f : -inf) : z);
+      if (!(nx < 32.0f)) return;
+      const int b = static_cast<int>(nx * 32.0f);
+      if (use_k) {
+        atomicAdd(&s.count[b], 1u);
+      } else {
+        const uint32_t w = weight_of(exp2_neg(nx));
+        atomicAdd(&half[b], w & 0xFFFFu);
+        atomicAdd(&half[kClasses + b], w >> 16);
+        // the sample below counts it too if it holds its vector
+        if (((i - vb - lane) >> 5) % kSampled == 0) atomicSub(&s.count[b], 1u);
+      }
+    };
+    count_max(m1, i1);
+    count_max(m2, i2);
+    if (!use_k) {
+      if (lane == 0) {  // groups of 32 vectors, every kSampled-th of them in the sample
+        const int len = ve - vb, groups = len / (32 * kSampled), rest = len - groups * 32 * kSampled;
+        red_add_cluster_u32(to_first(&s.vectors), static_cast<uint32_t>(len));
+        red_add_cluster_u32(to_first(&s.sampled), static_cast<uint32_t>(groups * 32 + min(rest, 32)));
+      }
+      walk<kSampled>(row, vb, ve, lane, [&](const uint4 &q, int) {
         float z[EV];
         unpack(q, z);
 #pragma unroll
@@ -451,7 +504,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
       });
     }
     __syncthreads();
-    add_to_first(s.count, nullptr, kClasses);
+    if (!use_k) {
+      for (int i = threadIdx.x; i < kClasses; i += kThreads)
+        if (half[i] | half[kClasses + i])  // (added, not stored: the first CTA's may be getting others' already)
+          red_add_cluster_u64(map_to_rank(smem_u32(&s.mass[i]), rank), (static_cast<uint64_t>(half[kClasses + i]) << 16) + half[i]);
+      __syncthreads();
+    }
+    add_to_first(s.count, s.mass, kClasses);
     row_sync(ctas);
     if (rank == 0) {
       if (use_k) {
@@ -459,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         __syncthreads();
         if (threadIdx.x == 0) s.edge_lo = 0, s.edge_hi = s.found.ok ? s.found.bin + 1 : 0;
       } else {
-        sample_bracket(s, top_p, 1.0f - 1.0f / kSampled, kSampled, 0.5f * Row<T>::kList * kThreads * ctas);
+        sample_bracket(s, top_p, 0.5f * Row<T>::kList * kThreads * ctas);
       }
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -486,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         const float reach = hi / sc.c;
         float floor = mx - reach - (fabsf(mx) + reach) * 9.5367431640625e-7f;
         if (only_max || !(floor > -inf)) floor = -inf;
-        walk<1>(row, vb, ve, lane, [&](const uint4 &q) {
+        walk<1>(row, vb, ve, lane, [&](const uint4 &q, int) {
           if (!(Row<T>::max_of(q) >= floor)) return;
           room();
           float z[EV];
@@ -501,20 +560,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         });
       } else {
         const uint32_t lo_key = __float_as_uint(lo), span = __float_as_uint(hi) - lo_key;
-        walk<1>(row, vb, ve, lane, [&](const uint4 &q) {
+        walk<1>(row, vb, ve, lane, [&](const uint4 &q, int) {
           room();
           float z[EV];
           unpack(q, z);
 #pragma unroll
-          for (int i = 0; i < EV; ++i) {
-            const float nx = sc.neg_x(z[i]);
-            const uint32_t w = weight_of(exp2_neg(nx));
-            all += w;
-            if (nx < lo) above += w;
-            if (__float_as_uint(nx) - lo_key < span) {
-              *at = static_cast<T>(z[i]);
-              at += kThreads;
-              ++mine;
+          for (int i = 0; i < EV; i += 2) {
+            float nx[2];
+            sc.neg_x2(z[i], z[i + 1], nx);
+            const uint32_t w[2] = {weight_of(exp2_neg(nx[0])), weight_of(exp2_neg(nx[1]))};
+            all += w[0] + w[1];  // (at most 2^31)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (nx[j] < lo) above += w[j];
+              if (__float_as_uint(nx[j]) - lo_key < span) {
+                *at = static_cast<T>(z[i + j]);
+                at += kThreads;
+                ++mine;
+              }
             }
           }
         });
@@ -562,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
           if (key >= lo && key < hi) f(key);
         }
       } else {
-        walk<1>(row, vb, ve, lane, [&](const uint4 &q) {
+        walk<1>(row, vb, ve, lane, [&](const uint4 &q, int) {
           float z[EV];
           unpack(q, z);
 #pragma unroll
@@ -715,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     }
   };
   auto add_row = [&](int b, int e) {
-    walk<1>(row, b, e, lane, [&](const uint4 &q) {
+    walk<1>(row, b, e, lane, [&](const uint4 &q, int) {
       float z[EV];
       unpack(q, z);
 #pragma unroll
