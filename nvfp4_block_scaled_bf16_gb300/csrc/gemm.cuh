@@ -1533,14 +1533,14 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
               if constexpr (EPI == kEpiGatedGrad) ld_global_nc_v8(p.dh + token * p.ldh + (wr >> 1), dv);
               gated_row_chunk<EPI>(p, token, wr, v, alpha, alpha1, dv);
             }
-            continue;
-          }
+          } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = 32 * c + i;
-            if (j < t.cols) {
-              const float v = __fmul_rn(alpha, __uint_as_float(r[i]));
-              p.d[(t.out_j0 + j) * p.ldd + t.out_i0 + row] = __float2bfloat16_rn(v);
+            for (int i = 0; i < 32; ++i) {
+              const int j = 32 * c + i;
+              if (j < t.cols) {
+                const float v = __fmul_rn(alpha, __uint_as_float(r[i]));
+                p.d[(t.out_j0 + j) * p.ldd + t.out_i0 + row] = __float2bfloat16_rn(v);
+              }
             }
           }
         }

@@ -1274,8 +1274,9 @@ extern "C" nvfp4_status_t block_norm_backward(const void *dh, int64_t lddh, cons
     if (w_pre) out[k++] = dw_pre;
     if (w_post) out[k++] = dw_post;
     if (channel_gate) out[k++] = static_cast<float *>(dgate);
+    // (behind the kernel above with PDL whatever the flags: it waits for that kernel itself)
     e = launch(norm_colsum_kernel, dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(planes) * n, 32))), dim3(32, 32), 0,
-               (cudaStream_t)stream, pdl, 1, (const float *)workspace, teams, planes, static_cast<int>(n), out[0], out[1], out[2]);
+               (cudaStream_t)stream, pdl || m > 0, 1, (const float *)workspace, teams, planes, static_cast<int>(n), out[0], out[1], out[2]);
   }
   return check_launch(e, name);
 }

@@ -35,14 +35,17 @@
 // pass for 5.  Both ways give the same cut.  Without top-k and top-p only 1 and 5 run, from the row.
 //
 // The row is read from memory once, then from L2.  What bounds it, measured on device: 256 rows of 131072
-// bf16 with top-p take 72 us (floor 10 us, the logits read once), of them 6 the maximum, 8 the bracket, 18 to
+// bf16 with top-p take 70 us (floor 10 us, the logits read once), of them 6 the maximum, 8 the bracket, 18 to
 // 26 the pass (issue: about 15 instructions a token on the SMs that hold two rows), 10 the cut; 64 rows with
 // every filter 28 us (floor 2.5) and one row of 32000 fp32 7.6 us, which is latency: seven passes or
-// cluster barriers of one to three microseconds each.
+// cluster barriers of one to three microseconds each.  Between the steps of a decoder the code itself
+// leaves L2, and fetching it costs as much again (one row: 19 us with nothing in L2, 27 us before the
+// code was halved: 304 -> 155 KB).
 // Measured and not kept: classes and 64-bit masses of the whole row with shared-memory atomics, two of
 // them a token (328 and 83 us: a 64-bit one costs several 32-bit ones), which is now only the fallback;
 // a sample of every fourth vector with p (1 - p) for the variance, which overflowed lists (206 us); a
-// sorted list instead of keys compared with one another (33 -> 26 us at 64 rows).
+// sorted list instead of keys compared with one another (33 -> 26 us at 64 rows); find_bin and find_key
+// as calls (64 rows 28 -> 32 us).
 #include <cuda_bf16.h>
 
 #include "host.h"
@@ -126,6 +129,9 @@ struct Row {
   __device__ __forceinline__ uint4 load(int vec) const {
     const int i0 = vec * EV - off;
     if (i0 >= 0 && i0 + EV <= v) return *reinterpret_cast<const uint4 *>(p + i0);
+    return load_edge(p, i0, v);
+  }
+  static __device__ __noinline__ uint4 load_edge(const T *p, int i0, int v) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < EV; ++i) {
@@ -188,10 +194,10 @@ __device__ __forceinline__ float exp2_neg(float nx) {
 }
 __device__ __forceinline__ uint32_t weight_of(float e) { return __float2uint_rn(e * 1073741824.0f); }
 
-// f(vector, its index) over the vectors b + lane, b + lane + 32 * STEP, ... of [b, e), U of them in flight.
-template <int STEP, typename T, typename F>
+// f(vector, its index) over the vectors b + lane, b + lane + 32 * STEP, ... of [b, e), U of them in flight (one where speed does not count: code is kept small, since a step of a
+// decoder finds it in DRAM again).
+template <int STEP, int U, typename T, typename F>
 __device__ __forceinline__ void walk(const Row<T> &row, int b, int e, int lane, F &&f) {
-  constexpr int U = 4;
   for (int s = b + lane; s < e; s += 32 * STEP * U) {
     uint4 q[U];
 #pragma unroll
@@ -228,7 +234,7 @@ __device__ __forceinline__ void block_prefix(uint64_t (&scan)[2][kWarps], uint64
 
 // The bin of [0, n) in which the running count (or mass), starting from what found holds, reaches
 // `target`; found then holds what lies before that bin.  Run by every thread of the first CTA.
-__device__ void find_bin(Smem &s, const uint32_t *count, const uint64_t *mass, int n, bool by_mass, uint64_t target) {
+__device__ __forceinline__ void find_bin(Smem &s, const uint32_t *count, const uint64_t *mass, int n, bool by_mass, uint64_t target) {
   const uint64_t c0 = s.found.count, m0 = s.found.mass;
   const int per = n > kThreads ? n / kThreads : 1;
   const int b0 = threadIdx.x * per;
@@ -259,7 +265,7 @@ __device__ void find_bin(Smem &s, const uint32_t *count, const uint64_t *mass, i
 // sorting them, and no barriers): the key at which the count reaches `k` (0: no such target), then
 // the one at which the mass reaches `target`, or with top_p < 1 that share of the mass up to the first cut.
 // Run by every thread of the first CTA.
-__device__ void find_key(Smem &s, int n, uint64_t k, uint64_t target, float top_p) {
+__device__ __forceinline__ void find_key(Smem &s, int n, uint64_t k, uint64_t target, float top_p) {
   uint32_t key = 0, w = 0, eq = 0;
   uint64_t less = s.found.count, mass = s.found.mass;
   const bool in = static_cast<int>(threadIdx.x) < n;
@@ -305,7 +311,7 @@ struct Cut {
 //   ((1 - p)^2 sum of w^2 above + p^2 sum of w^2 below) k (k - 1) / (sum of w)^2
 // over the tokens that were sampled.  The classes' own width adds a little (0.01 p (1 - p)).
 // `most`: keys that the lists should have to hold at most.
-__device__ void sample_bracket(Smem &s, float top_p, float most) {
+__device__ __forceinline__ void sample_bracket(Smem &s, float top_p, float most) {
   constexpr int PER = kClasses / kThreads;
   const int b0 = threadIdx.x * PER;
   uint64_t c = 0, m = 0, sq = 0, zero = 0;
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   // 1. maximum; m1 and m2: the largest logits of this thread's two heaviest vectors, i1 and i2
   float m1 = -inf, m2 = -inf;
   int i1 = 0, i2 = 0;
-  walk<1>(row, vb, ve, lane, [&](const uint4 &q, int i) {
+  walk<1, 4>(row, vb, ve, lane, [&](const uint4 &q, int i) {
     const float v = Row<T>::max_of(q);
     const bool first = v > m1, second = v > m2;
     m2 = first ? m1 : second ? v : m2;
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         red_add_cluster_u32(to_first(&s.vectors), static_cast<uint32_t>(len));
         red_add_cluster_u32(to_first(&s.sampled), static_cast<uint32_t>(groups * 32 + min(rest, 32)));
       }
-      walk<kSampled>(row, vb, ve, lane, [&](const uint4 &q, int) {
+      walk<kSampled, 4>(row, vb, ve, lane, [&](const uint4 &q, int) {
         float z[EV];
         unpack(q, z);
 #pragma unroll
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         const float reach = hi / sc.c;
         float floor = mx - reach - (fabsf(mx) + reach) * 9.5367431640625e-7f;
         if (only_max || !(floor > -inf)) floor = -inf;
-        walk<1>(row, vb, ve, lane, [&](const uint4 &q, int) {
+        walk<1, 4>(row, vb, ve, lane, [&](const uint4 &q, int) {
           if (!(Row<T>::max_of(q) >= floor)) return;
           room();
           float z[EV];
@@ -560,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         });
       } else {
         const uint32_t lo_key = __float_as_uint(lo), span = __float_as_uint(hi) - lo_key;
-        walk<1>(row, vb, ve, lane, [&](const uint4 &q, int) {
+        walk<1, 4>(row, vb, ve, lane, [&](const uint4 &q, int) {
           room();
           float z[EV];
           unpack(q, z);
@@ -625,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
           if (key >= lo && key < hi) f(key);
         }
       } else {
-        walk<1>(row, vb, ve, lane, [&](const uint4 &q, int) {
+        walk<1, 1>(row, vb, ve, lane, [&](const uint4 &q, int) {
           float z[EV];
           unpack(q, z);
 #pragma unroll
@@ -745,9 +751,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     };
     // (few keys in the bracket of top-k: both cuts are among them)
     const bool both = use_k && use_p && listed && n <= kFew;
-    if (use_k) total = keep(false, static_cast<uint64_t>(k), 0, both);
-    if (use_p && !both) {
-      if (total == 0) {  // no top-k and no bracket, or fewer than k tokens have weight: the whole row's mass
+#pragma unroll 1
+    for (int which = use_k ? 0 : 1; which < (use_p && !both ? 2 : 1); ++which) {
+      if (which == 1 && total == 0) {  // no top-k and no bracket, or fewer than k tokens have weight: the whole row's mass
         if (rank == 0) {
           uint64_t a = 0, b = 0;
           for (int i = threadIdx.x; i < kClasses; i += kThreads) a += s.mass[i];
@@ -759,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         total = first_u64(s.total);
         row_sync(ctas);
       }
-      keep(true, mass_target(top_p, total), 1, false);
+      const uint64_t mass = keep(which == 1, which == 1 ? mass_target(top_p, total) : static_cast<uint64_t>(k), which, both);
+      if (which == 0) total = mass;
     }
   }
   // the first of the order stays whatever the filters say
@@ -778,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     }
   };
   auto add_row = [&](int b, int e) {
-    walk<1>(row, b, e, lane, [&](const uint4 &q, int) {
+    walk<1, 2>(row, b, e, lane, [&](const uint4 &q, int) {
       float z[EV];
       unpack(q, z);
 #pragma unroll
@@ -788,48 +795,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
       }
     });
   };
-  auto to_warps = [&]() {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      mass += __shfl_xor_sync(0xFFFFFFFFu, mass, o);
-      ties += __shfl_xor_sync(0xFFFFFFFFu, ties, o);
-    }
-    if (lane == 0) s.warp_mass[warp] = mass, s.warp_ties[warp] = ties;
-    __syncthreads();
-  };
-  if (listed) {
-    // (all that is above the bracket is kept: neither the cut nor min-p reaches there)
-    for (int i = 0; i < mine; ++i) add(__float_as_uint(sc.neg_x(static_cast<float>(list[i * kThreads]))));
-    mass += above;
-  } else {
-    add_row(vb, ve);
-  }
-  to_warps();
-  uint64_t cta_mass = 0;
-  uint32_t cta_ties = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) cta_mass += s.warp_mass[w], cta_ties += s.warp_ties[w];
-  if (ctas > 1) {
-    if (threadIdx.x < ctas) {
-      st_cluster_u64(map_to_rank(smem_u32(&s.cta_mass[rank]), threadIdx.x), cta_mass);
-      st_cluster_u32(map_to_rank(smem_u32(&s.cta_ties[rank]), threadIdx.x), cta_ties);
-    }
-    cluster_sync();  // (the last access to another CTA's shared memory: a CTA may leave after it)
-  } else {
-    if (threadIdx.x == 0) s.cta_mass[0] = cta_mass, s.cta_ties[0] = cta_ties;
-    __syncthreads();
-  }
-  const uint64_t wc = cut.key == kNoCut ? 0 : weight_of(exp2_neg(__uint_as_float(cut.key)));
-  uint64_t total = 0;
-  uint32_t all_ties = 0;
-  for (int i = 0; i < ctas; ++i) total += s.cta_mass[i], all_ties += s.cta_ties[i];
-  total += wc * min(all_ties, cut.r);
-  const double want = static_cast<double>(p.uniform[r]) * static_cast<double>(total);
-  uint64_t target = want > 0.0 ? static_cast<uint64_t>(want) : 0;
-  if (target >= total) target = total - 1;
   // Which of n consecutive stretches holds the target (-1: none); `before` and `left`, the mass before the
   // stretch and the ties still to keep from it on, go by index: ties are kept until r of them are.
-  uint64_t before = 0;
+  const uint64_t wc = cut.key == kNoCut ? 0 : weight_of(exp2_neg(__uint_as_float(cut.key)));
+  uint64_t before = 0, target = 0, total = 0;
   uint32_t left = cut.r;
   auto find = [&](const uint64_t *m, const uint32_t *ti, int n) {
     for (int i = 0; i < n; ++i) {
@@ -841,19 +810,57 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     }
     return -1;
   };
-  if (find(s.cta_mass, s.cta_ties, ctas) != rank) return;
-  const int w0 = find(s.warp_mass, s.warp_ties, kWarps);
-  __syncthreads();  // (everyone has read the warps' sums)
-  // the CTA's warps share the piece, then the one whose part holds the target walks it to the token
-  const int pb = piece_at(rank * kWarps + w0), pe = piece_at(rank * kWarps + w0 + 1);
-  auto part_at = [&](int i) { return pb + static_cast<int>(static_cast<int64_t>(i) * (pe - pb) / kWarps); };
-  mass = 0;
-  ties = 0;
-  add_row(part_at(warp), part_at(warp + 1));
-  to_warps();
+  // first every warp's piece; then the CTA's warps share the piece that holds the target, and the warp whose
+  // part does walks it to the token
+  int qb = vb, qe = ve;
+#pragma unroll 1
+  for (int round = 0;; ++round) {
+    mass = 0;
+    ties = 0;
+    if (round == 0 && listed) {
+      // (all that is above the bracket is kept: neither the cut nor min-p reaches there)
+      for (int i = 0; i < mine; ++i) add(__float_as_uint(sc.neg_x(static_cast<float>(list[i * kThreads]))));
+      mass += above;
+    } else {
+      add_row(qb, qe);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mass += __shfl_xor_sync(0xFFFFFFFFu, mass, o);
+      ties += __shfl_xor_sync(0xFFFFFFFFu, ties, o);
+    }
+    if (lane == 0) s.warp_mass[warp] = mass, s.warp_ties[warp] = ties;
+    __syncthreads();
+    if (round == 1) break;
+    uint64_t cta_mass = 0;
+    uint32_t cta_ties = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) cta_mass += s.warp_mass[w], cta_ties += s.warp_ties[w];
+    if (ctas > 1) {
+      if (threadIdx.x < ctas) {
+        st_cluster_u64(map_to_rank(smem_u32(&s.cta_mass[rank]), threadIdx.x), cta_mass);
+        st_cluster_u32(map_to_rank(smem_u32(&s.cta_ties[rank]), threadIdx.x), cta_ties);
+      }
+      cluster_sync();  // (the last access to another CTA's shared memory: a CTA may leave after it)
+    } else {
+      if (threadIdx.x == 0) s.cta_mass[0] = cta_mass, s.cta_ties[0] = cta_ties;
+      __syncthreads();
+    }
+    uint32_t all_ties = 0;
+    for (int i = 0; i < ctas; ++i) total += s.cta_mass[i], all_ties += s.cta_ties[i];
+    total += wc * min(all_ties, cut.r);
+    const double want = static_cast<double>(p.uniform[r]) * static_cast<double>(total);
+    target = want > 0.0 ? static_cast<uint64_t>(want) : 0;
+    if (target >= total) target = total - 1;
+    if (find(s.cta_mass, s.cta_ties, ctas) != rank) return;
+    const int w0 = find(s.warp_mass, s.warp_ties, kWarps);
+    __syncthreads();  // (everyone has read the warps' sums)
+    const int pb = piece_at(rank * kWarps + w0), len = piece_at(rank * kWarps + w0 + 1) - pb;
+    qb = pb + static_cast<int>(static_cast<int64_t>(warp) * len / kWarps);
+    qe = pb + static_cast<int>(static_cast<int64_t>(warp + 1) * len / kWarps);
+  }
   if (find(s.warp_mass, s.warp_ties, kWarps) != warp) return;
-  const int qe = part_at(warp + 1);
-  for (int v0 = part_at(warp); v0 < qe; v0 += 32) {
+  for (int v0 = qb; v0 < qe; v0 += 32) {
     float z[EV];
     uint32_t wt[EV];
     uint32_t n_ties = 0;
