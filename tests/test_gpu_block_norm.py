@@ -298,3 +298,40 @@ def test_broadcast_inputs(nv):
     assert got[4].shape == (m, n)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(nv):
+    """Rows whose element offsets pass 2^31 (three rows, 2^30 + 8 elements apart), in and out."""
+    m, n, ld = 3, 1032, (1 << 30) + 8
+    d = inputs(m, n, gate="token")
+    buf = torch.empty(2 * ld + n, dtype=torch.bfloat16, device="cuda")
+    far = buf.as_strided((m, n), (ld, 1))
+    kw = dict(y=d["y"], w_post=d["w_post"], gate=d["gate"])
+    want, h = nv.block_norm(d["x"], d["w_pre"], **kw)
+    for k in ("x", "y", "gate"):
+        far.copy_(d[k])
+        got = nv.block_norm(**{**dict(x=d["x"], w_pre=d["w_pre"]), **kw, k: far})
+        assert torch.equal(got[0], want) and torch.equal(got[1], h)
+    nv.block_norm(d["x"], d["w_pre"], **kw, h=far)
+    assert torch.equal(far, h)
+    nv.block_norm(d["x"], d["w_pre"], **kw, x_out=far)
+    assert torch.equal(far, want)
+    g = nv.block_norm_backward(d["dh"], d["dr"], d["x"], d["w_pre"], **kw)
+    far.copy_(d["dh"])
+    for a, b in zip(g, nv.block_norm_backward(far, d["dr"], d["x"], d["w_pre"], **kw)):
+        assert torch.equal(a, b)
+
+
+def test_rows_copied_ahead_past_32_bits(nv):
+    """More elements than 2^31 in rows that are brought ahead through shared memory."""
+    m, n = 262200, 8192
+    x = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    last = torch.randn(40, n, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    x[-40:] = last
+    _, h = nv.block_norm(x, w)
+    assert torch.equal(h[-40:], nv.block_norm(torch.cat([last] * 20), w)[1][:40])
+    assert not h[:40].any()
+    dx = nv.block_norm_backward(h, None, x, w)[0]
+    want = nv.block_norm_backward(torch.cat([h[-40:]] * 20), None, torch.cat([last] * 20), w)[0][:40]
+    assert torch.equal(dx[-40:], want)

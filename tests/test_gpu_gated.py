@@ -182,3 +182,24 @@ def test_large_products_saturate_without_nan(nv, kind):
     big = np.abs(g) > 200
     ref = np.where(g > 0, g, 0.0) * u
     assert np.all(np.abs(hh - ref)[big] <= 2 * BF16 * np.abs(ref)[big] + 1e-2 * np.abs(u)[big])
+
+
+def test_offsets_past_32_bits(nv):
+    """More than 2^31 elements of dgu: the last rows equal those of a call on them alone (one K step, so
+    every plan adds the same numbers in the same order)."""
+    m, inter, k, tail = 132000, 8192, 32, 300
+    ops = nvfp4_operands(512, 2 * inter, k, 6)
+    b, sfb = dev(ops["qb"]), dev(ops["sfb"])
+    x = torch.randn(tail, k, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    full = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    full[-tail:] = x
+    gs = torch.tensor([float(ops["gsa"])], device="cuda")
+    alpha = torch.tensor([float(ops["alpha"]), float(ops["alpha"])], device="cuda")
+    dh = torch.ones(m, inter, dtype=torch.bfloat16, device="cuda")
+    a, sfa = nv.nvfp4_quantize(full, gs)
+    at, sfat = nv.nvfp4_quantize(x, gs)
+    dgu, h = nv.nvfp4_gated_gemm_backward(a, sfa, b, sfb, alpha, dh)
+    nv.check_status()
+    want, hw = nv.nvfp4_gated_gemm_backward(at, sfat, b, sfb, alpha, dh[-tail:].contiguous())
+    assert torch.equal(dgu[-tail:], want) and torch.equal(h[-tail:], hw)
+    assert not dgu[: m - tail].any()

@@ -234,3 +234,33 @@ def test_another_stream_and_pdl(nv):
     nv.sample_tokens(z, u, top_p=top_p, tokens=tok, logprobs=lp, stream=s, flags=nv.FLAG_PDL)
     s.synchronize()
     assert torch.equal(tok, want)
+
+
+def test_offsets_past_32_bits(nv):
+    """Rows 2^30 + 3 elements apart: the last one begins past 2^31."""
+    z = logits(3, 20000, torch.bfloat16, 2.0, 21)
+    ld = (1 << 30) + 3
+    far = torch.empty(2 * ld + 20000, dtype=torch.bfloat16, device="cuda").as_strided((3, 20000), (ld, 1))
+    far.copy_(z)
+    for kw in (dict(), dict(k=50), dict(p=0.9, mp=0.01)):
+        a, b = draw(nv, z, [0.2, 0.5, 0.8], **kw), draw(nv, far, [0.2, 0.5, 0.8], **kw)
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+def test_fallback_rows_beside_ordinary_ones(nv):
+    """A batch that mixes rows whose cut is found in the bracket with rows that need the whole row's classes
+    (equal logits, a k near the end), so that CTAs of different rows take different ways at once."""
+    v, rows = 30000, 60
+    z = logits(rows, v, torch.float32, 2.0, 33)
+    z[::3] = 1.5
+    k = np.where(np.arange(rows) % 5 == 0, v - 3, 40).astype(np.int32)
+    u = np.linspace(0.01, 0.97, rows).astype(np.float32)
+    p = np.full(rows, 0.8, dtype=np.float32)
+    tok, lp = draw(nv, z, u, k=k, p=p)
+    zz = z.double().cpu().numpy()
+    for r in range(rows):
+        if r % 3 == 0:       # ceil(0.8 k) equal tokens (k may be v - 3), by index
+            n = int(np.ceil(np.float64(p[r]) * int(k[r]) - 1e-9))
+            assert tok[r] == int(float(u[r]) * n), r
+        else:
+            covers(zz[r], float(u[r]), int(tok[r]), float(lp[r]), k=int(k[r]), p=float(p[r]))
