@@ -205,8 +205,10 @@ __device__ __forceinline__ void zero_pad_rows(const NormArgs &p, unsigned int bl
 // Blocks [0, row_blocks) hold the rows; with NVFP4 output the blocks after them zero the scale rows
 // between m and the next multiple of 128.
 // MAXT: threads of the largest block it is launched with (512 or 1024: 128 or 64 registers).
+// The one block an SM is spelled out for 1024: without it the compiler gave the widest rows 32 registers
+// (512 x 32768 forward 141 -> 65 us, 1024 x 8200 backward 162 -> 96, 512 x 32768 backward 567 -> 363).
 template <typename XT, int VPT, bool VEC, bool WARP, bool QUANT, int MAXT>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT)
+__global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 1 : 0)
     norm_kernel(const NormArgs p, unsigned int row_blocks) {
   __shared__ float s_buf[2][1][32];
   // The next kernel may launch now: it waits for this grid before it reads what is written here.
@@ -606,7 +608,7 @@ struct NormGradArgs {
 // row of the workspace, which norm_colsum_kernel adds up in order: no atomics, so the result does
 // not depend on timing.
 template <typename XT, int VPT, bool VEC, bool WARP, int MAXT>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT)
+__global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 1 : 0)
     norm_grad_kernel(const NormGradArgs p) {
   __shared__ float s_buf3[2][3][32];
   __shared__ float s_buf1[2][1][32];
@@ -986,23 +988,21 @@ Shape shape_of(int64_t n_pad, int vpt_pref) {
 
 template <typename XT, bool VEC, bool QUANT, int MAXT>
 auto forward_block(int vpt) {
-  return vpt == 1 ? norm_kernel<XT, 1, VEC, false, QUANT, MAXT>
-                  : (vpt == 2 ? norm_kernel<XT, 2, VEC, false, QUANT, MAXT> : norm_kernel<XT, 4, VEC, false, QUANT, MAXT>);
+  if constexpr (MAXT > 512)  // (more than 512 threads of two vectors each come before four vectors)
+    if (vpt == 4) return norm_kernel<XT, 4, VEC, false, QUANT, MAXT>;
+  return vpt == 1 ? norm_kernel<XT, 1, VEC, false, QUANT, MAXT> : norm_kernel<XT, 2, VEC, false, QUANT, MAXT>;
 }
 template <typename XT, bool VEC, bool QUANT>
 auto forward_kernel(const Shape &s) {
   if (s.warp) return s.vpt == 1 ? norm_kernel<XT, 1, VEC, true, QUANT, 512> : norm_kernel<XT, 2, VEC, true, QUANT, 512>;
   return s.threads <= 512 ? forward_block<XT, VEC, QUANT, 512>(s.vpt) : forward_block<XT, VEC, QUANT, 1024>(s.vpt);
 }
-template <typename XT, bool VEC, int MAXT>
-auto backward_block(int vpt) {
-  return vpt == 1 ? norm_grad_kernel<XT, 1, VEC, false, MAXT>
-                  : (vpt == 2 ? norm_grad_kernel<XT, 2, VEC, false, MAXT> : norm_grad_kernel<XT, 4, VEC, false, MAXT>);
-}
 template <typename XT, bool VEC>
 auto backward_kernel(const Shape &s) {
   if (s.warp) return s.vpt == 1 ? norm_grad_kernel<XT, 1, VEC, true, 512> : norm_grad_kernel<XT, 2, VEC, true, 512>;
-  return s.threads <= 512 ? backward_block<XT, VEC, 512>(s.vpt) : backward_block<XT, VEC, 1024>(s.vpt);
+  if (s.threads <= 512) return norm_grad_kernel<XT, 1, VEC, false, 512>;  // (one vector a thread up to 1024 threads)
+  return s.vpt == 1 ? norm_grad_kernel<XT, 1, VEC, false, 1024>
+                    : (s.vpt == 2 ? norm_grad_kernel<XT, 2, VEC, false, 1024> : norm_grad_kernel<XT, 4, VEC, false, 1024>);
 }
 
 // Teams of the backward pass: enough to fill the SMs, each with a row of its own.  (Fixed per shape
