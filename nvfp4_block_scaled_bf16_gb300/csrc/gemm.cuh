@@ -36,6 +36,11 @@
 //   warp 10     (pairs only) copies the scales into a ring of their own, ahead of the operands.
 // NACC accumulator buffers let the epilogue of tile t overlap the mainloop of tile t+1.
 //
+// EPI: instead of bf16(alpha * C), the epilogue may make the gated product of a feed-forward block of a
+// tile, or its gradient (gated.cu): operand rows alternate between 16 gate and 16 up rows, so both
+// products of an output meet in one thread (32 columns of a row), in one warp (a weight-side tile
+// without a split, turned around through shared memory) or in one unit of a split tile's reduction.
+//
 // CTA pairs (PAIR, 256 x 256 tiles for large M): a cluster of two CTAs runs cta_group::2 MMAs
 // (M = 256, issued by the first CTA; a 256x256x64 MMA occupies the pipe for the same ~128 cycles
 // as a 128x256x64 one on a single CTA).  Each CTA stages its 128 rows of A and its 128 rows of B;

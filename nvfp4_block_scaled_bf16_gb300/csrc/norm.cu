@@ -1022,7 +1022,7 @@ struct RingShape {
   int vpt, threads, per_sm, slots;
 };
 RingShape ring_slots(RingShape s, int slot) {
-  s.slots = (kSmemBudget / s.per_sm - kRingHead - 3072) / slot;
+  s.slots = (kSmemBudget / s.per_sm - kRingHead - 3 * 1024) / slot;
   if (s.slots > kMaxSlots) s.slots = kMaxSlots;
   s.use = s.slots >= 2;
   return s;
