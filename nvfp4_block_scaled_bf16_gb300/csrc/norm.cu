@@ -65,20 +65,6 @@ __device__ __forceinline__ int channel(int i, int t, int ts) {
   return VEC ? ((i >> 3) * ts + t) * 8 + (i & 7) : i * ts + t;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *f) {
-  const uint4 v = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void load8(const float *p, float *f) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float *f) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                                              pack_bf16x2(f[6], f[7]));
@@ -92,28 +78,91 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 
-// Channels past n read as zero, and so add nothing to any sum below.
-template <int VPT, bool VEC, typename T>
-__device__ __forceinline__ void load_row(const T *row, float (&f)[8 * VPT], int t, int ts, int n) {
-  if constexpr (VEC) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = (v * ts + t) * 8;
-      if (c < n) {
-        load8(row + c, f + 8 * v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[8 * v + i] = 0.0f;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8 * VPT; ++i) {
-      const int c = i * ts + t;
-      f[i] = c < n ? to_f32(row[c]) : 0.0f;
+// A row of an operand.  Channels past n read as zero, and so add nothing to any sum below.
+// AHEAD: load() loads, late() converts.  A kernel calls load() for every operand first: with load and
+// conversion together in each operand's branch, every operand waited for memory on its own (backward,
+// 2048 x 2047: 63 -> 35 us; forward, 4096 x 328: 8.2 -> 6.2 us).  Otherwise load() only notes the address and
+// early() does both: single channels in flight cost a register each (kernels say where that is too many).
+template <int VPT, bool VEC, bool AHEAD, typename T>
+struct Row {
+  static constexpr int kWords = VEC ? VPT * static_cast<int>(sizeof(T)) / 2 : 1;
+  static constexpr int kSingles = VEC ? 1 : 8 * VPT;
+  uint4 w[kWords];
+  T s[kSingles];
+  const T *at;
+  bool is;
+  // given: whether there is such an operand; one that is not there reads as zero.
+  __device__ __forceinline__ void load(bool given, const T *row, int t, int ts, int n) {
+    at = row;
+    is = given;
+    if constexpr (AHEAD) fetch(t, ts, n);
+  }
+  __device__ __forceinline__ void early(float (&f)[8 * VPT], int t, int ts, int n) {
+    if constexpr (!AHEAD) {
+      fetch(t, ts, n);
+      convert(f);
     }
   }
-}
+  __device__ __forceinline__ void late(float (&f)[8 * VPT]) const {
+    if constexpr (AHEAD) convert(f);
+  }
+
+ private:
+  __device__ __forceinline__ void zero() {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSingles; ++i) s[i] = T(0.0f);
+    }
+  }
+  __device__ __forceinline__ void fetch(int t, int ts, int n) {
+    zero();
+    if (!is) return;
+    if constexpr (VEC) {
+      constexpr int W = kWords / VPT;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (v * ts + t) * 8;
+        if (c < n)
+#pragma unroll
+          for (int k = 0; k < W; ++k) w[v * W + k] = reinterpret_cast<const uint4 *>(at + c)[k];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSingles; ++i) {
+        const int c = i * ts + t;
+        if (c < n) s[i] = at[c];
+      }
+    }
+  }
+  __device__ __forceinline__ void convert(float (&f)[8 * VPT]) const {
+    if constexpr (VEC) {
+      constexpr int W = kWords / VPT;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          const uint4 q = w[v * W + k];
+          const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+              f[8 * v + 4 * k + i] = __uint_as_float(u[i]);
+            } else {
+              f[8 * v + 2 * i] = __uint_as_float(u[i] << 16);
+              f[8 * v + 2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+            }
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSingles; ++i) f[i] = to_f32(s[i]);
+    }
+  }
+};
 template <int VPT, bool VEC, typename T>
 __device__ __forceinline__ void store_row(T *row, const float (&f)[8 * VPT], int t, int ts, int n) {
   if constexpr (VEC) {
@@ -204,7 +253,7 @@ __device__ __forceinline__ void zero_pad_rows(const NormArgs &p, unsigned int bl
 
 // Blocks [0, row_blocks) hold the rows; with NVFP4 output the blocks after them zero the scale rows
 // between m and the next multiple of 128.
-// MAXT: threads of the largest block it is launched with (512 or 1024: 128 or 64 registers).
+// MAXT: threads of the largest block it is launched with (512, 768 or 1024: 128, 80 or 64 registers).
 // The one block an SM is spelled out for 1024: without it the compiler gave the widest rows 32 registers
 // (512 x 32768 forward 141 -> 65 us, 1024 x 8200 backward 162 -> 96, 512 x 32768 backward 567 -> 363).
 template <typename XT, int VPT, bool VEC, bool WARP, bool QUANT, int MAXT>
@@ -224,26 +273,38 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 
   constexpr int E = 8 * VPT;
   TeamSum<1> team{s_buf};
   const float inv_n = 1.0f / static_cast<float>(p.n);
+  // (loaded ahead, a block's rows of single channels and rows of four vectors a thread were slower: 1024 x 8191
+  // 39 -> 46 us, 8 x 16385 22 -> 44, 512 x 32768 66 -> 92; registers again)
+  constexpr bool AHEAD = (VEC || WARP) && VPT < 4;
+  using Bf16Row = Row<VPT, VEC, AHEAD, __nv_bfloat16>;
   float r[E], w[E];
-  load_row<VPT, VEC>(static_cast<const XT *>(p.x) + row * p.ldx, r, t, ts, p.n);
+  Row<VPT, VEC, AHEAD, XT> rx;
+  Bf16Row ry, rw, rwp, rg;
+  rx.load(true, static_cast<const XT *>(p.x) + row * p.ldx, t, ts, p.n);
+  ry.load(p.y != nullptr, p.y + row * p.ldy, t, ts, p.n);
+  rw.load(p.w_pre != nullptr, p.w_pre, t, ts, p.n);
+  rwp.load(p.w_post != nullptr, p.w_post, t, ts, p.n);
+  rg.load(p.gate != nullptr, p.gate + row * p.ldg, t, ts, p.n);
+  rx.early(r, t, ts, p.n), rx.late(r);
   if (p.y) {
     float y[E];
-    load_row<VPT, VEC>(p.y + row * p.ldy, y, t, ts, p.n);
-    if (p.w_pre) load_row<VPT, VEC>(p.w_pre, w, t, ts, p.n);
+    ry.early(y, t, ts, p.n), ry.late(y);
+    rw.early(w, t, ts, p.n);
     if (p.w_post) {
       float wp[E];
-      load_row<VPT, VEC>(p.w_post, wp, t, ts, p.n);
+      rwp.early(wp, t, ts, p.n);
       float s[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < E; ++i) s[0] += y[i] * y[i];
       team.template sum<WARP>(s);
       const float rstd = rsqrtf(s[0] * inv_n + p.eps);
+      rwp.late(wp);
 #pragma unroll
       for (int i = 0; i < E; ++i) y[i] = y[i] * rstd * (p.offset + wp[i]);
     }
     if (p.gate) {
       float g[E];
-      load_row<VPT, VEC>(p.gate + row * p.ldg, g, t, ts, p.n);
+      rg.early(g, t, ts, p.n), rg.late(g);
 #pragma unroll
       for (int i = 0; i < E; ++i) y[i] *= g[i];
     }
@@ -251,7 +312,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 
     for (int i = 0; i < E; ++i) r[i] = r[i] + p.scale * y[i];
     store_row<VPT, VEC>(static_cast<XT *>(p.x_out) + row * p.ldxo, r, t, ts, p.n);
   } else {
-    load_row<VPT, VEC>(p.w_pre, w, t, ts, p.n);
+    rw.early(w, t, ts, p.n);
   }
   if (!p.w_pre) return;
   float s[1] = {0.0f};
@@ -259,6 +320,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 
   for (int i = 0; i < E; ++i) s[0] += r[i] * r[i];
   team.template sum<WARP>(s);
   const float rstd = rsqrtf(s[0] * inv_n + p.eps);
+  rw.late(w);
 #pragma unroll
   for (int i = 0; i < E; ++i) r[i] = r[i] * rstd * (p.offset + w[i]);
   if constexpr (QUANT) {
@@ -608,7 +670,7 @@ struct NormGradArgs {
 // row of the workspace, which norm_colsum_kernel adds up in order: no atomics, so the result does
 // not depend on timing.
 template <typename XT, int VPT, bool VEC, bool WARP, int MAXT>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 1 : 0)
+__global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT > 512 ? 1 : 0)
     norm_grad_kernel(const NormGradArgs p) {
   __shared__ float s_buf3[2][3][32];
   __shared__ float s_buf1[2][1][32];
@@ -618,6 +680,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 
   if (WARP && teamid >= p.teams) return;
   const int t = WARP ? threadIdx.x & 31 : threadIdx.x, ts = WARP ? 32 : blockDim.x;
   constexpr int E = 8 * VPT;
+  // (1024 threads have 64 registers each; loaded ahead: 1024 x 8191 94 -> 111 us, 1 x 7168 17 -> 23)
+  constexpr bool AHEAD = MAXT < 1024;
+  using Bf16Row = Row<VPT, VEC, AHEAD, __nv_bfloat16>;
   TeamSum<3> team3{s_buf3};
   TeamSum<1> team1{s_buf1};
   const float inv_n = 1.0f / static_cast<float>(p.n);
@@ -626,35 +691,22 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 
   for (int i = 0; i < E; ++i) aw[i] = ap[i] = ag[i] = 0.0f;
   for (int64_t row = teamid; row < p.m; row += p.teams) {
     float r[E], d[E], g[E], y[E];
-    load_row<VPT, VEC>(static_cast<const XT *>(p.r) + row * p.ldr, r, t, ts, p.n);
-    if (p.dh) {
-      load_row<VPT, VEC>(p.dh + row * p.lddh, d, t, ts, p.n);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) d[i] = 0.0f;
-    }
-    if (p.dr) {
-      load_row<VPT, VEC>(static_cast<const XT *>(p.dr) + row * p.lddr, g, t, ts, p.n);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) g[i] = 0.0f;
-    }
-    if (p.y) {
-      load_row<VPT, VEC>(p.y + row * p.ldy, y, t, ts, p.n);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) y[i] = 0.0f;
-    }
+    Row<VPT, VEC, AHEAD, XT> rr, rdr;
+    Bf16Row rd, ry, rw, rwp, rg;
+    rr.load(true, static_cast<const XT *>(p.r) + row * p.ldr, t, ts, p.n);
+    rd.load(p.dh != nullptr, p.dh + row * p.lddh, t, ts, p.n);
+    rdr.load(p.dr != nullptr, static_cast<const XT *>(p.dr) + row * p.lddr, t, ts, p.n);
+    ry.load(p.y != nullptr, p.y + row * p.ldy, t, ts, p.n);
+    rw.load(p.dh != nullptr, p.w_pre, t, ts, p.n);
+    rwp.load(p.w_post != nullptr, p.w_post, t, ts, p.n);
+    rg.load(p.gate != nullptr, p.gate + row * p.ldg, t, ts, p.n);
+    rr.early(r, t, ts, p.n), rd.early(d, t, ts, p.n), rdr.early(g, t, ts, p.n), ry.early(y, t, ts, p.n);
+    rr.late(r), rd.late(d), rdr.late(g), ry.late(y);
     // sums of r^2, of (dh w) r and of y^2 in one go: mean(d xn) = rstd * sum(d r) / n
     float s[3] = {0.0f, 0.0f, 0.0f};
     {
       float w[E];
-      if (p.dh) {
-        load_row<VPT, VEC>(p.w_pre, w, t, ts, p.n);
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) w[i] = 0.0f;
-      }
+      rw.early(w, t, ts, p.n), rw.late(w);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         s[0] += r[i] * r[i];
@@ -678,7 +730,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 
     const float rstd = p.w_post ? rsqrtf(s[2] * inv_n + p.eps) : 1.0f;
     float wp[E];
     if (p.w_post) {
-      load_row<VPT, VEC>(p.w_post, wp, t, ts, p.n);
+      rwp.early(wp, t, ts, p.n), rwp.late(wp);
 #pragma unroll
       for (int i = 0; i < E; ++i) wp[i] += p.offset;
     } else {
@@ -691,7 +743,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpTeams : MAXT, MAXT == 1024 ? 
       y[i] *= rstd;
     }
     if (p.gate) {
-      load_row<VPT, VEC>(p.gate + row * p.ldg, d, t, ts, p.n);
+      rg.early(d, t, ts, p.n), rg.late(d);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         r[i] = g[i] * y[i] * wp[i];
@@ -1001,15 +1053,20 @@ template <typename XT, bool VEC>
 auto backward_kernel(const Shape &s) {
   if (s.warp) return s.vpt == 1 ? norm_grad_kernel<XT, 1, VEC, true, 512> : norm_grad_kernel<XT, 2, VEC, true, 512>;
   if (s.threads <= 512) return norm_grad_kernel<XT, 1, VEC, false, 512>;  // (one vector a thread up to 1024 threads)
+  // (80 registers instead of 64: 2048 x 4099 126 -> 98 us)
+  if (s.threads <= 768 && s.vpt == 1) return norm_grad_kernel<XT, 1, VEC, false, 768>;
   return s.vpt == 1 ? norm_grad_kernel<XT, 1, VEC, false, 1024>
                     : (s.vpt == 2 ? norm_grad_kernel<XT, 2, VEC, false, 1024> : norm_grad_kernel<XT, 4, VEC, false, 1024>);
 }
 
-// Teams of the backward pass: enough to fill the SMs, each with a row of its own.  (Fixed per shape
-// and device, so that the order of the column sums is too.)
+// Teams of the backward pass: as many blocks as an SM holds at up to 104 registers a thread, each with a
+// row of its own (two whatever their size: 4096 x 723 82 us, 62 so); more than two of them only where each
+// keeps two rows (600 x 720 with a row a block 12.4 us instead of 10.3: its sums are written and read for
+// one row).  (Fixed per shape and device, so that the order of the column sums is too.)
 int grad_teams(int64_t m, const Shape &s, int sm_count) {
-  const int64_t per_sm = s.warp ? 4 * kWarpTeams : (s.threads <= 512 ? 2 : 1);
-  const int64_t cap = per_sm * sm_count;
+  const int64_t per_sm = s.warp ? 4 * kWarpTeams : (s.threads < 630 ? 630 / s.threads : 1);
+  int64_t cap = per_sm * sm_count;
+  if (!s.warp && cap > 2 * sm_count) cap = m / 2 < 2 * sm_count ? 2 * sm_count : (m / 2 < cap ? m / 2 : cap);
   return static_cast<int>(m < cap ? m : cap);
 }
 
@@ -1105,6 +1162,7 @@ static bool forward_ring(const NormArgs &a, bool f32, bool pdl, cudaStream_t str
   return true;
 }
 
+// (Rows of single channels: one always, 1024 x 8191 63 -> 43 us.)
 // One vector a thread while the rows are few (the call waits for one row's latency: 7168 channels,
 // one row), two from four rows an SM on (fewer, wider threads: more bytes in flight per warp).
 static int forward_vpt(int64_t m, int64_t n, int sm_count) { return m >= 4LL * sm_count && n > 2048 ? 2 : 1; }
@@ -1128,7 +1186,7 @@ extern "C" nvfp4_status_t block_norm(const void *x, int x_type, int64_t ldx, con
   const int xe = elem_of(x_type);
   const bool vec = n % 8 == 0 && rows_aligned(x, ldx, xe) && rows_aligned(y, ldy, 2) && rows_aligned(gate, ldg, 2) &&
                    rows_aligned(x_out, ldxo, xe) && rows_aligned(h, ldh, 2) && aligned(w_post, 16) && aligned(w_pre, 16);
-  const Shape s = shape_of(n, forward_vpt(m, n, dev.sm_count));
+  const Shape s = shape_of(n, vec ? forward_vpt(m, n, dev.sm_count) : 1);
   NormArgs a{x, ldx, (const __nv_bfloat16 *)y, ldy, (const __nv_bfloat16 *)w_post, (const __nv_bfloat16 *)w_pre,
              (const __nv_bfloat16 *)gate, ldg, residual_scale, eps, weight_offset, x_out, ldxo, (__nv_bfloat16 *)h, ldh,
              nullptr, nullptr, nullptr, m, static_cast<int>(n), 0};
