@@ -481,7 +481,7 @@ struct Ring {
 // norm_kernel for many rows (see the head of this file).  The sums of r^2 of a row
 // and of y^2 of the row after it share a barrier.  A thread keeps its channels' factors in fp32:
 // scale * gate * (offset + w_post) of y and offset + w_pre.
-// Measured at 4096 x 7168, cold L2: 47.6 us for 235 MB, where 34.9 us is the measured copy rate and 37 us
+// Measured at 4096 x 7168, cold L2: 48 to 49 us for 235 MB, where 34.9 us is the measured copy rate and 37 us
 // what a kernel takes that only reads two such arrays and writes two.  Against it, the same ring with two
 // barriers a row and the copies issued by one computing thread took 54 us, a warp per row 74 us (too few
 // warps fit beside the rows), plain loads 59 us, one more warp for the copies 52 us.  What is left is

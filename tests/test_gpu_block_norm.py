@@ -216,6 +216,37 @@ def test_backward_forms(nv, stream, post, gate, m, n, pad):
     check_backward(nv, d, 1.3, 1.0)
 
 
+# Rows of single channels (n no multiple of 8, or a wider buffer that breaks the alignment) over every block size,
+# and blocks of several to an SM; 4097 to 6144 channels also aligned with few rows.
+PLAIN = [(1500, 523, 0), (700, 723, 0), (1300, 1025, 0), (400, 2561, 0), (160, 4097, 0), (3, 6001, 0), (3, 5000, 0), (160, 6144, 3),
+         (5, 7169, 0), (2, 8200, 1), (160, 12289, 0), (2, 16385, 0), (1, 32767, 0)]
+
+
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n,pad", PLAIN)
+def test_single_channels(nv, m, n, pad, stream):
+    d = inputs(m, n, stream, pad=pad)
+    x_out, h = nv.block_norm(d["x"], d["w_pre"], y=d["y"], w_post=d["w_post"], gate=d["gate"], residual_scale=0.7, eps=EPS)
+    r_ref, h_ref = block.block_norm(f64(d["x"]), f64(d["w_pre"]), f64(d["y"]), f64(d["w_post"]), f64(d["gate"]), 0.7, EPS)
+    tr, th = forward_terms(d, 0.7, 0.0)
+    check(x_out, r_ref, BF16 if stream == torch.bfloat16 else 2.0 ** -23, tr, "x_out")
+    check(h, h_ref, BF16, th, "h")
+    check_backward(nv, d, 0.7, 0.0)
+
+
+@pytest.mark.parametrize("post,gate", [(True, "token"), (False, "none"), (None, "none")])
+@pytest.mark.parametrize("m,n", [(3, 5001), (3, 5000), (2, 7001), (2, 9001), (2, 20001)])
+def test_absent_operands_of_wide_rows(nv, m, n, post, gate):
+    """What is not there reads as zero in every block size, whether loaded ahead or not."""
+    d = inputs(m, n, torch.bfloat16, post, gate)
+    check_backward(nv, d, 1.3, 1.0)
+    d["dr"] = None
+    check_backward(nv, d, 1.3, 1.0)
+    if post is not None:
+        d["w_pre"] = None
+        check_backward(nv, d, 0.9, 0.0)
+
+
 def test_backward_without_the_second_norm_and_without_rows(nv):
     d = inputs(33, 512, gate="token")
     d["w_pre"] = None
