@@ -468,8 +468,8 @@ nvfp4_status_t block_norm_backward(const void *dh, int64_t lddh, const void *dx_
  * (2^x by the hardware's approximation, within 2^-22).  Tokens are ordered by x, largest first, ties by
  * index; each filter keeps a beginning of that order, and the first token always stays:
  *   top_k   the first top_k (<= 0: all)
- *   top_p   those before which the top_k weigh less than top_p * their total (>= 1: all)
- *   min_p   those with e_i >= min_p (<= 0: all)
+ *   top_p   those before which the top_k weigh less than top_p * their total (>= 1 or NaN: all)
+ *   min_p   those with e_i >= min_p (<= 0: all; above 1 or NaN: none but the first token)
  * The token is the first, by index, at which the kept tokens' cumulative weight exceeds
  * floor(uniform * total).  The weights are whole numbers and their sums exact, so the result depends
  * neither on timing nor on how a row is split.

@@ -384,9 +384,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
 
   const float t = p.temperature ? p.temperature[r] : 1.0f;
   const bool greedy = !(t > 0.0f);
-  const int32_t k = p.top_k && !greedy ? p.top_k[r] : 0;
-  const float top_p = p.top_p && !greedy ? p.top_p[r] : 1.0f;
-  const float min_p = p.min_p && !greedy ? p.min_p[r] : 0.0f;
+  // greedy, or a min_p that no token passes: the first of the order alone, whatever the other filters say
+  const bool only_first = greedy || (p.min_p && !(p.min_p[r] <= 1.0f));
+  const int32_t k = p.top_k && !only_first ? p.top_k[r] : 0;
+  const float top_p = p.top_p && !only_first ? p.top_p[r] : 1.0f;
+  const float min_p = p.min_p && !only_first ? p.min_p[r] : 0.0f;
   const bool use_k = k > 0 && k < p.v, use_p = top_p < 1.0f;
 
   // 1. maximum; m1 and m2: the largest logits of this thread's two heaviest vectors, i1 and i2
@@ -769,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
       if (which == 0) total = mass;
     }
   }
-  // the first of the order stays whatever the filters say
-  if (greedy || min_p > 1.0f || min_p != min_p) cut = Cut{0, 1};
+  // (so a token of the largest weight is always kept, and their total is never zero)
+  if (only_first) cut = Cut{0, 1};
 
   // 5. kept weight and ties, of a key and of a stretch of the row
   uint64_t mass = 0;
