@@ -176,8 +176,9 @@ struct Row {
 // What turns a logit into its place in the order.
 struct Scale {
   float m, c;
-  // -x = (m - z) c, which is the exact negative of (z - m) c and never -0.  A token whose -x is 32 or
-  // more, or NaN, weighs nothing (exp2_neg and weight_of give 0 for those too).
+  // -x = (m - z) c, which is the exact negative of (z - m) c.  It is never -0, whose bits are no key below
+  // any edge: m is not -0, so m - z is +0 for either zero z.  A token whose -x is 32 or more, or NaN, weighs
+  // nothing (exp2_neg and weight_of give 0 for those too).
   __device__ __forceinline__ float neg_x(float z) const { return __fmul_rn(__fsub_rn(m, z), c); }
   // Two at once: z * -1 + m rounds as m - z does.
   __device__ __forceinline__ void neg_x2(float z0, float z1, float (&nx)[2]) const {
@@ -431,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     mx = s.cta_max[0];
     for (int i = 1; i < ctas; ++i) mx = fmaxf(mx, s.cta_max[i]);
   }
+  mx = __fadd_rn(mx, 0.0f);  // -0 becomes +0 (see Scale)
   if (mx == -inf) {  // nothing but -inf and NaN (the same on every CTA of the row)
     if (rank == 0 && threadIdx.x == 0) {
       p.tokens[r] = -1;
