@@ -913,8 +913,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_grad_ring_kernel(const NormGr
     for (int i = 0; i < 6; ++i) v6[i] = __shfl_sync(0xFFFFFFFFu, tot, 4 * i);
     const float rx1 = rsqrtf(v6[0] * inv_n + p.eps), mean1 = v6[1] * rx1 * inv_n;
     const float ry1 = p.w_post ? rsqrtf(v6[2] * inv_n + p.eps) : 1.0f;
-    // without w_post dy has no mean, without dh v6[4] and mean1 are zero
-    const float e1 = p.w_post ? p.scale * ry1 * inv_n * (v6[3] + rx1 * v6[4] - rx1 * rx1 * mean1 * v6[5]) : 0.0f;
+    // without w_post dy has no mean; without dh the stream has no part in it (and rx1 and mean1 mean nothing: r^2
+    // is not added up, so with eps = 0 they are inf and NaN)
+    float dot = v6[3];
+    if (p.dh) dot = v6[3] + rx1 * v6[4] - rx1 * rx1 * mean1 * v6[5];
+    const float e1 = p.w_post ? p.scale * ry1 * inv_n * dot : 0.0f;
     const F2 rx = f2(rx1), neg_mean = f2(-mean1), ry = f2(ry1), neg_e = f2(-e1), scale = f2(p.scale);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
