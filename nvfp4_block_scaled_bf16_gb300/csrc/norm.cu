@@ -967,7 +967,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_grad_ring_kernel(const NormGr
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         ap[4 * v + i] = fma(g[i], a[i], ap[4 * v + i]);
-        g[i] = ry * fma(a[i], neg_e, g[i] * b[i]);
+        if (p.w_post) g[i] = ry * fma(a[i], neg_e, g[i] * b[i]);  // (otherwise dy does not depend on y)
       }
       store4(p.dy + row * p.lddy + c, g);
     }

@@ -81,3 +81,25 @@ def test_forward_without_the_second_norm(nv, m, n, stream):
         x = d["x"].clone()
         nv.block_norm(x, None, x_out=x, **kw)
         assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+@pytest.mark.parametrize("m,n", ROWS)
+def test_backward_without_the_norm_after_the_block(nv, m, n, gate, stream):
+    """Without w_post y is a factor of dgate alone: dx and dy do not depend on it, finite or not."""
+    d = inputs(m, n, stream, gate)
+    kw = dict(gate=d["gate"], residual_scale=0.9)
+    want = nv.block_norm_backward(d["dh"], d["dr"], d["x"], d["w_pre"], y=d["y"], **kw)
+    y = d["y"].clone()
+    at = [(0, 3), (m // 2, n // 2), (m - 1, n - 1)]
+    for (r, c), v in zip(at, ("nan", "inf", "-inf")):
+        y[r, c] = float(v)
+    got = nv.block_norm_backward(d["dh"], d["dr"], d["x"], d["w_pre"], y=y, **kw)
+    for a, b in zip(got[:3], want[:3]):
+        assert torch.equal(a, b)
+    if gate == "token":
+        same = torch.ones_like(got[4], dtype=torch.bool)
+        for r, c in at:
+            same[r, c] = False
+        assert torch.equal(got[4][same], want[4][same]) and not torch.isfinite(got[4][~same].float()).any()
