@@ -247,11 +247,15 @@ enum : int {
 
 // f = g * sigmoid(q), q = g * (a + b g^2), and its derivative f' = s + g s (1 - s) (a + 3 b g^2):
 // SiLU with a = 1, b = 0, GELU's tanh form with a = sqrt(8 / pi), b = 0.044715 a, because
-// (1 + tanh z) / 2 = sigmoid(2 z).  q is taken at g clamped to +-128, where the sigmoid is 0 or 1
-// in fp32 already, so that an infinite g gives no inf * 0.  (Approximate exp and reciprocal: both
-// are within a few fp32 ulps, and every result is rounded to bf16.)
+// (1 + tanh z) / 2 = sigmoid(2 z).  q and f' are taken at g clamped to +-128, where the sigmoid is 0 or 1
+// in fp32 already, so that f' is 0 or 1 at an infinite g and not inf * 0 (f itself is NaN at -inf, as
+// g / (1 + exp(-g)) is); a NaN passes the clamp and makes f and f' NaN.
+// Approximate exp and reciprocal: __expf is off by up to 2 + 1.2 |q| ulps and q by 3 roundings, so s is
+// within 2^-15 of itself, far below the rounding to bf16; it is 0 where exp(-q) passes 2^126.
 __device__ __forceinline__ void gate_act(const GemmArgs &p, float g, float &f, float &df) {
-  const float gc = fminf(fmaxf(g, -128.0f), 128.0f), g2 = gc * gc;
+  float gc;
+  asm("max.NaN.f32 %0, %1, %2;\n min.NaN.f32 %0, %0, %3;" : "=&f"(gc) : "f"(g), "f"(-128.0f), "f"(128.0f));
+  const float g2 = gc * gc;
   const float s = __fdividef(1.0f, 1.0f + __expf(-gc * (p.act_a + p.act_b * g2)));
   f = g * s;
   df = s + gc * s * (1.0f - s) * (p.act_a + 3.0f * p.act_b * g2);
