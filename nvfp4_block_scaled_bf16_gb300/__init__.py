@@ -99,8 +99,9 @@ def _check(code: int) -> None:
 
 # The pointers and the stream go to ctypes as plain integers (its argument types make them void *), and
 # the device and stream are asked of torch's C layer: a small call spends its time here, not on the GPU.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (Where that layer lacks them, in a torch without CUDA for one, the public functions stand in.)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _ptr(t):
