@@ -143,6 +143,19 @@ def _room(t, dtype, name, numel):
         raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
 
 
+def _on(stream):
+    """A context in which the caching allocator and torch's own kernels use the launch stream."""
+    return torch.cuda.stream(stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
+
+
+def _capturing(stream) -> bool:
+    """Whether the launch stream is being captured into a graph."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with _on(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _contig(t, stream):
     """`t` with dense rows.  A copy is made on the launch stream, so that the caching allocator
     cannot hand its memory out again before that stream's kernel has read it."""
@@ -150,8 +163,7 @@ def _contig(t, stream):
         return t
     if stream is None:
         return t.contiguous()
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
-    with torch.cuda.stream(s):
+    with _on(stream):
         return t.contiguous()
 
 
@@ -159,8 +171,7 @@ def _scratch(nbytes: int, device, stream):
     """An uninitialised uint8 workspace that belongs to the launch stream (see _contig)."""
     if stream is None:
         return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
-    with torch.cuda.stream(s):
+    with _on(stream):
         return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
@@ -194,9 +205,15 @@ def gemm_workspace(nbytes: int, device=None) -> torch.Tensor:
 _ws_cache: dict = {}
 
 
-def _default_workspace(nbytes: int, device: torch.device) -> torch.Tensor:
-    """One zeroed workspace per device, grown on demand and shared by every nvfp4_gemm call that
-    passes none.  Calls on streams that may overlap must pass their own workspace."""
+def _default_workspace(nbytes: int, device: torch.device, stream) -> torch.Tensor:
+    """A workspace for a product that was given none: one zeroed buffer per device, grown on demand.  Calls on
+    streams that may overlap must pass their own.  A call under graph capture gets a buffer of the
+    graph's, zeroed by every replay: the shared one is dropped when it grows, and was filled outside the graph."""
+    if _capturing(stream):
+        with _on(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            ws[:4096].zero_()      # the counters, one per split tile (at most one tile per two SMs); partials need no zero
+            return ws
     ws = _ws_cache.get(device)
     if ws is None or ws.numel() < nbytes:
         ws = gemm_workspace(nbytes, device)
@@ -268,7 +285,7 @@ def nvfp4_gemm(a, sfa, b, sfb, alpha, d=None, flags: int = 0, stream=None, works
     if workspace is None and m > 0:
         need = gemm_workspace_size(m, n, 2 * kh)
         if need:
-            workspace = _default_workspace(need, a.device)
+            workspace = _default_workspace(need, a.device, stream)
     if workspace is not None:
         _room(workspace, torch.uint8, "workspace", 0)   # the library checks its size
     _check(_lib.nvfp4_gemm(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(alpha), _ptr(d), m, n, 2 * kh,
@@ -341,7 +358,7 @@ def interleave_gate_up(gate, up):
     return torch.stack((gate.reshape(groups), up.reshape(groups)), dim=1).reshape(2 * gate.shape[0], *gate.shape[1:])
 
 
-def _gated_operands(a, sfa, b, sfb, alpha, activation, workspace):
+def _gated_operands(a, sfa, b, sfb, alpha, activation, workspace, stream):
     """Checks what the gated products share: (m, inter, k, activation, workspace)."""
     _need(a, torch.uint8, "a", 2)
     _need(b, torch.uint8, "b", 2)
@@ -361,7 +378,7 @@ def _gated_operands(a, sfa, b, sfb, alpha, activation, workspace):
     if workspace is None and m > 0 and n > 0:
         need = gemm_workspace_size(m, n, 2 * kh)
         if need:
-            workspace = _default_workspace(need, a.device)
+            workspace = _default_workspace(need, a.device, stream)
     if workspace is not None:
         _room(workspace, torch.uint8, "workspace", 0)   # the library checks its size
     return m, n // 2, 2 * kh, ACTIVATIONS[activation], workspace
@@ -374,7 +391,7 @@ def nvfp4_gated_gemm(a, sfa, b, sfb, alpha, activation: str = "silu", h=None, fl
 
     a [m, k/2] packed, b [2 inter, k/2] packed with gate and up rows alternating in groups of 16
     (interleave_gate_up), alpha fp32 [2], activation "silu" or "gelu_tanh"; workspace as nvfp4_gemm."""
-    m, inter, k, act, workspace = _gated_operands(a, sfa, b, sfb, alpha, activation, workspace)
+    m, inter, k, act, workspace = _gated_operands(a, sfa, b, sfb, alpha, activation, workspace, stream)
     if h is None:
         h = a.new_empty((m, inter), dtype=torch.bfloat16)
     else:
@@ -390,7 +407,7 @@ def nvfp4_gated_gemm_backward(a, sfa, b, sfb, alpha, dh, activation: str = "silu
 
     Returns (dgu, h): dgu bf16 [m, 2 inter] in the row order of b, and the forward result, both
     computed again from the packed operands."""
-    m, inter, k, act, workspace = _gated_operands(a, sfa, b, sfb, alpha, activation, workspace)
+    m, inter, k, act, workspace = _gated_operands(a, sfa, b, sfb, alpha, activation, workspace, stream)
     _need(dh, torch.bfloat16, "dh", 2)
     if tuple(dh.shape) != (m, inter):
         raise ValueError(f"dh must have shape {(m, inter)}, got {tuple(dh.shape)}")
