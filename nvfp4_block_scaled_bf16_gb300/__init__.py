@@ -206,18 +206,20 @@ _ws_cache: dict = {}
 
 
 def _default_workspace(nbytes: int, device: torch.device, stream) -> torch.Tensor:
-    """A workspace for a product that was given none: one zeroed buffer per device, grown on demand.  Calls on
-    streams that may overlap must pass their own.  A call under graph capture gets a buffer of the
-    graph's, zeroed by every replay: the shared one is dropped when it grows, and was filled outside the graph."""
+    """A workspace for a product that was given none: one zeroed buffer per device and launch stream, grown
+    on demand.  It is made on that stream, so its zero fill comes before the kernel and what it
+    replaces is not handed out before the stream is done with it.  A call under graph capture gets a
+    buffer of the graph's, zeroed by every replay."""
     if _capturing(stream):
         with _on(stream):
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
             ws[:4096].zero_()      # the counters, one per split tile (at most one tile per two SMs); partials need no zero
             return ws
-    ws = _ws_cache.get(device)
+    key = (device, _stream(stream))
+    ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = gemm_workspace(nbytes, device)
-        _ws_cache[device] = ws
+        with _on(stream):
+            ws = _ws_cache[key] = gemm_workspace(nbytes, device)
     return ws
 
 
@@ -264,7 +266,7 @@ def nvfp4_gemm(a, sfa, b, sfb, alpha, d=None, flags: int = 0, stream=None, works
     """D[m, n] = bf16(alpha * deq(a) @ deq(b)^T); a [m, k/2], b [n, k/2] packed uint8.
 
     workspace: zero-filled uint8 CUDA tensor of at least gemm_workspace_size(m, n, k) bytes
-    (the library leaves it zero after each call); None uses a per-device shared one."""
+    (the library leaves it zero after each call); None uses one that the calls on a stream share."""
     _need(a, torch.uint8, "a", 2)
     _need(b, torch.uint8, "b", 2)
     _need(sfa, torch.uint8, "sfa")

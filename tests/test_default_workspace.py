@@ -111,6 +111,30 @@ def test_a_captured_call_has_a_buffer_of_its_own(fake, gated):
     assert gemm(fake, gated)[2] is eager
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_each_stream_has_a_buffer_made_on_it(fake, gated):
+    """Zeroed on the launch stream whichever is current, kept for that stream alone, replaced when it is too small."""
+    side = FakeStream(5)
+    kept = {}
+    for by_argument in (True, False):
+        if by_argument:
+            stream, made, ws = gemm(fake, gated, side)
+        else:
+            with torch.cuda.stream(side):
+                stream, made, ws = gemm(fake, gated)
+        assert stream == made == 5 and not ws.any()
+        assert kept.setdefault(5, ws) is ws
+    stream, made, ws = gemm(fake, gated, 6)                       # a raw handle
+    assert stream == made == 6 and not ws.any() and ws is not kept[5]
+    stream, made, ws = gemm(fake, gated)
+    assert stream == made == 0 and not ws.any() and ws is not kept[5]
+    fake.log.need = 8192
+    stream, made, larger = gemm(fake, gated, side)
+    assert stream == made == 5 and larger is not kept[5] and not larger.any()
+    fake.log.need = 512
+    assert gemm(fake, gated, side)[2] is larger and gemm(fake, gated)[2] is ws
+
+
 @pytest.fixture(scope="module")
 def nv():
     import __graft_entry__
@@ -161,3 +185,25 @@ def test_a_graph_outlives_the_shared_buffer(nv, warm):
         assert torch.equal(nv.nvfp4_gemm(*b), want_large) and torch.equal(nv.nvfp4_gemm(*a), want)
     assert all(bool((t == 0xFF).all()) for t in junk)
     nv.check_status()
+
+
+@pytest.mark.gpu
+def test_first_calls_on_side_streams(nv):
+    """The first calls without a workspace, on streams that run beside a busy current one and beside each other."""
+    a, b = operands(SMALL), operands(SMALL, 3)
+    wants = explicit(nv, SMALL, a), explicit(nv, SMALL, b)
+    nv._ws_cache.clear()
+    x = torch.randn(4096, 4096, device="cuda")
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [[torch.empty_like(w) for _ in range(8)] for w in wants]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        x = x @ x * 0.01
+    for i in range(8):
+        for s, args, out in zip(streams, (a, b), outs):
+            nv.nvfp4_gemm(*args, out[i], stream=s)
+    torch.cuda.synchronize()
+    nv.check_status()
+    for want, out in zip(wants, outs):
+        assert all(torch.equal(d, want) for d in out)
+    assert len(nv._ws_cache) == 2 and not any(bool(ws[:256].any()) for ws in nv._ws_cache.values())
