@@ -332,33 +332,31 @@ __device__ __forceinline__ void gated_chunks(const GemmArgs &p, const Tile &t, u
   }
 }
 
-// The gated epilogue where operand A is the weight: one token, `N` neighbouring gate rows and their
+// The gated epilogue where operand A is the weight: one token, four neighbouring gate rows and their
 // up rows; wr is the first gate row in the interleaved weight.
-template <int EPI, int N>
-__device__ __forceinline__ void gated_col_units(const GemmArgs &p, int64_t token, int64_t wr, const float (&g)[N],
-                                                const float (&u)[N], float a0, float a1) {
+template <int EPI>
+__device__ __forceinline__ void gated_col_units(const GemmArgs &p, int64_t token, int64_t wr, const float (&g)[4],
+                                                const float (&u)[4], float a0, float a1) {
   const int64_t hc = ((wr >> 5) << 4) + (wr & 15);
-  float f[N], df[N], uu[N];
+  float f[4], df[4], uu[4];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < 4; ++i) {
     gate_act(p, a0 * g[i], f[i], df[i]);
     uu[i] = a1 * u[i];
   }
-  auto store = [](__nv_bfloat16 *dst, const float (&v)[N]) {
-    if constexpr (N == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    else
-      for (int i = 0; i < N; ++i) dst[i] = __float2bfloat16_rn(v[i]);
+  auto store = [](__nv_bfloat16 *dst, const float (&v)[4]) {
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   };
-  float hv[N];
+  float hv[4];
 #pragma unroll
-  for (int i = 0; i < N; ++i) hv[i] = f[i] * uu[i];
+  for (int i = 0; i < 4; ++i) hv[i] = f[i] * uu[i];
   if constexpr (EPI == kEpiGated) {
     store(p.d + token * p.ldd + hc, hv);
   } else {
-    float gv[N], uv[N];
+    float gv[4], uv[4];
     const __nv_bfloat16 *dh = p.dh + token * p.ldh + hc;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const float d = __bfloat162float(dh[i]);
       gv[i] = d * uu[i] * df[i];
       uv[i] = d * f[i];
@@ -856,7 +854,7 @@ __device__ __forceinline__ void reduce_read_gated(const GemmArgs &p, const TileI
         v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
       }
       const int c = u >> 4, r0 = ((u >> 2) & 3) * 32 + (u & 3) * 4;
-      if (r0 < t.rows) gated_col_units<EPI, 4>(p, t.out_j0 + c, t.out_i0 + r0, v[0], v[1], a0, a1);
+      if (r0 < t.rows) gated_col_units<EPI>(p, t.out_j0 + c, t.out_i0 + r0, v[0], v[1], a0, a1);
     }
   }
 }
@@ -1693,7 +1691,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
               const int c = u / 32, r0 = (u % 32) * 4;
               if (r0 < t.rows) {
                 const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {x.x, x.y, x.z, x.w};
-                gated_col_units<EPI, 4>(p, t.out_j0 + c, t.out_i0 + r0, gv, uv, alpha, alpha1);
+                gated_col_units<EPI>(p, t.out_j0 + c, t.out_i0 + r0, gv, uv, alpha, alpha1);
               }
             }
           } else

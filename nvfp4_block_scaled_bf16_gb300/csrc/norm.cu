@@ -1043,9 +1043,13 @@ Shape shape_of(int64_t n_pad, int vpt_pref) {
 
 template <typename XT, bool VEC, bool QUANT, int MAXT>
 auto forward_block(int vpt) {
-  if constexpr (MAXT > 512)  // (more than 512 threads of two vectors each come before four vectors)
+  if constexpr (MAXT > 512) {  // (more than 512 threads of two vectors each come before four vectors)
     if (vpt == 4) return norm_kernel<XT, 4, VEC, false, QUANT, MAXT>;
-  return vpt == 1 ? norm_kernel<XT, 1, VEC, false, QUANT, MAXT> : norm_kernel<XT, 2, VEC, false, QUANT, MAXT>;
+    if (vpt == 2) return norm_kernel<XT, 2, VEC, false, QUANT, MAXT>;
+  } else if constexpr (VEC && sizeof(XT) == 4) {  // (two vectors: forward_vpt)
+    if (vpt == 2) return norm_kernel<XT, 2, VEC, false, QUANT, MAXT>;
+  }
+  return norm_kernel<XT, 1, VEC, false, QUANT, MAXT>;
 }
 template <typename XT, bool VEC, bool QUANT>
 auto forward_kernel(const Shape &s) {
@@ -1081,6 +1085,9 @@ struct RingShape {
   bool use;
   int vpt, threads, per_sm, slots;
 };
+// Two slots for each block of an SM, or no ring.  All widths have them but the widest rows of an fp32 stream with a
+// gate per token (a slot of x, y and gate is 8 bytes a channel, with dh and dx_out 14): 7040 to 7168 channels
+// forward, where two blocks share the SM, and from 8152 on backward.
 RingShape ring_slots(RingShape s, int slot) {
   s.slots = (kSmemBudget / s.per_sm - kRingHead - 3 * 1024) / slot;
   if (s.slots > kMaxSlots) s.slots = kMaxSlots;
@@ -1165,9 +1172,9 @@ static bool forward_ring(const NormArgs &a, bool f32, bool pdl, cudaStream_t str
   return true;
 }
 
-// (Rows of single channels: one always, 1024 x 8191 63 -> 43 us.)
-// One vector a thread while the rows are few (the call waits for one row's latency: 7168 channels,
-// one row), two from four rows an SM on (fewer, wider threads: more bytes in flight per warp).
+// Vectors a thread in the plain forward kernel, aligned rows: one while the rows are few (the call waits for one
+// row's latency), two from four rows an SM on (fewer, wider threads: more bytes in flight per warp).  Many rows
+// of up to 8192 channels go to the ring, so this decides for the one width that it does not hold (ring_slots).
 static int forward_vpt(int64_t m, int64_t n, int sm_count) { return m >= 4LL * sm_count && n > 2048 ? 2 : 1; }
 
 extern "C" nvfp4_status_t block_norm(const void *x, int x_type, int64_t ldx, const void *y, int64_t ldy,
@@ -1189,6 +1196,7 @@ extern "C" nvfp4_status_t block_norm(const void *x, int x_type, int64_t ldx, con
   const int xe = elem_of(x_type);
   const bool vec = n % 8 == 0 && rows_aligned(x, ldx, xe) && rows_aligned(y, ldy, 2) && rows_aligned(gate, ldg, 2) &&
                    rows_aligned(x_out, ldxo, xe) && rows_aligned(h, ldh, 2) && aligned(w_post, 16) && aligned(w_pre, 16);
+  // (rows of single channels: one vector a thread where they fit, 1024 x 8191 63 -> 43 us)
   const Shape s = shape_of(n, vec ? forward_vpt(m, n, dev.sm_count) : 1);
   NormArgs a{x, ldx, (const __nv_bfloat16 *)y, ldy, (const __nv_bfloat16 *)w_post, (const __nv_bfloat16 *)w_pre,
              (const __nv_bfloat16 *)gate, ldg, residual_scale, eps, weight_offset, x_out, ldxo, (__nv_bfloat16 *)h, ldh,
