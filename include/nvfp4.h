@@ -250,7 +250,8 @@ nvfp4_status_t nvfp4_gemm_noalloc(const uint8_t *a, const uint8_t *sfa, const ui
  * with A, Bg and Bu the dequantised operands, fp32 sums, and act
  *   NVFP4_ACT_SILU       g / (1 + exp(-g))
  *   NVFP4_ACT_GELU_TANH  g/2 * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
- * (fp32, approximate exponential and reciprocal, a few fp32 ulps; one rounding, at the end).
+ * (fp32; approximate exponential and reciprocal: 1 / (1 + exp(-q)) is within 2^-15 of itself, and 0 where
+ * exp(-q) passes 2^126; one rounding, at the end).  NaN products give NaN in h and in every gradient they enter.
  * The pages fuse the activation with the quantiser after the product ([vLLM-SM103] ops.h,
  * silu_and_mul_scaled_fp4_experts_quant); here it is the product's epilogue, so the [m, 2 inter]
  * pre-activations never reach memory.
@@ -431,8 +432,9 @@ nvfp4_status_t block_norm(const void *x, int x_type, int64_t ldx, const void *y,
                           uint32_t flags, nvfp4_stream_t stream);
 
 /* block_norm whose h goes out as NVFP4, ready for nvfp4_gemm: q and sf equal nvfp4_quantize of
- * block_norm's h under global scale gs, bit for bit (scale rows up to the next multiple of 128 are
- * zeroed).  n % 16 == 0; every row of x, y, gate and x_out, the weights and sf on 16 bytes. */
+ * block_norm's h under global scale gs, bit for bit, for an h whose rows start on 16 bytes too (other rows
+ * are computed with their sums in another order); scale rows up to the next multiple of 128 are
+ * zeroed.  n % 16 == 0; every row of x, y, gate and x_out, the weights and sf on 16 bytes. */
 nvfp4_status_t block_norm_quantize(const void *x, int x_type, int64_t ldx, const void *y, int64_t ldy,
                                    const void *w_post, const void *gate, int64_t ldg, const void *w_pre,
                                    float residual_scale, float eps, float weight_offset, void *x_out, int64_t ldxo,

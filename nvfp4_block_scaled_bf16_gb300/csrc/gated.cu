@@ -2,8 +2,9 @@
 // the dense NVFP4 GEMM kernel (gemm.cuh) with another epilogue.
 //
 // The weight's rows alternate between 16 gate and 16 up rows, so that both products of an element of
-// h meet in one tile: 32 neighbouring columns held by one thread where tokens fill the MMA's rows,
-// lanes l and l + 16 of a warp (or units u and u + 4 of a split-K partial) where the weight does.
+// h meet in one tile: 32 neighbouring columns held by one thread where tokens fill the MMA's rows (and, turned
+// around through shared memory, where the weight does and K is not split), units u and u + 4 of a split-K
+// partial otherwise.
 // The activation and the product are then taken on the fp32 accumulators and h is rounded once;
 // neither product ever reaches memory.  The plans, pipelines and split reductions are the plain
 // GEMM's.  The backward pass computes both products again from the packed operands (reading

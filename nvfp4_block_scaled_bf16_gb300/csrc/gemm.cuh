@@ -39,7 +39,7 @@
 // EPI: instead of bf16(alpha * C), the epilogue may make the gated product of a feed-forward block of a
 // tile, or its gradient (gated.cu): operand rows alternate between 16 gate and 16 up rows, so both
 // products of an output meet in one thread (32 columns of a row), in one warp (a weight-side tile
-// without a split, turned around through shared memory) or in one unit of a split tile's reduction.
+// without a split, turned around through shared memory) or in one thread of a split tile's reduction.
 //
 // CTA pairs (PAIR, 256 x 256 tiles for large M): a cluster of two CTAs runs cta_group::2 MMAs
 // (M = 256, issued by the first CTA; a 256x256x64 MMA occupies the pipe for the same ~128 cycles
@@ -1522,8 +1522,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
         } else if (row < t.rows) {
           // operand A is the weight: TMEM lane = output column, TMEM column = output row
           if constexpr (EPI != kEpiPlain) {
-            // 32 weight rows (16 gate, 16 up) x 32 tokens: turned around through this warp's 4 KB of the
-            // idle ring, so that a lane holds a token's 32 columns and stores whole vectors (valid rows
+            // 32 weight rows (16 gate, 16 up) x 32 tokens: turned around through this warp's 4224 bytes of
+            // the idle ring, so that a lane holds a token's 32 columns and stores whole vectors (valid rows
             // come in whole warps).  With single elements instead, two bytes a store, 128 x 14336 x 4096
             // took 26.1 us, its backward pass 78.9.
             float *turn = reinterpret_cast<float *>(smem) + quad * (32 * 33);

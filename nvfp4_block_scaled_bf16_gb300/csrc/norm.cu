@@ -1087,7 +1087,8 @@ struct RingShape {
 };
 // Two slots for each block of an SM, or no ring.  All widths have them but the widest rows of an fp32 stream with a
 // gate per token (a slot of x, y and gate is 8 bytes a channel, with dh and dx_out 14): 7040 to 7168 channels
-// forward, where two blocks share the SM, and from 8152 on backward.
+// forward, where two blocks share the SM, and from 8152 on backward.  (Forward it costs nothing: 1024 x 7168 23.8 us
+// by norm_kernel, 1024 x 7032 26.6 by the ring.)
 RingShape ring_slots(RingShape s, int slot) {
   s.slots = (kSmemBudget / s.per_sm - kRingHead - 3 * 1024) / slot;
   if (s.slots > kMaxSlots) s.slots = kMaxSlots;

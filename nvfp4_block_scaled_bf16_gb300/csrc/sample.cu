@@ -10,8 +10,8 @@
 // and the first token always stays.  The token drawn is the first one, by index, at which the kept
 // tokens' cumulative weight exceeds floor(u * total).  Sums of whole numbers are exact in any
 // order, so the token depends neither on how a row is split over CTAs and threads nor on the order of
-// atomics.  (A weight below 2^-31 of the largest is zero; 2^21 tokens of weight 2^30 stay below 2^53,
-// so the products with p and u are taken in fp64 without losing a unit.)
+// atomics.  (A weight below 2^-31 of the largest is zero; 2^21 tokens of weight 2^30 stay below 2^53, so a total is
+// exact in fp64, and its products with p and u are rounded once.)
 //
 // No sort of the row.  A cluster of 1 to 8 CTAs owns a row; each of its warps owns a contiguous piece:
 //   1. the row's maximum (and the largest logits of each thread's two heaviest vectors);
@@ -29,7 +29,8 @@
 //   5. the kept weight and the ties of every piece, from the weight above and the lists; then the piece
 //      that the random number falls in is split over its CTA's warps, and one of them walks its
 //      part to the token.
-// Where the bracket is missed or a list overflows (equal logits, k or p near the end of a flat row) the
+// Where the bracket is missed or a list overflows (equal logits, k or p near the end of a flat row, top-p over
+// 131072 and more fp32 logits in one CTA: a list holds half as many of them) the
 // cut is found from the row itself: counts and weights of 1024 classes of -x, then splits of the class
 // down to a single key if need be (a row of equal logits), with a pass over the row each, and one more
 // pass for 5.  Both ways give the same cut.  Without top-k and top-p only 1 and 5 run, from the row.

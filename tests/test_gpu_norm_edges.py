@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_block_norm as common
 from oracle import block
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +104,22 @@ def test_backward_without_the_norm_after_the_block(nv, m, n, gate, stream):
         for r, c in at:
             same[r, c] = False
         assert torch.equal(got[4][same], want[4][same]) and not torch.isfinite(got[4][~same].float()).any()
+
+
+@pytest.mark.parametrize("m,n", [(620, 7168), (609, 7040), (608, 8192), (610, 8152)])
+def test_rows_too_wide_to_be_copied_ahead(nv, m, n):
+    """An fp32 stream with a gate per token: at 7040 to 7168 channels forward and from 8152 on backward two rows do not
+    fit beside each other, and the plain kernels take many rows too."""
+    d = common.inputs(m, n, torch.float32, True, "token")
+    kw = dict(y=d["y"], w_post=d["w_post"], gate=d["gate"], residual_scale=0.7)
+    x_out, h = nv.block_norm(d["x"], d["w_pre"], eps=common.EPS, **kw)
+    r_ref, h_ref = block.block_norm(f64(d["x"]), f64(d["w_pre"]), f64(d["y"]), f64(d["w_post"]), f64(d["gate"]), 0.7, common.EPS)
+    tr, th = common.forward_terms(d, 0.7, 0.0)
+    common.check(x_out, r_ref, 2.0 ** -23, tr, "x_out")
+    common.check(h, h_ref, BF16, th, "h")
+    if n % 16 == 0:
+        gs = (2688.0 / h.float().abs().max()).reshape(1)
+        q_ref, sf_ref = nv.nvfp4_quantize(h, gs)
+        x2, q, sf = nv.block_norm_quantize(d["x"], d["w_pre"], gs, eps=common.EPS, **kw)
+        assert torch.equal(x2, x_out) and torch.equal(q, q_ref) and torch.equal(sf, sf_ref)
+    common.check_backward(nv, d, 0.7, 0.0)
