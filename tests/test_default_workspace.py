@@ -207,3 +207,19 @@ def test_first_calls_on_side_streams(nv):
     for want, out in zip(wants, outs):
         assert all(torch.equal(d, want) for d in out)
     assert len(nv._ws_cache) == 2 and not any(bool(ws[:256].any()) for ws in nv._ws_cache.values())
+
+
+@pytest.mark.gpu
+def test_captured_calls_launched_with_pdl(nv):
+    """The fill of a graph's buffer lies between two kernels that may otherwise overlap."""
+    a = operands(SMALL)
+    want = explicit(nv, SMALL, a)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [nv.nvfp4_gemm(*a, flags=nv.FLAG_PDL) for _ in range(3)]
+    for _ in range(3):
+        for d in outs:
+            d.zero_()
+        graph.replay()
+        assert all(torch.equal(d, want) for d in outs)
+    nv.check_status()
