@@ -491,6 +491,106 @@ nvfp4_status_t sample_tokens(const void *logits, int logits_type, int64_t ld, co
                              int32_t *tokens, float *logprobs, int64_t rows, int64_t vocab, uint32_t flags,
                              nvfp4_stream_t stream);
 
+/* ---- 8-bit products scaled per block of 128, and what an expert layer trains with ----
+ *
+ * e4m3 quantisation with one fp32 scale per block of 128.  A block whose largest magnitude is amax
+ * (taken as at least 2^-100) gets
+ *   s = fl(amax / 448),  codes e4m3(fl(x * fl(448 / amax)))  (RNE, saturating)
+ * with fl one rounding to fp32, so that a code times s stands for x within 2^-4 of x where |x| is
+ * at least amax * 2^-6 / 448, and within amax / 448 * 2^-10 below.  A block that holds an infinity or a NaN
+ * comes back as no finite number.  The sources quantise to 4 bits only; this is the 8-bit counterpart
+ * of nvfp4_quantize, with blocks of the usual 128.
+ *   x           bf16 or fp32 (x_type: NVFP4_DTYPE_*) [x_rows, k], row stride ldx >= k or 0 (one row for all);
+ *               k % 16 == 0,
+ *               every row starts on 16 bytes
+ *   src_rows    int32 [rows] or NULL: row r of the result is row src_rows[r] of x (without it rows ==
+ *               x_rows).  An entry outside [0, x_rows) quantises zeros and makes nvfp4_check_status
+ *               report NVFP4_ERR_INVALID_ARG.
+ *   q, sf       along the rows: e4m3 [rows, k], fp32 [ceil(k/128), rows]: one scale per row and
+ *               128 columns (a block of columns' scales lie together), or both NULL
+ *   qt, sft     along the columns, transposed: e4m3 [k, P], fp32 [P/128, k] with
+ *               P = fp8_padded_rows(rows, num_experts): one scale per column and 128 rows, or both NULL.
+ *               Columns past the last row hold zeros.
+ *   row_offsets int64 [num_experts+1] on the device (as moe_sort_by_expert writes it; its last entry
+ *               may be below rows) or NULL with num_experts 0.  Expert e's rows begin at column
+ *               sum_{j<e} round_up(M_j, 128) of qt, so that no block spans two experts; rows past the last
+ *               expert's are not quantised (q and sf stay as they were there).  Needs qt.  Malformed
+ *               offsets: the columns of qt are zeros and nvfp4_check_status reports
+ *               NVFP4_ERR_INVALID_ARG.
+ *   q and qt 16-B aligned; 1 <= num_experts <= 1024; rows, k <= 2^31 - 512, k <= 2^23.
+ * x is read once for both. */
+int64_t fp8_padded_rows(int64_t rows, int num_experts); /* round_up(rows, 128) + 128 * num_experts */
+nvfp4_status_t fp8_quantize(const void *x, int x_type, int64_t x_rows, int64_t k, int64_t ldx, const int32_t *src_rows,
+                            int64_t rows, const int64_t *row_offsets, int num_experts, uint8_t *q, float *sf, uint8_t *qt,
+                            float *sft, uint32_t flags, nvfp4_stream_t stream);
+
+/* The same for weights, one scale per 128 x 128 block.
+ *   w       bf16 or fp32 [matrices, n, k], row stride ldw (matrix stride n * ldw), k % 16 == 0,
+ *           every row starts on 16 bytes
+ *   q, sf   e4m3 [matrices, n, k], fp32 [matrices, ceil(n/128), ceil(k/128)]
+ *   qt, sft the transposes, e4m3 [matrices, k, n] and fp32 [matrices, ceil(k/128), ceil(n/128)]: the same
+ *           codes and scales, for the gradient of the product's input; or both NULL.  n % 16 == 0 with them. */
+nvfp4_status_t fp8_quantize_weight(const void *w, int w_type, int64_t matrices, int64_t n, int64_t k, int64_t ldw, uint8_t *q,
+                                   float *sf, uint8_t *qt, float *sft, uint32_t flags, nvfp4_stream_t stream);
+
+/* Product of two such matrices:
+ *   D[i, j] = sum over blocks b of sa[i, b] * sb[j, b] * (sum over the block's k of A[i, k] B[j, k])
+ * The sums inside a block are the tensor core's, the scaled sums over the blocks fp32; one rounding to
+ * D's type at the end.
+ *   a, sfa   e4m3 [m, k] and fp32 [ceil(k/128), m], as fp8_quantize's q and sf
+ *   b, sfb   e4m3 [n, k]; block_b = 128: fp32 [ceil(n/128), ceil(k/128)] (fp8_quantize_weight);
+ *            block_b = 1: fp32 [ceil(k/128), n] (fp8_quantize)
+ *   d        bf16 or fp32 (d_type) [m, n];  accumulate != 0: D is added to (fp32 only)
+ *   a, b and d 16-B aligned, the scales 4-B; k % 16 == 0, any m and n.
+ * Gradients with the same call: of the input, fp8_gemm(dY, W^T) with W's qt and sft; of the weight,
+ * fp8_gemm(dY^T, X^T) with block_b = 1 and both operands from qt and sft.
+ * Every operand is read after the PDL wait.  Results do not depend on timing.  No workspace. */
+nvfp4_status_t fp8_gemm(const uint8_t *a, const float *sfa, const uint8_t *b, const float *sfb, int block_b, void *d,
+                        int d_type, int accumulate, int64_t m, int64_t n, int64_t k, uint32_t flags, nvfp4_stream_t stream);
+
+/* The product of every expert's rows with its weight: D[rows of e, :] = A_e B_e^T, scaled as fp8_gemm with
+ * block_b = 128.
+ *   a, sfa       e4m3 [t, k] (rows sorted by expert), fp32 [ceil(k/128), t]
+ *   row_offsets  DEVICE int64 [num_experts+1]: 0 first, non-decreasing, the last at most t.  Rows of D past
+ *                the last expert's stay as they were.  Malformed offsets: no work, and
+ *                nvfp4_check_status reports NVFP4_ERR_INVALID_ARG.
+ *   b, sfb       e4m3 [num_experts, n, k], fp32 [num_experts, ceil(n/128), ceil(k/128)]
+ *   d            bf16 or fp32 [t, n]
+ * 1 <= num_experts <= 1024, num_experts * n < 2^31; otherwise as fp8_gemm. */
+nvfp4_status_t fp8_grouped_gemm(const uint8_t *a, const float *sfa, const int64_t *row_offsets, int num_experts,
+                                const uint8_t *b, const float *sfb, void *d, int d_type, int64_t t, int64_t n, int64_t k,
+                                uint32_t flags, nvfp4_stream_t stream);
+
+/* The gradient of every expert's weight: D[e] = A_e^T B_e over the expert's rows, with A the gradient of
+ * the product's output and B its input, both as fp8_quantize's qt and sft under the same row_offsets:
+ *   a, sfa       e4m3 [n, P], fp32 [P/128, n];  b, sfb  e4m3 [k, P], fp32 [P/128, k]
+ *   padded_rows  P, a multiple of 128 with room for every expert's padded rows (fp8_padded_rows)
+ *   d            bf16 or fp32 (d_type) [num_experts, n, k];  accumulate != 0: D is added to (fp32 only).
+ *                An expert without rows gets zeros (with accumulate: stays).
+ * any n and k; otherwise as fp8_grouped_gemm. */
+nvfp4_status_t fp8_grouped_weight_grad(const uint8_t *a, const float *sfa, const uint8_t *b, const float *sfb,
+                                       const int64_t *row_offsets, int num_experts, void *d, int d_type, int accumulate,
+                                       int64_t padded_rows, int64_t n, int64_t k, uint32_t flags, nvfp4_stream_t stream);
+
+/* Backward pass of moe_combine: with dout the gradient of its result,
+ *   dy[pos[t, j], :]  = bf16(weights[t, j] * dout[t, :])
+ *   dweights[t, j]    = sum_c dout[t, c] * y[pos[t, j], c]     (fp32; 0 where pos[t, j] < 0)
+ *   dout  bf16 [num_tokens, h], row stride ldo >= h or 0 (one row for all), ldo % 8 == 0;  y, dy  bf16 [rows, h];  16-B aligned, h % 8 == 0
+ *   pos   int32 [num_tokens, topk], as moe_sort_by_expert writes it: no row twice (the rows of dy that are named
+ *         are each written by their slot, the others stay as they were).  An entry >= rows is skipped as
+ *         one < 0 is, and makes nvfp4_check_status report NVFP4_ERR_INVALID_ARG.
+ *   Inputs and outputs must not overlap. */
+nvfp4_status_t moe_combine_backward(const void *dout, int64_t ldo, const void *y, int64_t rows, const int32_t *pos,
+                                    const float *weights, int64_t num_tokens, int topk, int64_t h, void *dy, float *dweights,
+                                    uint32_t flags, nvfp4_stream_t stream);
+
+/* Backward pass of moe_gather_rows under moe_sort_by_expert's src_rows: dx[t, :] = bf16(sum_j dxs[pos[t, j], :])
+ * in fp32, slots in order.
+ *   dxs  bf16 [rows, h], the gradient of the gathered rows;  dx  bf16 [num_tokens, h];  16-B aligned, h % 8 == 0
+ *   pos  as above (entries < 0 add nothing; a row may be named more than once). */
+nvfp4_status_t moe_gather_backward(const void *dxs, int64_t rows, const int32_t *pos, int64_t num_tokens, int topk, int64_t h,
+                                   void *dx, uint32_t flags, nvfp4_stream_t stream);
+
 /* Scale layout conversion between a row-major scale matrix [rows, cols] (bytes) and the
  * 128x4 swizzled layout of nvfp4_sf_bytes size (swizzle writes the zero padding).
  * Source: [vLLM-SM103] nvfp4_utils.py swizzle_blockscale (pad to (128,4), then block

@@ -9,6 +9,7 @@ libnvfp4.so is missing (build it with ``python nvfp4_block_scaled_bf16_gb300/bui
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -71,6 +72,14 @@ _SIGS = {
     "block_norm_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _f32, _f32,
                                    _f32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _u32, _vp]),
     "sample_tokens": (_int, [_vp, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _u32, _vp]),
+    "fp8_padded_rows": (_i64, [_i64, _int]),
+    "fp8_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _int, _vp, _vp, _vp, _vp, _u32, _vp]),
+    "fp8_quantize_weight": (_int, [_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _u32, _vp]),
+    "fp8_gemm": (_int, [_vp, _vp, _vp, _vp, _int, _vp, _int, _int, _i64, _i64, _i64, _u32, _vp]),
+    "fp8_grouped_gemm": (_int, [_vp, _vp, _vp, _int, _vp, _vp, _vp, _int, _i64, _i64, _i64, _u32, _vp]),
+    "fp8_grouped_weight_grad": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _int, _int, _i64, _i64, _i64, _u32, _vp]),
+    "moe_combine_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _int, _i64, _vp, _vp, _u32, _vp]),
+    "moe_gather_backward": (_int, [_vp, _i64, _vp, _i64, _int, _i64, _vp, _u32, _vp]),
     "nvfp4_check_status": (_int, [_vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -173,6 +182,11 @@ def _scratch(nbytes: int, device, stream):
         return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
     with _on(stream):
         return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+
+
+def _on_made(stream):
+    """A context for outputs that are made for the launch stream: their memory then belongs to it (see _contig)."""
+    return contextlib.nullcontext() if stream is None else _on(stream)
 
 
 def sf_bytes(rows: int, k: int, sf_vec: int = 16) -> int:
@@ -823,6 +837,241 @@ def sample_tokens(logits, uniform, temperature=None, top_k=None, top_p=None, min
     _check(_lib.sample_tokens(_ptr(logits), lt, ld, _ptr(uniform), _ptr(temperature), _ptr(top_k),
                               _ptr(top_p), _ptr(min_p), _ptr(tokens), _ptr(logprobs), rows, vocab, flags, _stream(stream)))
     return tokens, logprobs
+
+
+# ---------------------------------------------------------------- 8-bit products with a scale per block of 128
+E4M3 = torch.float8_e4m3fn
+
+
+def _type_of(t, name):
+    """NVFP4_DTYPE_* of a bf16 or fp32 tensor."""
+    xt = _STREAM_TYPES.get(t.dtype)
+    if xt is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return xt
+
+
+def _dense(t, dtype, name, shape):
+    """A contiguous tensor of this shape on the current device."""
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _made(t, dtype, name, shape, like):
+    """The output tensor `t`, or a new one."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    _dense(t, dtype, name, shape)
+    return t
+
+
+def fp8_padded_rows(rows: int, experts: int = 0) -> int:
+    """Columns of fp8_quantize's transposed codes: round_up(rows, 128) + 128 * experts."""
+    return int(_lib.fp8_padded_rows(rows, experts))
+
+
+def fp8_quantize(x, src_rows=None, row_offsets=None, rows: bool = True, transpose: bool = False, q=None, sf=None, qt=None,
+                 sft=None, flags: int = 0, stream=None):
+    """e4m3 codes of x (bf16 or fp32 [n, k], k % 16 == 0) with one fp32 scale per block of 128.
+
+    Along the rows (rows=True): q [m, k], sf [ceil(k/128), m].  Along the columns and transposed
+    (transpose=True): qt [k, P], sft [P/128, k] with P = fp8_padded_rows(m, experts); with row_offsets (int64
+    [E+1]) each expert's rows begin at a multiple of 128 there.  src_rows (int32 [m]): row r of the result is
+    x[src_rows[r]] (without it m = n).  Returns (q, sf), (qt, sft) or (q, sf, qt, sft); x is read once."""
+    _check_device(x, "x")
+    xt = _type_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must have 2 dimensions")
+    if not rows and not transpose:
+        raise ValueError("rows or transpose: one at least")
+    n, k = x.shape
+    ldx = _rows(x, x.dtype, "x", n, k, x.get_device())
+    m, experts = n, 0
+    if src_rows is not None:
+        _need(src_rows, torch.int32, "src_rows", 1)
+        if not src_rows.is_contiguous():
+            raise ValueError("src_rows must be contiguous")
+        m = src_rows.numel()
+    if row_offsets is not None:
+        if not transpose:
+            raise ValueError("row_offsets belong to transpose")
+        _need(row_offsets, torch.int64, "row_offsets", 1)
+        if not row_offsets.is_contiguous() or row_offsets.numel() < 2:
+            raise ValueError("row_offsets must be contiguous and hold at least two entries")
+        experts = row_offsets.numel() - 1
+    kb, out = -(-k // 128), ()
+    with _on_made(stream):
+        if rows:
+            q, sf = _made(q, E4M3, "q", (m, k), x), _made(sf, torch.float32, "sf", (kb, m), x)
+            out += (q, sf)
+        elif q is not None or sf is not None:
+            raise ValueError("q and sf belong to rows")
+        if transpose:
+            p = fp8_padded_rows(m, experts)
+            qt, sft = _made(qt, E4M3, "qt", (k, p), x), _made(sft, torch.float32, "sft", (p // 128, k), x)
+            out += (qt, sft)
+        elif qt is not None or sft is not None:
+            raise ValueError("qt and sft belong to transpose")
+    _check(_lib.fp8_quantize(_ptr(x), xt, n, k, ldx, _ptr(src_rows), m, _ptr(row_offsets), experts, _ptr(q), _ptr(sf),
+                             _ptr(qt), _ptr(sft), flags, _stream(stream)))
+    return out
+
+
+def fp8_quantize_weight(w, transpose: bool = False, q=None, sf=None, qt=None, sft=None, flags: int = 0, stream=None):
+    """e4m3 codes of one weight or several (bf16 or fp32 [n, k] or [E, n, k], contiguous rows) with one fp32 scale
+    per 128 x 128 block: (q, sf [.., ceil(n/128), ceil(k/128)]), and with transpose the same codes and scales
+    transposed: (q, sf, qt, sft)."""
+    _check_device(w, "w")
+    wt = _type_of(w, "w")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must have 2 or 3 dimensions")
+    n, k = w.shape[-2:]
+    lead = tuple(w.shape[:-2])
+    matrices = lead[0] if lead else 1
+    if lead:
+        if not w.is_contiguous():
+            raise ValueError("w must be contiguous")
+        ldw = k
+    else:
+        ldw = _rows(w, w.dtype, "w", n, k, w.get_device())
+    nb, kb = -(-n // 128), -(-k // 128)
+    with _on_made(stream):
+        q, sf = _made(q, E4M3, "q", lead + (n, k), w), _made(sf, torch.float32, "sf", lead + (nb, kb), w)
+        if transpose:
+            qt, sft = _made(qt, E4M3, "qt", lead + (k, n), w), _made(sft, torch.float32, "sft", lead + (kb, nb), w)
+        elif qt is not None or sft is not None:
+            raise ValueError("qt and sft belong to transpose")
+    _check(_lib.fp8_quantize_weight(_ptr(w), wt, matrices, n, k, ldw, _ptr(q), _ptr(sf), _ptr(qt), _ptr(sft), flags,
+                                    _stream(stream)))
+    return (q, sf, qt, sft) if transpose else (q, sf)
+
+
+def _product_out(d, out_dtype, accumulate, shape, like, stream):
+    """(d, its NVFP4_DTYPE_*)."""
+    if d is not None:
+        out_dtype = d.dtype
+    elif accumulate:
+        raise ValueError("accumulate needs d")
+    dt = _STREAM_TYPES.get(out_dtype)
+    if dt is None:
+        raise TypeError(f"the result must be bfloat16 or float32, got {out_dtype}")
+    with _on_made(stream):
+        return _made(d, out_dtype, "d", shape, like), dt
+
+
+def fp8_gemm(a, sfa, b, sfb, block_b: int = 128, out_dtype=torch.bfloat16, d=None, accumulate: bool = False, flags: int = 0,
+             stream=None):
+    """D[m, n] = deq(a) @ deq(b)^T; a [m, k] and b [n, k] e4m3, sfa fp32 [ceil(k/128), m] (fp8_quantize), sfb
+    fp32 [ceil(n/128), ceil(k/128)] (block_b=128, fp8_quantize_weight) or [ceil(k/128), n] (block_b=1,
+    fp8_quantize).  D is bf16 or fp32; accumulate adds to an fp32 d."""
+    _need(a, E4M3, "a", 2)
+    _need(b, E4M3, "b", 2)
+    m, k = a.shape
+    n = b.shape[0]
+    if b.shape[1] != k:
+        raise ValueError("a and b disagree on K")
+    if block_b not in (1, 128):
+        raise ValueError(f"block_b must be 1 or 128, got {block_b}")
+    kb = -(-k // 128)
+    _dense(a, E4M3, "a", (m, k))
+    _dense(b, E4M3, "b", (n, k))
+    _dense(sfa, torch.float32, "sfa", (kb, m))
+    _dense(sfb, torch.float32, "sfb", (-(-n // 128), kb) if block_b == 128 else (kb, n))
+    d, dt = _product_out(d, out_dtype, accumulate, (m, n), a, stream)
+    _check(_lib.fp8_gemm(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), block_b, _ptr(d), dt, int(accumulate), m, n, k, flags,
+                         _stream(stream)))
+    return d
+
+
+def fp8_grouped_gemm(a, sfa, row_offsets, b, sfb, out_dtype=torch.bfloat16, d=None, flags: int = 0, stream=None):
+    """Per expert e: D[rows of e] = deq(A_e) @ deq(B_e)^T; a e4m3 [t, k] with its rows sorted by expert (sfa
+    [ceil(k/128), t]), b e4m3 [E, n, k] (sfb [E, ceil(n/128), ceil(k/128)]), D bf16 or fp32.  Rows past the last
+    expert's stay as they were."""
+    _need(a, E4M3, "a", 2)
+    _need(b, E4M3, "b", 3)
+    _need(row_offsets, torch.int64, "row_offsets", 1)
+    t, k = a.shape
+    experts, n, kb_ = b.shape
+    if kb_ != k or row_offsets.numel() != experts + 1:
+        raise ValueError("shape mismatch")
+    kb = -(-k // 128)
+    _dense(a, E4M3, "a", (t, k))
+    _dense(b, E4M3, "b", (experts, n, k))
+    _dense(row_offsets, torch.int64, "row_offsets", (experts + 1,))
+    _dense(sfa, torch.float32, "sfa", (kb, t))
+    _dense(sfb, torch.float32, "sfb", (experts, -(-n // 128), kb))
+    d, dt = _product_out(d, out_dtype, False, (t, n), a, stream)
+    _check(_lib.fp8_grouped_gemm(_ptr(a), _ptr(sfa), _ptr(row_offsets), experts, _ptr(b), _ptr(sfb), _ptr(d), dt, t, n, k,
+                                 flags, _stream(stream)))
+    return d
+
+
+def fp8_grouped_weight_grad(a, sfa, b, sfb, row_offsets, out_dtype=torch.bfloat16, d=None, accumulate: bool = False,
+                            flags: int = 0, stream=None):
+    """Per expert e: D[e] = deq(a)[:, rows of e] @ deq(b)[:, rows of e]^T, the gradient of its weight; a e4m3 [n, P]
+    (of the output's gradient) and b e4m3 [k, P] (of the input) with sfa [P/128, n], sfb [P/128, k], as
+    fp8_quantize(transpose=True) gives them under the same row_offsets.  D [E, n, k] bf16 or fp32; accumulate adds
+    to an fp32 d."""
+    _need(a, E4M3, "a", 2)
+    _need(b, E4M3, "b", 2)
+    _need(row_offsets, torch.int64, "row_offsets", 1)
+    n, p = a.shape
+    k = b.shape[0]
+    if b.shape[1] != p:
+        raise ValueError("a and b disagree on the rows")
+    experts = row_offsets.numel() - 1
+    _dense(a, E4M3, "a", (n, p))
+    _dense(b, E4M3, "b", (k, p))
+    _dense(row_offsets, torch.int64, "row_offsets", (experts + 1,))
+    _dense(sfa, torch.float32, "sfa", (p // 128, n))
+    _dense(sfb, torch.float32, "sfb", (p // 128, k))
+    d, dt = _product_out(d, out_dtype, accumulate, (experts, n, k), a, stream)
+    _check(_lib.fp8_grouped_weight_grad(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(row_offsets), experts, _ptr(d), dt,
+                                        int(accumulate), p, n, k, flags, _stream(stream)))
+    return d
+
+
+# ---------------------------------------------------------------- gradients of the MoE steps
+def moe_combine_backward(dout, y, pos, weights, dy=None, dweights=None, flags: int = 0, stream=None):
+    """Gradients of moe_combine: (dy bf16 [rows, h], dweights fp32 [T, topk]) with dy[pos[t, j]] = weights[t, j] *
+    dout[t] and dweights[t, j] = dout[t] . y[pos[t, j]].  Rows of dy that no slot names stay as they were; no row
+    may be named twice (moe_sort_by_expert's pos names none twice)."""
+    _need(y, torch.bfloat16, "y", 2)
+    _need(pos, torch.int32, "pos", 2)
+    _need(weights, torch.float32, "weights", 2)
+    if not y.is_contiguous():
+        raise ValueError("y must be contiguous")
+    rows, h = y.shape
+    T, topk = pos.shape
+    ldo = _rows(dout, torch.bfloat16, "dout", T, h, y.get_device())
+    if tuple(weights.shape) != (T, topk):
+        raise ValueError(f"weights must have shape {(T, topk)}, got {tuple(weights.shape)}")
+    pos, weights = _contig(pos, stream), _contig(weights, stream)
+    with _on_made(stream):
+        dy = _made(dy, torch.bfloat16, "dy", (rows, h), y)
+        dweights = _made(dweights, torch.float32, "dweights", (T, topk), y)
+    _check(_lib.moe_combine_backward(_ptr(dout), ldo, _ptr(y), rows, _ptr(pos), _ptr(weights), T, topk, h, _ptr(dy),
+                                     _ptr(dweights), flags, _stream(stream)))
+    return dy, dweights
+
+
+def moe_gather_backward(dxs, pos, dx=None, flags: int = 0, stream=None):
+    """Gradient of moe_gather_rows under moe_sort_by_expert's src_rows: dx[t] = bf16(sum_j dxs[pos[t, j]]) (fp32, slot
+    order)."""
+    _need(dxs, torch.bfloat16, "dxs", 2)
+    _need(pos, torch.int32, "pos", 2)
+    if not dxs.is_contiguous():
+        raise ValueError("dxs must be contiguous")
+    rows, h = dxs.shape
+    T, topk = pos.shape
+    pos = _contig(pos, stream)
+    with _on_made(stream):
+        dx = _made(dx, torch.bfloat16, "dx", (T, h), dxs)
+    _check(_lib.moe_gather_backward(_ptr(dxs), rows, _ptr(pos), T, topk, h, _ptr(dx), flags, _stream(stream)))
+    return dx
 
 
 def check_status(stream=None) -> None:

@@ -1,0 +1,84 @@
+// e4m3 products scaled per block of 128: the dense entry point and its choice of tiles.
+#include "fp8_gemm.cuh"
+
+using namespace nvfp4;
+
+namespace {
+
+struct Call {
+  const char *name;
+  const uint8_t *a, *b;
+  int64_t m, n, k;
+  int block_b;
+  fp8::Args args;
+  const DeviceInfo *dev;
+  uint32_t flags;
+  nvfp4_stream_t stream;
+  const float *sfa, *sfb;
+};
+
+// Scales of one per row and block: [blocks along K][rows].  One per 128 rows: [blocks of rows][blocks along K].
+fp8::Scales row_scales(const float *p, int64_t rows) { return fp8::Scales{p, 0, 1, rows}; }
+fp8::Scales block_scales(const float *p, int64_t nk) { return fp8::Scales{p, 0, nk, 1}; }
+
+template <class C>
+nvfp4_status_t run(const Call &c) {
+  fp8::Args args = c.args;
+  const fp8::Scales sa = row_scales(c.sfa, c.m);
+  const fp8::Scales sb = c.block_b == 128 ? block_scales(c.sfb, args.nk) : row_scales(c.sfb, c.n);
+  const int64_t p = C::SWAP ? c.n : c.m, q = C::SWAP ? c.m : c.n;
+  args.sp = C::SWAP ? sb : sa;
+  args.sq = C::SWAP ? sa : sb;
+  args.p_rows = static_cast<int>(p);
+  args.q_rows = static_cast<int>(q);
+  args.p_tiles = static_cast<int>(ceil_div(p, 128 * C::CG));
+  args.q_tiles = static_cast<int>(ceil_div(q, C::NT));
+  const int64_t tiles = static_cast<int64_t>(args.p_tiles) * args.q_tiles;
+  if (tiles >= (1LL << 31)) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", c.name);
+  args.splits = 1;
+  if (C::SWAP) {
+    int64_t s = tiles > 0 ? c.dev->sm_count / tiles : 1;
+    if (s > 8) s = 8;
+    if (s > args.nk) s = args.nk;
+    args.splits = s < 1 ? 1 : static_cast<int>(s);
+  }
+  return fp8::launch_gemm<C>(c.name, C::SWAP ? c.b : c.a, p, C::SWAP ? c.a : c.b, q, c.k, tiles, args, *c.dev, c.flags,
+                             c.stream);
+}
+
+template <int NT>
+nvfp4_status_t run_swap(const Call &c) {
+  return c.block_b == 128 ? run<fp8::Cfg<NT, true, false, true, fp8::kDense>>(c)
+                          : run<fp8::Cfg<NT, true, true, true, fp8::kDense>>(c);
+}
+template <int NT, int CG>
+nvfp4_status_t run_rows(const Call &c) {
+  return c.block_b == 128 ? run<fp8::Cfg<NT, false, true, false, fp8::kDense, CG>>(c)
+                          : run<fp8::Cfg<NT, false, true, true, fp8::kDense, CG>>(c);
+}
+
+}  // namespace
+
+extern "C" nvfp4_status_t fp8_gemm(const uint8_t *a, const float *sfa, const uint8_t *b, const float *sfb, int block_b,
+                                   void *d, int d_type, int accumulate, int64_t m, int64_t n, int64_t k, uint32_t flags,
+                                   nvfp4_stream_t stream) {
+  clear_error();
+  const char *name = "fp8_gemm";
+  nvfp4_status_t st = fp8::check_product(name, m, n, k, d_type, accumulate, flags);
+  if (st != NVFP4_OK) return st;
+  if (block_b != 1 && block_b != 128) return fail(NVFP4_ERR_INVALID_ARG, "%s: block_b=%d (1 or 128)", name, block_b);
+  if (m == 0) return NVFP4_OK;
+  if (!a || !sfa || !b || !sfb || !d) return fail(NVFP4_ERR_INVALID_ARG, "%s: null pointer", name);
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(d, 16) || !aligned(sfa, 4) || !aligned(sfb, 4))
+    return fail(NVFP4_ERR_MISALIGNED, "%s: a, b and d need 16-B, the scales 4-B alignment", name);
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != NVFP4_OK) return st;
+  Call c{name, a, b, m, n, k, block_b, fp8::Args{}, &dev, flags, stream, sfa, sfb};
+  fp8::fill_args(c.args, d, d_type, accumulate, n, k, dev, flags);
+  if (m <= 16) return run_swap<16>(c);
+  if (m <= 32) return run_swap<32>(c);
+  if (m <= 64) return run_swap<64>(c);
+  if (m <= 128) return run_swap<128>(c);
+  return run_rows<256, 1>(c);
+}

@@ -1,0 +1,739 @@
+// e4m3 products with one fp32 scale per block of 128 along K: D = sum over blocks b of
+// (sP[row, b] sQ[col, b]) * sum over the block's 128 elements of P[row, k] Q[col, k].
+//
+// The tensor core sums one 128-wide block at a time into a tensor-memory buffer of its own
+// (tcgen05.mma kind::f8f6f4, four instructions of K = 32), and eight warps scale that block's sums
+// in fp32 and add them to accumulators that stay in registers over the whole K: the factor of a
+// block is an fp32 number, which no scale format of the tensor core holds.  A 128 x 256 tile takes
+// the tensor core 512 cycles a block (8192 multiply-adds a cycle); its sums take 256 cycles to read
+// from tensor memory (128 lanes of 4 bytes a cycle) and 256 to scale and add (128 lanes), and with a
+// factor per column 256 more, so that the scaling of one block hides behind the products of the next.
+//
+// The operand whose rows lie in the 128 tensor-memory lanes is P, the other (the columns) is Q.
+// Usually P is A (the tokens); with SWAP it is B (a weight), so that few tokens fill a narrow tile.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "host.h"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+namespace fp8 {
+
+enum Mode { kDense = 0, kGrouped = 1, kWgrad = 2 };
+
+constexpr int kMaxExperts = 1024;
+constexpr int kThreads = 384;      // 4 warps that feed, 8 that scale and add
+constexpr int kScaleSlots = 8;     // ring of the blocks' scales
+
+template <int NT_, bool SWAP_, bool PV_, bool CV_, int MODE_, int CG_ = 1>
+struct Cfg {
+  static constexpr int NT = NT_;         // columns of a tile (rows of Q)
+  static constexpr bool SWAP = SWAP_;    // P is B
+  static constexpr bool PV = PV_;        // P has a scale per row (else per 128 rows)
+  static constexpr bool CV = CV_;        // Q has a scale per row
+  static constexpr int MODE = MODE_;
+  static constexpr int CG = CG_;         // 2: a CTA pair shares a 256-row tile
+  static constexpr int P_BYTES = 128 * 128;
+  static constexpr int Q_ROWS = NT / CG;
+  static constexpr int Q_BYTES = Q_ROWS * 128;
+  static constexpr int STAGE = P_BYTES + Q_BYTES;
+  static constexpr int STAGES_FIT = 200 * 1024 / STAGE;
+  static constexpr int STAGES = STAGES_FIT > 12 ? 12 : STAGES_FIT;
+  static constexpr int NACC = NT >= 256 ? 2 : 4;
+  static constexpr int TMEM = NACC * NT < 32 ? 32 : NACC * NT;
+  static constexpr int W = NT / 2;       // columns of one scaling warp
+  static constexpr int CH = W < 32 ? W : 32;
+  static constexpr int SC_P = PV ? 128 : 4;
+  static constexpr int SC_Q = CV ? NT : 4;
+  static constexpr int SC_BYTES = (SC_P + SC_Q) * 4;
+  static constexpr int TABLE = MODE == kDense ? 0 : 3 * (kMaxExperts + 4) * 4;
+  static constexpr int CTRL = 1024;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + kScaleSlots * SC_BYTES + TABLE + CTRL;
+  // f8f6f4: fp32 sums (1 at bit 4), e4m3 operands (0 at bits 7 and 10), both K-major
+  static constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
+                                    (static_cast<uint32_t>(128 * CG >> 4) << 24);
+  static_assert(SMEM <= 232448, "smem");
+};
+
+// Where an operand's scales lie: of row r (or of its block of 128) and block b along K at
+// p + expert * es + r * rs + b * ks.
+struct Scales {
+  const float *p;
+  int64_t es, rs, ks;
+};
+
+struct Args {
+  Scales sp, sq;
+  void *d;
+  int64_t ldd, d_expert;     // elements
+  int p_rows, q_rows;        // dense and wgrad: rows of P and Q; grouped: rows of the weight in both
+  int nk;                    // blocks along K (dense and grouped)
+  int p_tiles, q_tiles;      // tiles along the static operands
+  int splits;                // dense with SWAP: CTAs of a cluster that share a tile's K
+  int out_f32, accumulate;
+  const int64_t *row_offsets;
+  int experts;
+  int64_t total_rows;        // grouped: rows of A
+  unsigned int *status;
+  long long wait_limit;
+  int skip_first_load;
+};
+
+struct Tile {
+  int p0, q0, p_end, q_end;  // rows of P and Q that the tile covers, and where they end
+  int py, qy;                // their first rows in the tensor maps
+  int kb0, nk;               // first block along K and how many
+  int expert;
+};
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t pdesc, uint64_t qdesc, uint32_t idesc, uint32_t accumulate,
+                                       bool pair) {
+  if (pair)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
+}
+
+// N consecutive tensor-memory columns of the warp's 32 lanes, and the wait that makes them readable
+// (the registers pass through it, so that nothing that uses them moves ahead of it).
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 32) {
+    tmem_ld_32x32b_x32(taddr, r);
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  } else {
+    static_assert(N == 8, "columns");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 4-byte global -> shared copy; zero where `ok` is false (the address is not read then).
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const float *src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+// Arrives on `bar` once this thread's copies so far have landed (an arrival the barrier counts).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+enum Site { kSiteLoad = 0, kSiteMmaAcc = 1, kSiteMmaStage = 2, kSiteScaleSlot = 4, kSiteScaleStage = 5, kSiteAcc = 6 };
+
+// Tables of the grouped forms in shared memory: row offsets, first tile of each expert, first block
+// along K of each expert (wgrad).
+struct Tables {
+  int *ro, *tp, *kb;
+};
+
+template <class C>
+__device__ __forceinline__ int token_tile() {
+  return C::SWAP ? C::NT : 128 * C::CG;
+}
+
+template <class C>
+__device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t, int rank) {
+  Tile r;
+  r.expert = 0;
+  r.kb0 = 0;
+  r.nk = a.nk;
+  int pi, qi;
+  if constexpr (C::MODE == kGrouped) {
+    int lo = 0, hi = a.experts - 1;  // the last expert whose first tile is at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tb.tp[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    r.expert = lo;
+    const int rows = tb.ro[lo + 1] - tb.ro[lo];
+    const int tt = (rows + token_tile<C>() - 1) / token_tile<C>();
+    const int l = t - tb.tp[lo];
+    // an expert's token tiles are adjacent: CTAs that run at the same time share the weight's tile
+    if constexpr (C::SWAP) {
+      pi = l / tt;
+      qi = l % tt;
+      r.p0 = pi * 128;
+      r.p_end = a.p_rows;
+      r.py = lo * a.p_rows + r.p0;
+      r.q0 = r.qy = tb.ro[lo] + qi * C::NT;
+      r.q_end = tb.ro[lo + 1];
+    } else {
+      qi = l / tt;
+      pi = l % tt;
+      r.p0 = r.py = tb.ro[lo] + (pi * C::CG + rank) * 128;
+      r.p_end = tb.ro[lo + 1];
+      r.q0 = qi * C::NT;
+      r.q_end = a.q_rows;
+      r.qy = lo * a.q_rows + r.q0;
+    }
+    return r;
+  }
+  if constexpr (C::MODE == kWgrad) {
+    const int per = a.p_tiles * a.q_tiles;
+    r.expert = t / per;
+    t -= r.expert * per;
+    r.kb0 = tb.kb[r.expert];
+    r.nk = tb.kb[r.expert + 1] - r.kb0;
+  }
+  // groups of 8 tiles along P: what runs at the same time shares both operands through L2
+  constexpr int G = 8;
+  const int g = t / (G * a.q_tiles), l = t - g * G * a.q_tiles;
+  const int gs = min(G, a.p_tiles - g * G);
+  pi = g * G + l % gs;
+  qi = l / gs;
+  r.p0 = r.py = (pi * C::CG + rank) * 128;
+  r.q0 = r.qy = qi * C::NT;
+  r.p_end = a.p_rows;
+  r.q_end = a.q_rows;
+  return r;
+}
+
+// One row's W values to D (contiguous columns): 32-byte stores where the row allows it, else 16, else
+// one by one.  `n` of them are inside.
+template <int W>
+__device__ __forceinline__ void store_row(const Args &a, int64_t at, int n, uint64_t (&acc)[W / 2]) {
+  if (n <= 0) return;
+  if (a.out_f32) {
+    float *d = static_cast<float *>(a.d) + at;
+    const bool vec = (reinterpret_cast<uintptr_t>(d) & 15) == 0;
+#pragma unroll
+    for (int c = 0; c < W; c += 4) {
+      float v[4];
+      unpack2(acc[c / 2], v[0], v[1]);
+      unpack2(acc[c / 2 + 1], v[2], v[3]);
+      if (vec && c + 4 <= n) {
+        float4 o = make_float4(v[0], v[1], v[2], v[3]);
+        if (a.accumulate) {
+          const float4 old = *reinterpret_cast<const float4 *>(d + c);
+          o = make_float4(old.x + o.x, old.y + o.y, old.z + o.z, old.w + o.w);
+        }
+        *reinterpret_cast<float4 *>(d + c) = o;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < n) d[c + i] = a.accumulate ? d[c + i] + v[i] : v[i];
+      }
+    }
+    return;
+  }
+  __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(a.d) + at;
+  const bool vec = (reinterpret_cast<uintptr_t>(d) & 15) == 0;
+#pragma unroll
+  for (int c = 0; c < W; c += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpack2(acc[c / 2 + i], lo, hi);
+      w[i] = pack_bf16x2(lo, hi);
+    }
+    if (vec && c + 8 <= n) {
+      *reinterpret_cast<uint4 *>(d + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < n) reinterpret_cast<uint16_t *>(d)[c + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
+  }
+}
+
+__device__ __forceinline__ void store_one(const Args &a, int64_t at, float v) {
+  if (a.out_f32) {
+    float *d = static_cast<float *>(a.d) + at;
+    *d = a.accumulate ? *d + v : v;
+  } else {
+    static_cast<__nv_bfloat16 *>(a.d)[at] = __float2bfloat16_rn(v);
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  // the ring begins on a 1024-byte boundary (the swizzle's period), at the same offset in each CTA of a pair
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  float *scales = reinterpret_cast<float *>(smem + C::STAGES * C::STAGE);
+  uint8_t *ctrl = reinterpret_cast<uint8_t *>(scales) + kScaleSlots * C::SC_BYTES;
+  uint64_t *full = reinterpret_cast<uint64_t *>(ctrl);           // [STAGES] operands have landed
+  uint64_t *empty = full + C::STAGES;                            // [STAGES] the products have read them
+  uint64_t *tfull = empty + C::STAGES;                           // [NACC] a block's sums are in tensor memory
+  uint64_t *tempty = tfull + C::NACC;                            // [NACC] they have been read
+  uint64_t *sfull = tempty + C::NACC;                            // [kScaleSlots]
+  uint64_t *sempty = sfull + kScaleSlots;
+  uint64_t *drain = sempty + kScaleSlots;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+  int *abort_flag = reinterpret_cast<int *>(tmem_holder + 1);
+  int *issued_count = abort_flag + 1;
+  int *bad = issued_count + 1;
+  Tables tb;
+  tb.ro = reinterpret_cast<int *>(ctrl + C::CTRL);
+  tb.tp = tb.ro + kMaxExperts + 4;
+  tb.kb = tb.tp + kMaxExperts + 4;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int splits = (C::MODE == kDense && C::SWAP) ? a.splits : 1;
+  const int cluster = C::CG == 2 ? 2 : splits;
+  const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int prank = C::CG == 2 ? rank : 0;   // which CTA of a pair
+  const int srank = C::CG == 2 ? 0 : rank;   // which part of K
+  const int unit = blockIdx.x / cluster, units = gridDim.x / cluster;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    for (int i = 0; i < C::NACC; ++i) {
+      mbar_init(smem_u32(&tfull[i]), 1);
+      mbar_init(smem_u32(&tempty[i]), 8 * C::CG);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(smem_u32(&sfull[i]), 32);
+      mbar_init(smem_u32(&sempty[i]), 8);
+    }
+    mbar_init(smem_u32(drain), 1);
+    fence_barrier_init();
+    *abort_flag = 0;
+    *issued_count = 0;
+    *bad = 0;
+    prefetch_tmap(&map_p);
+    prefetch_tmap(&map_q);
+  }
+  if (warp == 1) {
+    tmem_alloc<C::CG>(smem_u32(tmem_holder), C::TMEM);
+    tmem_relinquish<C::CG>();
+  }
+  pdl_trigger();
+  pdl_wait();
+  int total = 0;
+  if constexpr (C::MODE != kDense) {
+    __syncthreads();  // *bad is clear
+    for (int e = threadIdx.x; e <= a.experts; e += kThreads) {
+      const int64_t v = a.row_offsets[e];
+      const int64_t prev = e > 0 ? a.row_offsets[e - 1] : 0;
+      // (wgrad: total_rows is the number of padded rows that the operands hold)
+      if (v < prev || v > a.total_rows || (e == 0 && v != 0)) *bad = 1;
+      tb.ro[e] = static_cast<int>(v);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int tiles = 0, blocks = 0;
+      for (int b = 0; b < a.experts; b += 32) {
+        const int e = b + lane;
+        const int rows = e < a.experts ? tb.ro[e + 1] - tb.ro[e] : 0;
+        int nt = rows > 0 ? (rows + token_tile<C>() - 1) / token_tile<C>() * (C::SWAP ? a.p_tiles : a.q_tiles) : 0;
+        int nb = rows > 0 ? (rows + 127) / 128 : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xFFFFFFFFu, nt, o), y = __shfl_up_sync(0xFFFFFFFFu, nb, o);
+          if (lane >= o) {
+            nt += x;
+            nb += y;
+          }
+        }
+        if (e < a.experts) {
+          tb.tp[e + 1] = tiles + nt;
+          tb.kb[e + 1] = blocks + nb;
+        }
+        tiles += __shfl_sync(0xFFFFFFFFu, nt, 31);
+        blocks += __shfl_sync(0xFFFFFFFFu, nb, 31);
+      }
+      if (lane == 0) {
+        tb.tp[0] = tb.kb[0] = 0;
+        if (C::MODE == kWgrad && static_cast<int64_t>(blocks) * 128 > a.total_rows) *bad = 1;
+      }
+    }
+  }
+  tc_fence_before();
+  if constexpr (C::CG == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  if constexpr (C::MODE == kDense) total = a.p_tiles * a.q_tiles;
+  else if constexpr (C::MODE == kGrouped) total = tb.tp[a.experts];
+  else total = a.experts * a.p_tiles * a.q_tiles;
+  if (C::MODE != kDense && *bad) {
+    if (threadIdx.x == 0) atomicOr(a.status, 2u);
+    total = 0;
+  }
+  const uint32_t tmem = *tmem_holder;
+  const WaitCtl wc{a.wait_limit, abort_flag, a.status};
+  constexpr bool PAIR = C::CG == 2;
+
+  // this CTA's share of a tile's blocks along K
+  auto k_range = [&](const Tile &t, int &k0, int &k1) {
+    k0 = static_cast<int>(static_cast<int64_t>(t.nk) * srank / splits);
+    k1 = static_cast<int>(static_cast<int64_t>(t.nk) * (srank + 1) / splits);
+  };
+
+  uint64_t acc[C::W / 2];
+  if (warp < 4) {
+    if constexpr (C::NT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0) {
+      // ------------------------------------------------------------ operands
+      if (lane == 0) {
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = unit; u < total && ok; u += units) {
+          const Tile t = tile_at<C>(a, tb, u, prank);
+          int k0, k1;
+          k_range(t, k0, k1);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait<PAIR>(smem_u32(&empty[stage]), phase ^ 1, wc, kSiteLoad)) {
+              ok = false;
+              break;
+            }
+            const uint32_t bar = smem_u32(&full[stage]);
+            uint8_t *dst = smem + stage * C::STAGE;
+            const int x = (t.kb0 + kb) * 128;
+            if (prank == 0) mbar_arrive_expect_tx(bar, C::CG * C::STAGE);
+            if (!(a.skip_first_load && issued == 0)) {
+              if constexpr (PAIR) {
+                const uint32_t bar0 = map_to_rank(bar, 0);
+                tma_load_2d_pair(smem_u32(dst), &map_p, bar0, x, t.py);
+                tma_load_2d_pair(smem_u32(dst + C::P_BYTES), &map_q, bar0, x, t.qy + prank * C::Q_ROWS);
+              } else {
+                tma_load_2d(smem_u32(dst), &map_p, bar, x, t.py);
+                tma_load_2d(smem_u32(dst + C::P_BYTES), &map_q, bar, x, t.qy);
+              }
+            }
+            ++issued;
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        *issued_count = issued;
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ products
+      if (lane == 0 && prank == 0) {
+        int stage = 0, ab = 0;
+        uint32_t phase = 0, aphase = 0;
+        bool ok = true;
+        for (int u = unit; u < total && ok; u += units) {
+          const Tile t = tile_at<C>(a, tb, u, prank);
+          int k0, k1;
+          k_range(t, k0, k1);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait<PAIR>(smem_u32(&tempty[ab]), aphase ^ 1, wc, kSiteMmaAcc) ||
+                !mbar_wait<PAIR>(smem_u32(&full[stage]), phase, wc, kSiteMmaStage)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t pd = sdesc_k_sw128(smem_u32(smem + stage * C::STAGE));
+            const uint64_t qd = sdesc_k_sw128(smem_u32(smem + stage * C::STAGE + C::P_BYTES));
+            const uint32_t d = tmem + ab * C::NT;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_f8(d, pd + 2 * i, qd + 2 * i, C::IDESC, i > 0 ? 1u : 0u, PAIR);
+            if constexpr (PAIR) {
+              tc_commit_pair_mc(smem_u32(&empty[stage]), static_cast<uint16_t>(0x3));
+              tc_commit_pair_mc(smem_u32(&tfull[ab]), static_cast<uint16_t>(0x3));
+            } else {
+              tc_commit(smem_u32(&empty[stage]));
+              tc_commit(smem_u32(&tfull[ab]));
+            }
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+            if (++ab == C::NACC) {
+              ab = 0;
+              aphase ^= 1;
+            }
+          }
+        }
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ scales
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = unit; u < total && ok; u += units) {
+        const Tile t = tile_at<C>(a, tb, u, prank);
+        int k0, k1;
+        k_range(t, k0, k1);
+        const float *sp = a.sp.p + t.expert * a.sp.es, *sq = a.sq.p + t.expert * a.sq.es;
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!mbar_wait(smem_u32(&sempty[slot]), phase ^ 1, wc, kSiteScaleSlot)) {
+            ok = false;
+            break;
+          }
+          const int64_t b = t.kb0 + kb;
+          const uint32_t dst = smem_u32(scales) + slot * C::SC_BYTES;
+          if constexpr (C::PV) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = t.p0 + i * 32 + lane;
+              const bool in = r < t.p_end;
+              cp_async_4(dst + (i * 32 + lane) * 4, sp + (in ? r : t.p0 < t.p_end ? t.p0 : 0) * a.sp.rs + b * a.sp.ks, in);
+            }
+          } else if (lane == 0) {
+            const bool in = t.p0 < t.p_end;
+            cp_async_4(dst, sp + (in ? t.p0 / 128 : 0) * a.sp.rs + b * a.sp.ks, in);
+          }
+          if constexpr (C::CV) {
+#pragma unroll
+            for (int i = 0; i < (C::NT + 31) / 32; ++i) {
+              const int c = i * 32 + lane;
+              const int r = t.q0 + c;
+              const bool in = r < t.q_end;
+              if (C::NT >= 32 || c < C::NT)
+                cp_async_4(dst + (C::SC_P + c) * 4, sq + (in ? r : t.q0) * a.sq.rs + b * a.sq.ks, in);
+            }
+          } else if (lane < (C::NT + 127) / 128) {
+            const int r = t.q0 + lane * 128;
+            const bool in = r < t.q_end;
+            cp_async_4(dst + (C::SC_P + lane) * 4, sq + (in ? r / 128 : 0) * a.sq.rs + b * a.sq.ks, in);
+          }
+          cp_async_arrive(smem_u32(&sfull[slot]));
+          if (++slot == kScaleSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      cp_async_wait_all();
+    }
+  } else {
+    // -------------------------------------------------------------- scaling and sums
+    if constexpr (C::NT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * C::W;
+    int slot = 0, ab = 0;
+    uint32_t sphase = 0, aphase = 0;
+    bool ok = true;
+    for (int u = unit; u < total && ok; u += units) {
+      const Tile t = tile_at<C>(a, tb, u, prank);
+      int k0, k1;
+      k_range(t, k0, k1);
+#pragma unroll
+      for (int i = 0; i < C::W / 2; ++i) acc[i] = 0;
+      for (int kb = k0; kb < k1; ++kb) {
+        ok = mbar_wait(smem_u32(&sfull[slot]), sphase, wc, kSiteScaleStage) &&
+             mbar_wait<PAIR>(smem_u32(&tfull[ab]), aphase, wc, kSiteAcc);
+        ok = __all_sync(0xFFFFFFFFu, ok);  // the loads below are the whole warp's
+        if (!ok) break;
+        tc_fence_after();
+        const float *sc = scales + slot * (C::SC_BYTES / 4);
+        const float rs = C::PV ? sc[quad * 32 + lane] : sc[0];
+        float f = rs;
+        if constexpr (!C::CV) f = rs * sc[C::SC_P + (C::NT == 256 ? half : 0)];
+        const uint64_t f2 = pack2(f, f);
+#pragma unroll
+        for (int c = 0; c < C::W; c += C::CH) {
+          uint32_t r[C::CH];
+          tmem_ld<C::CH>(t_lane + ab * C::NT + c, r);
+          tmem_ld_done<C::CH>(r);
+          if (c + C::CH == C::W) {  // the last columns are in registers: the buffer may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR) mbar_arrive_remote(map_to_rank(smem_u32(&tempty[ab]), 0));
+              else mbar_arrive(smem_u32(&tempty[ab]));
+            }
+          }
+          if constexpr (C::CV) {
+            const float4 *cs = reinterpret_cast<const float4 *>(sc + C::SC_P + half * C::W + c);
+#pragma unroll
+            for (int i = 0; i < C::CH; i += 4) {
+              const float4 s = cs[i / 4];
+              acc[(c + i) / 2] = fma2(mul2f(pack2u(r[i], r[i + 1]), pack2(s.x, s.y)), f2, acc[(c + i) / 2]);
+              acc[(c + i) / 2 + 1] = fma2(mul2f(pack2u(r[i + 2], r[i + 3]), pack2(s.z, s.w)), f2, acc[(c + i) / 2 + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < C::CH; i += 2) acc[(c + i) / 2] = fma2(pack2u(r[i], r[i + 1]), f2, acc[(c + i) / 2]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sempty[slot]));
+        if (++slot == kScaleSlots) {
+          slot = 0;
+          sphase ^= 1;
+        }
+        if (++ab == C::NACC) {
+          ab = 0;
+          aphase ^= 1;
+        }
+      }
+      if (!ok || splits > 1) continue;
+      const int p = t.p0 + quad * 32 + lane, q = t.q0 + half * C::W;
+      if (p < t.p_end) {
+        if constexpr (C::SWAP) {
+          const int64_t at = static_cast<int64_t>(q) * a.ldd + p;
+#pragma unroll
+          for (int i = 0; i < C::W; ++i) {
+            float lo, hi;
+            unpack2(acc[i / 2], lo, hi);
+            if (q + i < t.q_end) store_one(a, at + i * a.ldd, (i & 1) ? hi : lo);
+          }
+        } else {
+          store_row<C::W>(a, t.expert * a.d_expert + static_cast<int64_t>(p) * a.ldd + q, t.q_end - q, acc);
+        }
+      }
+    }
+  }
+
+  // -------------------------------------------------------------- end
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // wait (bounded) for copies still landing and for outstanding products, so that nothing writes
+    // shared or tensor memory after the CTA is gone (a pair's copies complete on the first CTA's barriers)
+    if (threadIdx.x == 0 && prank == 0) {
+      const int issued = *issued_count;
+      for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i) {
+        const uint32_t bar = smem_u32(&full[i % C::STAGES]);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, (i / C::STAGES) & 1) && clock64() - t0 < a.wait_limit) {
+        }
+      }
+    }
+    if (threadIdx.x == 32 && prank == 0) {
+      tc_commit<C::CG>(smem_u32(drain));
+      const long long t0 = clock64();
+      while (!mbar_try_wait(smem_u32(drain), 0) && clock64() - t0 < a.wait_limit) {
+      }
+    }
+    __syncthreads();
+  }
+  if constexpr (C::MODE == kDense && C::SWAP) {
+    if (splits > 1) {
+      // Each CTA of the cluster holds the sums over its part of K; they are laid down in the (now idle)
+      // ring, columns outermost, and each CTA adds a share of the columns in rank order.
+      float *red = reinterpret_cast<float *>(smem);
+      if (warp >= 4) {
+        const int row = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;
+#pragma unroll
+        for (int i = 0; i < C::W; ++i) {
+          float lo, hi;
+          unpack2(acc[i / 2], lo, hi);
+          red[(half * C::W + i) * 128 + row] = (i & 1) ? hi : lo;
+        }
+      }
+      cluster_sync();
+      const Tile t = tile_at<C>(a, tb, unit, 0);
+      const int cols = min(C::NT, t.q_end - t.q0);
+      // 32 float4 a column
+      for (int i = threadIdx.x + rank * kThreads; i < cols * 32; i += kThreads * splits) {
+        const uint32_t off = smem_u32(red) + i * 16;
+        float4 s = ld_cluster_v4(map_to_rank(off, 0));
+        for (int r = 1; r < splits; ++r) {
+          const float4 v = ld_cluster_v4(map_to_rank(off, r));
+          s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        const int p = t.p0 + (i % 32) * 4;
+        const int64_t at = static_cast<int64_t>(t.q0 + i / 32) * a.ldd + p;
+        const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (p + j < t.p_end) store_one(a, at + j, v[j]);
+      }
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<C::CG>(tmem, C::TMEM);
+  }
+  if (cluster > 1) cluster_sync();  // no CTA leaves while another reads its memory or arrives on its barriers
+}
+
+// What the products' entry points check and fill alike.  rows, cols: of the result; k: what is summed over.
+inline nvfp4_status_t check_product(const char *name, int64_t rows, int64_t cols, int64_t k, int d_type, int accumulate,
+                                    uint32_t flags) {
+  constexpr int64_t kMost = (1LL << 31) - 512;  // tile origins step past the ends by less
+  if (rows < 0 || cols <= 0 || k <= 0 || rows > kMost || cols > kMost || k > kMost)
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: sizes %lld, %lld, %lld", name, (long long)rows, (long long)cols, (long long)k);
+  if (k % 16) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: k=%lld is not a multiple of 16", name, (long long)k);
+  if (d_type != NVFP4_DTYPE_BF16 && d_type != NVFP4_DTYPE_F32)
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: d_type=%d", name, d_type);
+  if (accumulate && d_type != NVFP4_DTYPE_F32)
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: only an fp32 result is accumulated", name);
+  if (flags & ~(uint32_t)(NVFP4_FLAG_PDL | NVFP4_FLAG_DEBUG_TIMEOUT | NVFP4_FLAG_DEBUG_SKIP_FIRST_LOAD))
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name, flags);
+  return NVFP4_OK;
+}
+inline void fill_args(Args &a, void *d, int d_type, int accumulate, int64_t ldd, int64_t k, const DeviceInfo &dev,
+                      uint32_t flags) {
+  a.d = d;
+  a.out_f32 = d_type == NVFP4_DTYPE_F32;
+  a.accumulate = accumulate != 0;
+  a.ldd = ldd;
+  a.nk = static_cast<int>(ceil_div(k, 128));
+  a.splits = 1;
+  a.status = dev.status;
+  a.wait_limit = wait_limit(flags);
+  a.skip_first_load = (flags & NVFP4_FLAG_DEBUG_SKIP_FIRST_LOAD) && (flags & NVFP4_FLAG_DEBUG_TIMEOUT);
+}
+
+// Tensor maps, shared memory and launch of one configuration.  tiles: an upper bound of the tiles (the
+// grid is the smaller of that and what the device holds at once).
+template <class C>
+nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, const uint8_t *q, int64_t q_rows,
+                           int64_t k, int64_t tiles, const Args &args, const DeviceInfo &dev, uint32_t flags,
+                           nvfp4_stream_t stream) {
+  CUtensorMap mp, mq;
+  nvfp4_status_t st = encode_tmap_2d_u8(&mp, p, k, p_rows, k, 128, 128, true);
+  if (st == NVFP4_OK) st = encode_tmap_2d_u8(&mq, q, k, q_rows, k, 128, C::Q_ROWS, true);
+  if (st != NVFP4_OK) return st;
+  auto kern = fp8_gemm_kernel<C>;
+  st = allow_smem(reinterpret_cast<const void *>(kern), C::SMEM, dev.device);
+  if (st != NVFP4_OK) return st;
+  const int cluster = C::CG == 2 ? 2 : args.splits;
+  int64_t grid = tiles * cluster;
+  // split tiles: one per cluster (their partials are joined once); else persistent
+  const int64_t cap = dev.sm_count / cluster * cluster;
+  if (args.splits == 1 && grid > cap) grid = cap;
+  cudaError_t e = launch(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), C::SMEM, (cudaStream_t)stream,
+                         (flags & NVFP4_FLAG_PDL) != 0, cluster, mp, mq, args);
+  return check_launch(e, name);
+}
+
+}  // namespace fp8
+}  // namespace nvfp4

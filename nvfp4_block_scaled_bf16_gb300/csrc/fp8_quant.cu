@@ -1,0 +1,504 @@
+// e4m3 quantisation with one fp32 scale per block of 128, along the rows, along the columns (transposed), both
+// from one read, or per 128 x 128 block.
+//
+// A block with largest magnitude amax (at least 2^-100) has scale s = fl(amax / 448) and codes
+// e4m3(fl(x * fl(448 / amax))): every step is one fp32 rounding to nearest even, so the codes are the same
+// wherever a block is quantised.  Magnitudes are compared as integers (the bits of |x|), in which NaN lies above
+// infinity: a block that holds either gets a scale and codes that stand for nothing finite.
+//
+// All of it is bound by memory: a value is read once (2 or 4 bytes) and written once or twice (1 byte each).
+#include "host.h"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kQuantThreads = 256;
+constexpr int kMaxQuantExperts = 1024;
+constexpr uint32_t kTinyBits = 27u << 23;  // 2^-100
+
+// Sixteen consecutive values of a row, as loaded.
+template <bool F32>
+struct Vals {
+  uint32_t w[F32 ? 16 : 8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 16 : 8); ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void load(const void *p) {
+    uint32_t a[8];
+    ld_global_nc_v8(p, a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = a[i];
+    if constexpr (F32) {
+      ld_global_nc_v8(static_cast<const uint8_t *>(p) + 32, a);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[8 + i] = a[i];
+    }
+  }
+  // 16-byte loads, for rows that are not 32-byte aligned
+  __device__ __forceinline__ void load16(const void *p) {
+    const uint4 *q = static_cast<const uint4 *>(p);
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+      const uint4 v = __ldg(q + i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (F32) return __uint_as_float(w[i]);
+    else return __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+  }
+  // the bits of the largest magnitude, as fp32
+  __device__ __forceinline__ uint32_t amax() const {
+    if constexpr (F32) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      return max(m & 0xFFFF0000u, m << 16);
+    }
+  }
+};
+
+__device__ __forceinline__ void divided(uint32_t amax_bits, float &scale, float &factor) {
+  const float a = __uint_as_float(max(amax_bits, kTinyBits));
+  scale = __fdiv_rn(a, 448.0f);
+  factor = __fdiv_rn(448.0f, a);
+}
+
+// Two fp32 -> two e4m3 codes (RNE, saturating; NaN stays NaN), `lo` in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+  return h;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+template <bool F32>
+__device__ __forceinline__ uint4 codes16(const Vals<F32> &v, float f) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = e4m3x4(__fmul_rn(v.at(4 * i), f), __fmul_rn(v.at(4 * i + 1), f), __fmul_rn(v.at(4 * i + 2), f),
+                  __fmul_rn(v.at(4 * i + 3), f));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ------------------------------------------------------------------ along the rows only
+// Eight lanes share a block of 128 (16 values each), a warp takes the same block of four rows, a CTA 32 rows
+// and U blocks, whose loads are all in flight before the first is used.
+template <bool F32, int U>
+__global__ void __launch_bounds__(kQuantThreads) fp8_rows_kernel(const void *__restrict__ x, int64_t ldx,
+                                                                 const int32_t *__restrict__ src, int64_t x_rows, int64_t m,
+                                                                 int k, int kb, uint8_t *__restrict__ q,
+                                                                 float *__restrict__ sf, int wide, unsigned int *status) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x % 32, cg = lane & 7;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32) * 4 + (lane >> 3);
+  const int b0 = blockIdx.y * U;
+  bool in = row < m;
+  int64_t xr = in ? row : 0;
+  if (src && in) {
+    xr = src[row];
+    if (xr < 0 || xr >= x_rows) {
+      if (b0 == 0 && cg == 0) atomicOr(status, 8u);
+      xr = -1;  // quantises zeros
+    }
+  }
+  const uint8_t *xp = static_cast<const uint8_t *>(x) + (xr < 0 ? 0 : xr) * ldx * (F32 ? 4 : 2);
+  Vals<F32> v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = (b0 + u) * 128 + cg * 16;
+    v[u].zero();
+    if (in && xr >= 0 && c < k) {
+      if (wide) v[u].load(xp + static_cast<int64_t>(c) * (F32 ? 4 : 2));
+      else v[u].load16(xp + static_cast<int64_t>(c) * (F32 ? 4 : 2));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (b0 + u >= kb) break;
+    uint32_t am = v[u].amax();
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+    float s, f;
+    divided(am, s, f);
+    const int c = (b0 + u) * 128 + cg * 16;
+    if (in && c < k) *reinterpret_cast<uint4 *>(q + row * k + c) = codes16<F32>(v[u], f);
+    if (in && cg == 0) sf[static_cast<int64_t>(b0 + u) * m + row] = s;
+  }
+}
+
+// ------------------------------------------------------------------ 128 x 128 tiles
+// What a tile is quantised along.
+enum Along { kColumns = 0, kBoth = 1, kBlock = 2 };
+
+struct TileArgs {
+  const void *x;
+  int64_t ldx, x_rows, m;      // m: rows of the result
+  const int32_t *src;
+  int k, kb;
+  const int64_t *row_offsets;  // experts' rows (each expert's columns of qt begin at a multiple of 128)
+  int experts;
+  int64_t row_blocks;          // 128-row blocks of qt (kBlock: of one matrix)
+  uint8_t *q;
+  float *sf;
+  uint8_t *qt;
+  float *sft;
+  int wide, chain;             // chain: consecutive tiles along k that a CTA takes
+  unsigned int *status;
+};
+
+// A warp holds 16 rows of the tile, a thread 4 rows x 16 columns.  The codes along the columns go through shared
+// memory, four rows of a column to a word; the word's place is turned by its column group, so that the 32 lanes'
+// words fall into 32 banks, and a column's 128 bytes leave as eight 16-byte stores side by side.
+template <bool F32, int ALONG>
+__global__ void __launch_bounds__(kQuantThreads) fp8_tile_kernel(const TileArgs a) {
+  __shared__ uint32_t s_max[8][F32 ? 128 : 64];
+  __shared__ __align__(16) float s_fac[128];
+  __shared__ __align__(16) uint32_t s_t[128 * 32];
+  __shared__ int s_row0, s_rows;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, cg = lane & 7, rg = lane >> 3;
+  const int64_t blk = blockIdx.x;
+  int64_t row0, rows;           // first row of the result in this tile, rows in it
+  int64_t mat = 0, mblk = blk;  // kBlock: matrix and its row block
+  if (ALONG == kBlock) {
+    mat = blk / a.row_blocks;
+    mblk = blk % a.row_blocks;
+    row0 = mat * a.m + mblk * 128;
+    rows = min(static_cast<int64_t>(128), a.m - mblk * 128);
+  } else if (a.row_offsets) {
+    // the expert whose padded rows hold this block: a warp's running sum over the experts
+    if (warp == 0) {
+      int64_t first = 0;  // first block of expert e0
+      bool found = false, bad = false;
+      if (lane == 0) s_rows = 0;
+      __syncwarp();
+      for (int e0 = 0; e0 < a.experts && !found; e0 += 32) {
+        const int e = e0 + lane;
+        int64_t lo = 0, hi = 0;
+        if (e < a.experts) {
+          lo = a.row_offsets[e];
+          hi = a.row_offsets[e + 1];
+        }
+        bad = bad || lo < 0 || hi < lo || hi > a.m || (e == 0 && lo != 0);
+        if (__any_sync(0xFFFFFFFFu, bad)) break;
+        const int nb = static_cast<int>((hi - lo + 127) / 128);
+        int incl = nb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (lane >= o) incl += n;
+        }
+        const int64_t mine = first + incl - nb;
+        const bool here = nb > 0 && blk >= mine && blk < mine + nb;
+        if (here) {
+          s_row0 = static_cast<int>(lo + (blk - mine) * 128);
+          s_rows = static_cast<int>(min(static_cast<int64_t>(128), hi - lo - (blk - mine) * 128));
+        }
+        found = __any_sync(0xFFFFFFFFu, here);
+        first += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      }
+      if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, 2u);
+    }
+    __syncthreads();
+    row0 = s_row0;
+    rows = s_rows;  // 0: past the last expert (or malformed offsets): the block is written as zeros
+    if (rows == 0) row0 = 0;
+  } else {
+    row0 = blk * 128;
+    rows = min(static_cast<int64_t>(128), a.m - row0);
+  }
+  // this thread's four rows
+  const uint8_t *xp[4];
+  bool in[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = warp * 16 + rg * 4 + i;
+    in[i] = r < rows;
+    int64_t xr = in[i] ? row0 + r : 0;
+    if (ALONG != kBlock && a.src && in[i]) {
+      xr = a.src[xr];
+      if (xr < 0 || xr >= a.x_rows) {
+        if (blockIdx.y == 0 && cg == 0) atomicOr(a.status, 8u);
+        xr = -1;
+      }
+    }
+    xp[i] = xr < 0 ? nullptr : static_cast<const uint8_t *>(a.x) + (xr * a.ldx + cg * 16) * (F32 ? 4 : 2);
+  }
+  Vals<F32> v[4];
+  auto load = [&](int b) {
+    const int c = b * 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i].zero();
+      if (in[i] && xp[i] && c + cg * 16 < a.k) {
+        const uint8_t *p = xp[i] + static_cast<int64_t>(c) * (F32 ? 4 : 2);
+        if (a.wide) v[i].load(p);
+        else v[i].load16(p);
+      }
+    }
+  };
+  const int b0 = blockIdx.y * a.chain, b1 = min(a.kb, b0 + a.chain);
+  for (int b = b0; b < b1; ++b) {
+    load(b);
+    const int c0 = b * 128;
+    float fb = 0.0f;  // kBlock: the tile's factor
+    if constexpr (ALONG == kBlock) {
+      uint32_t am = max(max(v[0].amax(), v[1].amax()), max(v[2].amax(), v[3].amax()));
+      am = __reduce_max_sync(0xFFFFFFFFu, am);
+      if (lane == 0) s_max[warp][0] = am;
+      __syncthreads();
+      am = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) am = max(am, s_max[w][0]);
+      float s;
+      divided(am, s, fb);
+      if (tid == 0) {
+        a.sf[(mat * a.row_blocks + mblk) * a.kb + b] = s;
+        if (a.qt) a.sft[(mat * a.kb + b) * a.row_blocks + mblk] = s;
+      }
+    }
+    if constexpr (ALONG != kColumns) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f = fb;
+        if constexpr (ALONG == kBoth) {
+          uint32_t am = v[i].amax();
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+          float s;
+          divided(am, s, f);
+          if (in[i] && cg == 0) a.sf[static_cast<int64_t>(b) * a.m + row0 + warp * 16 + rg * 4 + i] = s;
+        }
+        if (in[i] && c0 + cg * 16 < a.k)
+          *reinterpret_cast<uint4 *>(a.q + (row0 + warp * 16 + rg * 4 + i) * a.k + c0 + cg * 16) = codes16<F32>(v[i], f);
+      }
+    }
+    float f[16];
+    if constexpr (ALONG == kBlock) {
+      if (!a.qt) {
+        __syncthreads();  // s_max is written again by the next tile
+        continue;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = fb;
+    } else {
+      // largest magnitude of each column: over the thread's rows, the warp's four row groups, the warps
+      constexpr int NW = F32 ? 16 : 8;
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        uint32_t am = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (F32) am = max(am, v[i].w[j] & 0x7FFFFFFFu);
+          else am = __vmaxu2(am, v[i].w[j] & 0x7FFF7FFFu);
+        }
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+          const uint32_t n = __shfl_xor_sync(0xFFFFFFFFu, am, o);
+          if constexpr (F32) am = max(am, n);
+          else am = __vmaxu2(am, n);
+        }
+        if (rg == 0) s_max[warp][cg * NW + j] = am;
+      }
+      __syncthreads();
+      if (tid < 128) {
+        uint32_t am = 0;
+        if constexpr (F32) {
+#pragma unroll
+          for (int w = 0; w < 8; ++w) am = max(am, s_max[w][tid]);
+        } else {
+#pragma unroll
+          for (int w = 0; w < 8; ++w) am = __vmaxu2(am, s_max[w][tid / 2]);
+          am = (tid & 1) ? (am & 0xFFFF0000u) : (am << 16);
+        }
+        float s, fc;
+        divided(am, s, fc);
+        s_fac[tid] = fc;
+        if (c0 + tid < a.k) a.sft[blk * a.k + c0 + tid] = s;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 t = *reinterpret_cast<const float4 *>(&s_fac[cg * 16 + 4 * j]);
+        f[4 * j] = t.x;
+        f[4 * j + 1] = t.y;
+        f[4 * j + 2] = t.z;
+        f[4 * j + 3] = t.w;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t w = e4m3x4(__fmul_rn(v[0].at(j), f[j]), __fmul_rn(v[1].at(j), f[j]), __fmul_rn(v[2].at(j), f[j]),
+                                __fmul_rn(v[3].at(j), f[j]));
+      s_t[(cg * 16 + j) * 32 + ((warp * 4 + rg) ^ (cg * 4))] = w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = i * 32 + tid / 8, ch = tid % 8;  // column, 16-byte piece of its 128 rows
+      const uint4 w = *reinterpret_cast<const uint4 *>(&s_t[c * 32 + ((ch * 4) ^ ((c / 16) * 4))]);
+      if (c0 + c < a.k) {
+        if constexpr (ALONG == kBlock) {
+          if (mblk * 128 + ch * 16 < a.m)
+            *reinterpret_cast<uint4 *>(a.qt + (mat * a.k + c0 + c) * a.m + mblk * 128 + ch * 16) = w;
+        } else {
+          *reinterpret_cast<uint4 *>(a.qt + static_cast<int64_t>(c0 + c) * a.row_blocks * 128 + blk * 128 + ch * 16) = w;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+nvfp4_status_t check_input(const char *name, const void *x, int x_type, int64_t ldx, int64_t k, int64_t rows) {
+  if (x_type != NVFP4_DTYPE_BF16 && x_type != NVFP4_DTYPE_F32)
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: x_type=%d", name, x_type);
+  if (rows < 0 || k <= 0 || rows > (1LL << 31) - 512 || k > (1LL << 31) - 512)
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: rows=%lld k=%lld", name, (long long)rows, (long long)k);
+  if (k % 16) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: k=%lld is not a multiple of 16", name, (long long)k);
+  const int unit = x_type == NVFP4_DTYPE_F32 ? 4 : 8;
+  if ((ldx != 0 && ldx < k) || ldx % unit || !aligned(x, 16))
+    return fail(NVFP4_ERR_MISALIGNED, "%s: x needs 16-B alignment and rows of at least k that start on 16 B (ldx=%lld)", name,
+                (long long)ldx);
+  return NVFP4_OK;
+}
+int wide_rows(const void *x, int x_type, int64_t ldx) {
+  return aligned(x, 32) && ldx * (x_type == NVFP4_DTYPE_F32 ? 4 : 2) % 32 == 0;
+}
+
+template <int ALONG>
+cudaError_t launch_tiles(int x_type, TileArgs &a, int64_t blocks, const DeviceInfo &dev, uint32_t flags, nvfp4_stream_t s) {
+  // tiles that a CTA takes in turn: one while that fills the device, then as many as leave it four rounds
+  const int64_t tiles = blocks * a.kb, want = static_cast<int64_t>(dev.sm_count) * 16;
+  int64_t chain = tiles / want;
+  chain = chain < 1 ? 1 : chain > 8 ? 8 : chain;
+  a.chain = static_cast<int>(chain);
+  auto kern = x_type == NVFP4_DTYPE_F32 ? fp8_tile_kernel<true, ALONG> : fp8_tile_kernel<false, ALONG>;
+  return launch(kern, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(ceil_div(a.kb, chain))), dim3(kQuantThreads),
+                0, (cudaStream_t)s, (flags & NVFP4_FLAG_PDL) != 0, 1, a);
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" int64_t fp8_padded_rows(int64_t rows, int num_experts) {
+  if (rows < 0 || num_experts < 0) return 0;
+  return round_up(rows, 128) + 128 * static_cast<int64_t>(num_experts);
+}
+
+extern "C" nvfp4_status_t fp8_quantize(const void *x, int x_type, int64_t x_rows, int64_t k, int64_t ldx,
+                                       const int32_t *src_rows, int64_t rows, const int64_t *row_offsets, int num_experts,
+                                       uint8_t *q, float *sf, uint8_t *qt, float *sft, uint32_t flags,
+                                       nvfp4_stream_t stream) {
+  clear_error();
+  const char *name = "fp8_quantize";
+  nvfp4_status_t st = check_input(name, x, x_type, ldx, k, rows);
+  if (st != NVFP4_OK) return st;
+  if (x_rows < 0 || (!src_rows && rows > 0 && rows != x_rows))
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: x_rows=%lld rows=%lld (equal without src_rows)", name, (long long)x_rows,
+                (long long)rows);
+  if (flags & ~(uint32_t)NVFP4_FLAG_PDL) return fail(NVFP4_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name, flags);
+  if ((q == nullptr) != (sf == nullptr) || (qt == nullptr) != (sft == nullptr) || (rows > 0 && !q && !qt))
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: q and sf, qt and sft: give both or neither, and one pair at least", name);
+  if (row_offsets ? (num_experts < 1 || num_experts > kMaxQuantExperts) : num_experts != 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: num_experts=%d (1..%d with row_offsets, 0 without)", name, num_experts,
+                kMaxQuantExperts);
+  if (row_offsets && !qt) return fail(NVFP4_ERR_INVALID_ARG, "%s: row_offsets belong to qt", name);
+  if (!aligned(q, 16) || !aligned(qt, 16) || !aligned(sf, 4) || !aligned(sft, 4) || !aligned(src_rows, 4) ||
+      !aligned(row_offsets, 8))
+    return fail(NVFP4_ERR_MISALIGNED, "%s: q and qt need 16-B, row_offsets 8-B, the others 4-B alignment", name);
+  const int64_t blocks = fp8_padded_rows(rows, num_experts) / 128;
+  if (blocks == 0 || (rows == 0 && !qt)) return NVFP4_OK;
+  if (!x && rows > 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: null pointer", name);
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != NVFP4_OK) return st;
+  const int kb = static_cast<int>(ceil_div(k, 128)), wide = wide_rows(x, x_type, ldx);
+  cudaError_t e;
+  if (!qt) {
+    // four blocks a CTA (their loads in flight together) once that still fills the device, one before
+    const int64_t ctas = ceil_div(rows, 32);
+    const int U = x_type == NVFP4_DTYPE_F32 ? 2 : 4;
+    const bool many = ctas * ceil_div(kb, U) >= dev.sm_count * 4LL;
+    if (ceil_div(kb, many ? U : 1) > 65535) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: k=%lld is too long", name, (long long)k);
+    auto kern = x_type == NVFP4_DTYPE_F32 ? (many ? fp8_rows_kernel<true, 2> : fp8_rows_kernel<true, 1>)
+                                          : (many ? fp8_rows_kernel<false, 4> : fp8_rows_kernel<false, 1>);
+    e = launch(kern, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(ceil_div(kb, many ? U : 1))), dim3(kQuantThreads), 0,
+               (cudaStream_t)stream, (flags & NVFP4_FLAG_PDL) != 0, 1, x, ldx, src_rows, x_rows, rows, static_cast<int>(k), kb, q,
+               sf, wide, dev.status);
+    return check_launch(e, name);
+  }
+  if (kb > 65535) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: k=%lld is too long", name, (long long)k);
+  TileArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.x_rows = x_rows;
+  a.m = rows;
+  a.src = src_rows;
+  a.k = static_cast<int>(k);
+  a.kb = kb;
+  a.row_offsets = row_offsets;
+  a.experts = num_experts;
+  a.row_blocks = blocks;
+  a.q = q;
+  a.sf = sf;
+  a.qt = qt;
+  a.sft = sft;
+  a.wide = wide;
+  a.status = dev.status;
+  e = q ? launch_tiles<kBoth>(x_type, a, blocks, dev, flags, stream) : launch_tiles<kColumns>(x_type, a, blocks, dev, flags, stream);
+  return check_launch(e, name);
+}
+
+extern "C" nvfp4_status_t fp8_quantize_weight(const void *w, int w_type, int64_t matrices, int64_t n, int64_t k, int64_t ldw,
+                                              uint8_t *q, float *sf, uint8_t *qt, float *sft, uint32_t flags,
+                                              nvfp4_stream_t stream) {
+  clear_error();
+  const char *name = "fp8_quantize_weight";
+  if (matrices < 0 || n < 0 || (n > 0 && matrices > ((1LL << 31) - 512) / n))
+    return fail(NVFP4_ERR_INVALID_ARG, "%s: matrices=%lld n=%lld", name, (long long)matrices, (long long)n);
+  nvfp4_status_t st = check_input(name, w, w_type, ldw, k, matrices * n);
+  if (st != NVFP4_OK) return st;
+  if (flags & ~(uint32_t)NVFP4_FLAG_PDL) return fail(NVFP4_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name, flags);
+  if ((qt == nullptr) != (sft == nullptr)) return fail(NVFP4_ERR_INVALID_ARG, "%s: qt and sft: give both or neither", name);
+  if (qt && n % 16) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: the transpose needs n %% 16 == 0 (n=%lld)", name, (long long)n);
+  if (!aligned(q, 16) || !aligned(qt, 16) || !aligned(sf, 4) || !aligned(sft, 4))
+    return fail(NVFP4_ERR_MISALIGNED, "%s: q and qt need 16-B, the scales 4-B alignment", name);
+  if (matrices == 0 || n == 0) return NVFP4_OK;
+  if (!w || !q || !sf) return fail(NVFP4_ERR_INVALID_ARG, "%s: null pointer", name);
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != NVFP4_OK) return st;
+  TileArgs a{};
+  a.x = w;
+  a.ldx = ldw;
+  a.x_rows = a.m = n;
+  a.k = static_cast<int>(k);
+  a.kb = static_cast<int>(ceil_div(k, 128));
+  if (a.kb > 65535) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: k=%lld is too long", name, (long long)k);
+  a.row_blocks = ceil_div(n, 128);
+  a.q = q;
+  a.sf = sf;
+  a.qt = qt;
+  a.sft = sft;
+  a.wide = wide_rows(w, w_type, ldw);
+  a.status = dev.status;
+  return check_launch(launch_tiles<kBlock>(w_type, a, matrices * a.row_blocks, dev, flags, stream), name);
+}
