@@ -31,7 +31,7 @@ nvfp4_status_t run(const Call &c) {
   args.sq = C::SWAP ? sa : sb;
   args.p_rows = static_cast<int>(p);
   args.q_rows = static_cast<int>(q);
-  args.p_tiles = static_cast<int>(ceil_div(p, 128 * C::CG));
+  args.p_tiles = static_cast<int>(ceil_div(p, 128));
   args.q_tiles = static_cast<int>(ceil_div(q, C::NT));
   const int64_t tiles = static_cast<int64_t>(args.p_tiles) * args.q_tiles;
   if (tiles >= (1LL << 31)) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", c.name);
@@ -51,10 +51,10 @@ nvfp4_status_t run_swap(const Call &c) {
   return c.block_b == 128 ? run<fp8::Cfg<NT, true, false, true, fp8::kDense>>(c)
                           : run<fp8::Cfg<NT, true, true, true, fp8::kDense>>(c);
 }
-template <int NT, int CG>
+template <int NT>
 nvfp4_status_t run_rows(const Call &c) {
-  return c.block_b == 128 ? run<fp8::Cfg<NT, false, true, false, fp8::kDense, CG>>(c)
-                          : run<fp8::Cfg<NT, false, true, true, fp8::kDense, CG>>(c);
+  return c.block_b == 128 ? run<fp8::Cfg<NT, false, true, false, fp8::kDense>>(c)
+                          : run<fp8::Cfg<NT, false, true, true, fp8::kDense>>(c);
 }
 
 }  // namespace
@@ -80,5 +80,5 @@ extern "C" nvfp4_status_t fp8_gemm(const uint8_t *a, const float *sfa, const uin
   if (m <= 32) return run_swap<32>(c);
   if (m <= 64) return run_swap<64>(c);
   if (m <= 128) return run_swap<128>(c);
-  return run_rows<256, 1>(c);
+  return run_rows<256>(c);
 }

@@ -24,36 +24,38 @@ namespace fp8 {
 enum Mode { kDense = 0, kGrouped = 1, kWgrad = 2 };
 
 constexpr int kMaxExperts = 1024;
-constexpr int kThreads = 384;      // 4 warps that feed, 8 that scale and add
-constexpr int kScaleSlots = 8;     // ring of the blocks' scales
 
-template <int NT_, bool SWAP_, bool PV_, bool CV_, int MODE_, int CG_ = 1>
+template <int NT_, bool SWAP_, bool PV_, bool CV_, int MODE_>
 struct Cfg {
   static constexpr int NT = NT_;         // columns of a tile (rows of Q)
   static constexpr bool SWAP = SWAP_;    // P is B
   static constexpr bool PV = PV_;        // P has a scale per row (else per 128 rows)
   static constexpr bool CV = CV_;        // Q has a scale per row
   static constexpr int MODE = MODE_;
-  static constexpr int CG = CG_;         // 2: a CTA pair shares a 256-row tile
   static constexpr int P_BYTES = 128 * 128;
-  static constexpr int Q_ROWS = NT / CG;
-  static constexpr int Q_BYTES = Q_ROWS * 128;
+  static constexpr int Q_BYTES = NT * 128;
   static constexpr int STAGE = P_BYTES + Q_BYTES;
   static constexpr int STAGES_FIT = 200 * 1024 / STAGE;
   static constexpr int STAGES = STAGES_FIT > 12 ? 12 : STAGES_FIT;
+  // ring of the blocks' scales; not longer than the operands', so that a block's scales never arrive at a stage's
+  // barrier before the block that had the stage before it has gone through
+  static constexpr int SLOTS = STAGES < 8 ? STAGES : 8;
   static constexpr int NACC = NT >= 256 ? 2 : 4;
   static constexpr int TMEM = NACC * NT < 32 ? 32 : NACC * NT;
-  static constexpr int W = NT / 2;       // columns of one scaling warp
-  static constexpr int CH = W < 32 ? W : 32;
+  static constexpr int SW = 8;     // scaling warps (behind 4 that feed)
+  static constexpr int THREADS = 128 + 32 * SW;
+  static constexpr int W = NT * 4 / SW;  // columns of one scaling warp
+  static constexpr int CH = W < 32 ? W : CV && W > 64 ? 16 : 32;
   static constexpr int SC_P = PV ? 128 : 4;
   static constexpr int SC_Q = CV ? NT : 4;
   static constexpr int SC_BYTES = (SC_P + SC_Q) * 4;
   static constexpr int TABLE = MODE == kDense ? 0 : 3 * (kMaxExperts + 4) * 4;
   static constexpr int CTRL = 1024;
-  static constexpr int SMEM = 1024 + STAGES * STAGE + kScaleSlots * SC_BYTES + TABLE + CTRL;
+  static_assert(NACC <= STAGES, "a buffer's next block must have a stage of its own");
+  static constexpr int SMEM = 1024 + STAGES * STAGE + SLOTS * SC_BYTES + TABLE + CTRL;
   // f8f6f4: fp32 sums (1 at bit 4), e4m3 operands (0 at bits 7 and 10), both K-major
   static constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
-                                    (static_cast<uint32_t>(128 * CG >> 4) << 24);
+                                    (static_cast<uint32_t>(128 >> 4) << 24);
   static_assert(SMEM <= 232448, "smem");
 };
 
@@ -88,22 +90,14 @@ struct Tile {
   int expert;
 };
 
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t pdesc, uint64_t qdesc, uint32_t idesc, uint32_t accumulate,
-                                       bool pair) {
-  if (pair)
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t pdesc, uint64_t qdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
 }
 
-// N consecutive tensor-memory columns of the warp's 32 lanes, and the wait that makes them readable
-// (the registers pass through it, so that nothing that uses them moves ahead of it).
+// N consecutive tensor-memory columns of the warp's 32 lanes.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
   if constexpr (N == 32) {
@@ -121,13 +115,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
                  : "r"(taddr));
   }
 }
-template <int N>
-__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[N]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -141,9 +128,11 @@ __device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
+// (volatile: the compiler otherwise puts the sums of one chunk of columns off past the loads of the next, and
+// runs out of registers)
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
 __device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
@@ -160,7 +149,7 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-enum Site { kSiteLoad = 0, kSiteMmaAcc = 1, kSiteMmaStage = 2, kSiteScaleSlot = 4, kSiteScaleStage = 5, kSiteAcc = 6 };
+enum Site { kSiteLoad = 0, kSiteMmaStage = 2, kSiteScaleSlot = 4, kSiteAcc = 6 };
 
 // Tables of the grouped forms in shared memory: row offsets, first tile of each expert, first block
 // along K of each expert (wgrad).
@@ -170,11 +159,11 @@ struct Tables {
 
 template <class C>
 __device__ __forceinline__ int token_tile() {
-  return C::SWAP ? C::NT : 128 * C::CG;
+  return C::SWAP ? C::NT : 128;
 }
 
 template <class C>
-__device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t, int rank) {
+__device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t) {
   Tile r;
   r.expert = 0;
   r.kb0 = 0;
@@ -203,7 +192,7 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t, 
     } else {
       qi = l / tt;
       pi = l % tt;
-      r.p0 = r.py = tb.ro[lo] + (pi * C::CG + rank) * 128;
+      r.p0 = r.py = tb.ro[lo] + pi * 128;
       r.p_end = tb.ro[lo + 1];
       r.q0 = qi * C::NT;
       r.q_end = a.q_rows;
@@ -224,7 +213,7 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t, 
   const int gs = min(G, a.p_tiles - g * G);
   pi = g * G + l % gs;
   qi = l / gs;
-  r.p0 = r.py = (pi * C::CG + rank) * 128;
+  r.p0 = r.py = pi * 128;
   r.q0 = r.qy = qi * C::NT;
   r.p_end = a.p_rows;
   r.q_end = a.q_rows;
@@ -234,7 +223,7 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t, 
 // One row's W values to D (contiguous columns): 32-byte stores where the row allows it, else 16, else
 // one by one.  `n` of them are inside.
 template <int W>
-__device__ __forceinline__ void store_row(const Args &a, int64_t at, int n, uint64_t (&acc)[W / 2]) {
+__device__ __forceinline__ void store_row(const Args &a, int64_t at, int n, const uint64_t (&acc)[W / 2]) {
   if (n <= 0) return;
   if (a.out_f32) {
     float *d = static_cast<float *>(a.d) + at;
@@ -290,20 +279,21 @@ __device__ __forceinline__ void store_one(const Args &a, int64_t at, float v) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(C::THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const Args a) {
   extern __shared__ uint8_t smem_raw[];
-  // the ring begins on a 1024-byte boundary (the swizzle's period), at the same offset in each CTA of a pair
+  // the ring begins on a 1024-byte boundary (the swizzle's period)
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   float *scales = reinterpret_cast<float *>(smem + C::STAGES * C::STAGE);
-  uint8_t *ctrl = reinterpret_cast<uint8_t *>(scales) + kScaleSlots * C::SC_BYTES;
-  uint64_t *full = reinterpret_cast<uint64_t *>(ctrl);           // [STAGES] operands have landed
-  uint64_t *empty = full + C::STAGES;                            // [STAGES] the products have read them
-  uint64_t *tfull = empty + C::STAGES;                           // [NACC] a block's sums are in tensor memory
-  uint64_t *tempty = tfull + C::NACC;                            // [NACC] they have been read
-  uint64_t *sfull = tempty + C::NACC;                            // [kScaleSlots]
-  uint64_t *sempty = sfull + kScaleSlots;
-  uint64_t *drain = sempty + kScaleSlots;
+  uint8_t *ctrl = reinterpret_cast<uint8_t *>(scales) + C::SLOTS * C::SC_BYTES;
+  // A block's products wait for one barrier and announce one: `full` collects the operands, the scales and the
+  // scaling warps that emptied the block's buffer (NACC blocks before); `done` tells the loader that the stage and
+  // the scaling warps that the sums are theirs.  Every wait and every commit of the issuing thread costs about 90
+  // cycles that the tensor core does not work through (measured; a block's products take 512).
+  uint64_t *full = reinterpret_cast<uint64_t *>(ctrl);  // [STAGES]
+  uint64_t *done = full + C::STAGES;                    // [STAGES]
+  uint64_t *sempty = done + C::STAGES;                  // [C::SLOTS] the scaling warps have read the scales
+  uint64_t *drain = sempty + C::SLOTS;
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
   int *abort_flag = reinterpret_cast<int *>(tmem_holder + 1);
   int *issued_count = abort_flag + 1;
@@ -314,26 +304,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   tb.kb = tb.tp + kMaxExperts + 4;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int splits = (C::MODE == kDense && C::SWAP) ? a.splits : 1;
-  const int cluster = C::CG == 2 ? 2 : splits;
-  const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int prank = C::CG == 2 ? rank : 0;   // which CTA of a pair
-  const int srank = C::CG == 2 ? 0 : rank;   // which part of K
-  const int unit = blockIdx.x / cluster, units = gridDim.x / cluster;
+  constexpr bool SPLIT = C::MODE == kDense && C::SWAP;
+  const int splits = SPLIT ? a.splits : 1;
+  const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = blockIdx.x / splits, units = gridDim.x / splits;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), 1);
+      mbar_init(smem_u32(&full[i]), 1 + 32 + C::SW);
+      mbar_init(smem_u32(&done[i]), 1);
     }
-    for (int i = 0; i < C::NACC; ++i) {
-      mbar_init(smem_u32(&tfull[i]), 1);
-      mbar_init(smem_u32(&tempty[i]), 8 * C::CG);
-    }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(smem_u32(&sfull[i]), 32);
-      mbar_init(smem_u32(&sempty[i]), 8);
-    }
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(smem_u32(&sempty[i]), C::SW);
     mbar_init(smem_u32(drain), 1);
     fence_barrier_init();
     *abort_flag = 0;
@@ -343,15 +324,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&map_q);
   }
   if (warp == 1) {
-    tmem_alloc<C::CG>(smem_u32(tmem_holder), C::TMEM);
-    tmem_relinquish<C::CG>();
+    tmem_alloc<1>(smem_u32(tmem_holder), C::TMEM);
+    tmem_relinquish<1>();
   }
   pdl_trigger();
   pdl_wait();
   int total = 0;
   if constexpr (C::MODE != kDense) {
     __syncthreads();  // *bad is clear
-    for (int e = threadIdx.x; e <= a.experts; e += kThreads) {
+    for (int e = threadIdx.x; e <= a.experts; e += C::THREADS) {
       const int64_t v = a.row_offsets[e];
       const int64_t prev = e > 0 ? a.row_offsets[e - 1] : 0;
       // (wgrad: total_rows is the number of padded rows that the operands hold)
@@ -388,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc_fence_before();
-  if constexpr (C::CG == 2) cluster_sync();
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   if constexpr (C::MODE == kDense) total = a.p_tiles * a.q_tiles;
   else if constexpr (C::MODE == kGrouped) total = tb.tp[a.experts];
@@ -400,17 +380,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem = *tmem_holder;
   const WaitCtl wc{a.wait_limit, abort_flag, a.status};
-  constexpr bool PAIR = C::CG == 2;
 
   // this CTA's share of a tile's blocks along K
   auto k_range = [&](const Tile &t, int &k0, int &k1) {
-    k0 = static_cast<int>(static_cast<int64_t>(t.nk) * srank / splits);
-    k1 = static_cast<int>(static_cast<int64_t>(t.nk) * (srank + 1) / splits);
+    k0 = 0;
+    k1 = t.nk;
+    if constexpr (SPLIT) {
+      k0 = static_cast<int>(static_cast<int64_t>(t.nk) * rank / splits);
+      k1 = static_cast<int>(static_cast<int64_t>(t.nk) * (rank + 1) / splits);
+    }
   };
 
-  uint64_t acc[C::W / 2];
+  uint64_t acc[C::W / 2];  // pairs of columns
   if (warp < 4) {
-    if constexpr (C::NT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (C::NT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 0) {
       // ------------------------------------------------------------ operands
       if (lane == 0) {
@@ -418,27 +401,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phase = 0;
         bool ok = true;
         for (int u = unit; u < total && ok; u += units) {
-          const Tile t = tile_at<C>(a, tb, u, prank);
+          const Tile t = tile_at<C>(a, tb, u);
           int k0, k1;
           k_range(t, k0, k1);
           for (int kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait<PAIR>(smem_u32(&empty[stage]), phase ^ 1, wc, kSiteLoad)) {
+            if (issued >= C::STAGES && !mbar_wait(smem_u32(&done[stage]), phase ^ 1, wc, kSiteLoad)) {
               ok = false;
               break;
             }
             const uint32_t bar = smem_u32(&full[stage]);
-            uint8_t *dst = smem + stage * C::STAGE;
+            const uint32_t dst = smem_u32(smem + stage * C::STAGE);
             const int x = (t.kb0 + kb) * 128;
-            if (prank == 0) mbar_arrive_expect_tx(bar, C::CG * C::STAGE);
+            mbar_arrive_expect_tx(bar, C::STAGE);
             if (!(a.skip_first_load && issued == 0)) {
-              if constexpr (PAIR) {
-                const uint32_t bar0 = map_to_rank(bar, 0);
-                tma_load_2d_pair(smem_u32(dst), &map_p, bar0, x, t.py);
-                tma_load_2d_pair(smem_u32(dst + C::P_BYTES), &map_q, bar0, x, t.qy + prank * C::Q_ROWS);
-              } else {
-                tma_load_2d(smem_u32(dst), &map_p, bar, x, t.py);
-                tma_load_2d(smem_u32(dst + C::P_BYTES), &map_q, bar, x, t.qy);
-              }
+              tma_load_2d(dst, &map_p, bar, x, t.py);
+              tma_load_2d(dst + C::P_BYTES, &map_q, bar, x, t.qy);
             }
             ++issued;
             if (++stage == C::STAGES) {
@@ -451,51 +428,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ products
-      if (lane == 0 && prank == 0) {
+      if (lane == 0) {
         int stage = 0, ab = 0;
-        uint32_t phase = 0, aphase = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int u = unit; u < total && ok; u += units) {
-          const Tile t = tile_at<C>(a, tb, u, prank);
+          const Tile t = tile_at<C>(a, tb, u);
           int k0, k1;
           k_range(t, k0, k1);
           for (int kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait<PAIR>(smem_u32(&tempty[ab]), aphase ^ 1, wc, kSiteMmaAcc) ||
-                !mbar_wait<PAIR>(smem_u32(&full[stage]), phase, wc, kSiteMmaStage)) {
+            if (!mbar_wait(smem_u32(&full[stage]), phase, wc, kSiteMmaStage)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint64_t pd = sdesc_k_sw128(smem_u32(smem + stage * C::STAGE));
             const uint64_t qd = sdesc_k_sw128(smem_u32(smem + stage * C::STAGE + C::P_BYTES));
-            const uint32_t d = tmem + ab * C::NT;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_f8(d, pd + 2 * i, qd + 2 * i, C::IDESC, i > 0 ? 1u : 0u, PAIR);
-            if constexpr (PAIR) {
-              tc_commit_pair_mc(smem_u32(&empty[stage]), static_cast<uint16_t>(0x3));
-              tc_commit_pair_mc(smem_u32(&tfull[ab]), static_cast<uint16_t>(0x3));
-            } else {
-              tc_commit(smem_u32(&empty[stage]));
-              tc_commit(smem_u32(&tfull[ab]));
-            }
+            for (int i = 0; i < 4; ++i) mma_f8(tmem + ab * C::NT, pd + 2 * i, qd + 2 * i, C::IDESC, i > 0 ? 1u : 0u);
+            tc_commit(smem_u32(&done[stage]));
             if (++stage == C::STAGES) {
               stage = 0;
               phase ^= 1;
             }
-            if (++ab == C::NACC) {
-              ab = 0;
-              aphase ^= 1;
-            }
+            if (++ab == C::NACC) ab = 0;
           }
         }
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------ scales
-      int slot = 0;
+      int slot = 0, stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = unit; u < total && ok; u += units) {
-        const Tile t = tile_at<C>(a, tb, u, prank);
+        const Tile t = tile_at<C>(a, tb, u);
         int k0, k1;
         k_range(t, k0, k1);
         const float *sp = a.sp.p + t.expert * a.sp.es, *sq = a.sq.p + t.expert * a.sq.es;
@@ -531,8 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool in = r < t.q_end;
             cp_async_4(dst + (C::SC_P + lane) * 4, sq + (in ? r / 128 : 0) * a.sq.rs + b * a.sq.ks, in);
           }
-          cp_async_arrive(smem_u32(&sfull[slot]));
-          if (++slot == kScaleSlots) {
+          cp_async_arrive(smem_u32(&full[stage]));
+          if (++stage == C::STAGES) stage = 0;
+          if (++slot == C::SLOTS) {
             slot = 0;
             phase ^= 1;
           }
@@ -542,65 +509,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- scaling and sums
-    if constexpr (C::NT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if constexpr (C::NT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * C::W;
-    int slot = 0, ab = 0;
-    uint32_t sphase = 0, aphase = 0;
+    int slot = 0, ab = 0, stage = 0;
+    uint32_t phase = 0;
     bool ok = true;
+    if (lane == 0)  // the buffers of the first blocks are empty
+      for (int i = 0; i < C::NACC; ++i) mbar_arrive(smem_u32(&full[i]));
     for (int u = unit; u < total && ok; u += units) {
-      const Tile t = tile_at<C>(a, tb, u, prank);
+      const Tile t = tile_at<C>(a, tb, u);
       int k0, k1;
       k_range(t, k0, k1);
 #pragma unroll
       for (int i = 0; i < C::W / 2; ++i) acc[i] = 0;
-      for (int kb = k0; kb < k1; ++kb) {
-        ok = mbar_wait(smem_u32(&sfull[slot]), sphase, wc, kSiteScaleStage) &&
-             mbar_wait<PAIR>(smem_u32(&tfull[ab]), aphase, wc, kSiteAcc);
-        ok = __all_sync(0xFFFFFFFFu, ok);  // the loads below are the whole warp's
-        if (!ok) break;
+      // A block's first columns are loaded before the last columns of the block before it are added, so that the
+      // waits and the loads' latency pass while the arithmetic units have work.
+      constexpr int CHUNKS = C::W / C::CH;
+      constexpr bool AHEAD = CHUNKS > 1;
+      uint32_t r[AHEAD ? 2 : 1][C::CH];
+      float f = 0.0f;
+      const float *sc = scales;
+      // waits for the block's sums (and so its scales), and starts on its columns
+      auto begin = [&]() -> bool {
+        bool here = mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc);
+        here = __all_sync(0xFFFFFFFFu, here);  // the loads below are the whole warp's
+        if (!here) return false;
         tc_fence_after();
-        const float *sc = scales + slot * (C::SC_BYTES / 4);
-        const float rs = C::PV ? sc[quad * 32 + lane] : sc[0];
-        float f = rs;
-        if constexpr (!C::CV) f = rs * sc[C::SC_P + (C::NT == 256 ? half : 0)];
+        tmem_ld<C::CH>(t_lane + ab * C::NT, r[0]);
+        sc = scales + slot * (C::SC_BYTES / 4);
+        f = C::PV ? sc[quad * 32 + lane] : sc[0];
+        if constexpr (!C::CV) f *= sc[C::SC_P + half * C::W / 128];
+        return true;
+      };
+      if (k0 < k1) ok = begin();
+      for (int kb = k0; kb < k1 && ok; ++kb) {
         const uint64_t f2 = pack2(f, f);
+        const float *scb = sc;
+        const int slot_b = slot, ab_b = ab;
+        const int next = stage + C::NACC >= C::STAGES ? stage + C::NACC - C::STAGES : stage + C::NACC;  // the buffer's next block's stage
+        if (++slot == C::SLOTS) slot = 0;
+        if (++ab == C::NACC) ab = 0;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
 #pragma unroll
-        for (int c = 0; c < C::W; c += C::CH) {
-          uint32_t r[C::CH];
-          tmem_ld<C::CH>(t_lane + ab * C::NT + c, r);
-          tmem_ld_done<C::CH>(r);
-          if (c + C::CH == C::W) {  // the last columns are in registers: the buffer may be overwritten
+        for (int i = 0; i < CHUNKS; ++i) {
+          tmem_ld_wait();
+          if (i + 1 < CHUNKS) {
+            tmem_ld<C::CH>(t_lane + ab_b * C::NT + (i + 1) * C::CH, r[(i + 1) & 1]);
+          } else {  // the last columns are in registers: the buffer may be overwritten
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              if constexpr (PAIR) mbar_arrive_remote(map_to_rank(smem_u32(&tempty[ab]), 0));
-              else mbar_arrive(smem_u32(&tempty[ab]));
-            }
+            if (lane == 0) mbar_arrive(smem_u32(&full[next]));
+            if (AHEAD && kb + 1 < k1) ok = begin();
           }
+          uint32_t (&v)[C::CH] = r[AHEAD ? (i & 1) : 0];
+          uint64_t *sum = acc + i * C::CH / 2;
           if constexpr (C::CV) {
-            const float4 *cs = reinterpret_cast<const float4 *>(sc + C::SC_P + half * C::W + c);
+            const ulonglong2 *cs = reinterpret_cast<const ulonglong2 *>(scb + C::SC_P + half * C::W + i * C::CH);
 #pragma unroll
-            for (int i = 0; i < C::CH; i += 4) {
-              const float4 s = cs[i / 4];
-              acc[(c + i) / 2] = fma2(mul2f(pack2u(r[i], r[i + 1]), pack2(s.x, s.y)), f2, acc[(c + i) / 2]);
-              acc[(c + i) / 2 + 1] = fma2(mul2f(pack2u(r[i + 2], r[i + 3]), pack2(s.z, s.w)), f2, acc[(c + i) / 2 + 1]);
+            for (int j = 0; j < C::CH; j += 4) {
+              const ulonglong2 s = cs[j / 4];
+              sum[j / 2] = fma2(mul2f(pack2u(v[j], v[j + 1]), s.x), f2, sum[j / 2]);
+              sum[j / 2 + 1] = fma2(mul2f(pack2u(v[j + 2], v[j + 3]), s.y), f2, sum[j / 2 + 1]);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < C::CH; i += 2) acc[(c + i) / 2] = fma2(pack2u(r[i], r[i + 1]), f2, acc[(c + i) / 2]);
+            for (int j = 0; j < C::CH; j += 2) sum[j / 2] = fma2(pack2u(v[j], v[j + 1]), f2, sum[j / 2]);
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sempty[slot]));
-        if (++slot == kScaleSlots) {
-          slot = 0;
-          sphase ^= 1;
-        }
-        if (++ab == C::NACC) {
-          ab = 0;
-          aphase ^= 1;
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&sempty[slot_b]));
+        if (!AHEAD && kb + 1 < k1) ok = begin();
       }
       if (!ok || splits > 1) continue;
       const int p = t.p0 + quad * 32 + lane, q = t.q0 + half * C::W;
@@ -625,25 +607,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort_flag) {
     // wait (bounded) for copies still landing and for outstanding products, so that nothing writes
-    // shared or tensor memory after the CTA is gone (a pair's copies complete on the first CTA's barriers)
-    if (threadIdx.x == 0 && prank == 0) {
+    // shared or tensor memory after the CTA is gone (the stages' barriers wait for other arrivals too, that may
+    // never come: 2^25 cycles are ample for a copy)
+    if (threadIdx.x == 0) {
       const int issued = *issued_count;
       for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i) {
         const uint32_t bar = smem_u32(&full[i % C::STAGES]);
         const long long t0 = clock64();
-        while (!mbar_try_wait(bar, (i / C::STAGES) & 1) && clock64() - t0 < a.wait_limit) {
+        while (!mbar_try_wait(bar, (i / C::STAGES) & 1) && clock64() - t0 < (1LL << 25)) {
         }
       }
     }
-    if (threadIdx.x == 32 && prank == 0) {
-      tc_commit<C::CG>(smem_u32(drain));
+    if (threadIdx.x == 32) {
+      tc_commit(smem_u32(drain));
       const long long t0 = clock64();
       while (!mbar_try_wait(smem_u32(drain), 0) && clock64() - t0 < a.wait_limit) {
       }
     }
     __syncthreads();
   }
-  if constexpr (C::MODE == kDense && C::SWAP) {
+  if constexpr (SPLIT) {
     if (splits > 1) {
       // Each CTA of the cluster holds the sums over its part of K; they are laid down in the (now idle)
       // ring, columns outermost, and each CTA adds a share of the columns in rank order.
@@ -658,10 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       cluster_sync();
-      const Tile t = tile_at<C>(a, tb, unit, 0);
+      const Tile t = tile_at<C>(a, tb, unit);
       const int cols = min(C::NT, t.q_end - t.q0);
       // 32 float4 a column
-      for (int i = threadIdx.x + rank * kThreads; i < cols * 32; i += kThreads * splits) {
+      for (int i = threadIdx.x + rank * C::THREADS; i < cols * 32; i += C::THREADS * splits) {
         const uint32_t off = smem_u32(red) + i * 16;
         float4 s = ld_cluster_v4(map_to_rank(off, 0));
         for (int r = 1; r < splits; ++r) {
@@ -679,9 +662,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<C::CG>(tmem, C::TMEM);
+    tmem_dealloc<1>(tmem, C::TMEM);
   }
-  if (cluster > 1) cluster_sync();  // no CTA leaves while another reads its memory or arrives on its barriers
+  if (splits > 1) cluster_sync();  // no CTA leaves while another reads its memory
 }
 
 // What the products' entry points check and fill alike.  rows, cols: of the result; k: what is summed over.
@@ -720,17 +703,17 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
                            nvfp4_stream_t stream) {
   CUtensorMap mp, mq;
   nvfp4_status_t st = encode_tmap_2d_u8(&mp, p, k, p_rows, k, 128, 128, true);
-  if (st == NVFP4_OK) st = encode_tmap_2d_u8(&mq, q, k, q_rows, k, 128, C::Q_ROWS, true);
+  if (st == NVFP4_OK) st = encode_tmap_2d_u8(&mq, q, k, q_rows, k, 128, C::NT, true);
   if (st != NVFP4_OK) return st;
   auto kern = fp8_gemm_kernel<C>;
   st = allow_smem(reinterpret_cast<const void *>(kern), C::SMEM, dev.device);
   if (st != NVFP4_OK) return st;
-  const int cluster = C::CG == 2 ? 2 : args.splits;
+  const int cluster = args.splits;
   int64_t grid = tiles * cluster;
   // split tiles: one per cluster (their partials are joined once); else persistent
   const int64_t cap = dev.sm_count / cluster * cluster;
   if (args.splits == 1 && grid > cap) grid = cap;
-  cudaError_t e = launch(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), C::SMEM, (cudaStream_t)stream,
+  cudaError_t e = launch(kern, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), C::SMEM, (cudaStream_t)stream,
                          (flags & NVFP4_FLAG_PDL) != 0, cluster, mp, mq, args);
   return check_launch(e, name);
 }
