@@ -49,10 +49,11 @@ struct Cfg {
   static constexpr int SC_P = PV ? 128 : 4;
   static constexpr int SC_Q = CV ? NT : 4;
   static constexpr int SC_BYTES = (SC_P + SC_Q) * 4;
-  static constexpr int TABLE = MODE == kDense ? 0 : 3 * (kMaxExperts + 4) * 4;
+  static constexpr int TABLE = MODE == kDense ? 0 : 2 * (kMaxExperts + 4) * 4;
+  static constexpr int TURN = SWAP ? 0 : SW * 32 * 17 * 4;  // where rows of D that are not aligned are turned around
   static constexpr int CTRL = 1024;
   static_assert(NACC <= STAGES, "a buffer's next block must have a stage of its own");
-  static constexpr int SMEM = 1024 + STAGES * STAGE + SLOTS * SC_BYTES + TABLE + CTRL;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + SLOTS * SC_BYTES + TABLE + TURN + CTRL;
   // f8f6f4: fp32 sums (1 at bit 4), e4m3 operands (0 at bits 7 and 10), both K-major
   static constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
                                     (static_cast<uint32_t>(128 >> 4) << 24);
@@ -151,8 +152,8 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 
 enum Site { kSiteLoad = 0, kSiteMmaStage = 2, kSiteScaleSlot = 4, kSiteAcc = 6 };
 
-// Tables of the grouped forms in shared memory: row offsets, first tile of each expert, first block
-// along K of each expert (wgrad).
+// Tables of the grouped forms in shared memory: row offsets; first tile of each expert or (wgrad) its first
+// block along K.
 struct Tables {
   int *ro, *tp, *kb;
 };
@@ -220,61 +221,105 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t) 
   return r;
 }
 
-// One row's W values to D (contiguous columns): 32-byte stores where the row allows it, else 16, else
-// one by one.  `n` of them are inside.
-template <int W>
-__device__ __forceinline__ void store_row(const Args &a, int64_t at, int n, const uint64_t (&acc)[W / 2]) {
-  if (n <= 0) return;
-  if (a.out_f32) {
-    float *d = static_cast<float *>(a.d) + at;
-    const bool vec = (reinterpret_cast<uintptr_t>(d) & 15) == 0;
-#pragma unroll
-    for (int c = 0; c < W; c += 4) {
-      float v[4];
-      unpack2(acc[c / 2], v[0], v[1]);
-      unpack2(acc[c / 2 + 1], v[2], v[3]);
-      if (vec && c + 4 <= n) {
-        float4 o = make_float4(v[0], v[1], v[2], v[3]);
-        if (a.accumulate) {
-          const float4 old = *reinterpret_cast<const float4 *>(d + c);
-          o = make_float4(old.x + o.x, old.y + o.y, old.z + o.z, old.w + o.w);
-        }
-        *reinterpret_cast<float4 *>(d + c) = o;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c + i < n) d[c + i] = a.accumulate ? d[c + i] + v[i] : v[i];
-      }
-    }
-    return;
-  }
-  __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(a.d) + at;
-  const bool vec = (reinterpret_cast<uintptr_t>(d) & 15) == 0;
-#pragma unroll
-  for (int c = 0; c < W; c += 8) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      unpack2(acc[c / 2 + i], lo, hi);
-      w[i] = pack_bf16x2(lo, hi);
-    }
-    if (vec && c + 8 <= n) {
-      *reinterpret_cast<uint4 *>(d + c) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < n) reinterpret_cast<uint16_t *>(d)[c + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-    }
-  }
-}
-
 __device__ __forceinline__ void store_one(const Args &a, int64_t at, float v) {
   if (a.out_f32) {
     float *d = static_cast<float *>(a.d) + at;
     *d = a.accumulate ? *d + v : v;
   } else {
     static_cast<__nv_bfloat16 *>(a.d)[at] = __float2bfloat16_rn(v);
+  }
+}
+
+// A warp's 32 rows (one a lane) of W columns to D, the lane's row at element `at`, `n` columns and the row `in`
+// it.  Where every row of D starts on 16 bytes a lane writes its own row, 32 bytes at a time if it can (whole
+// sectors); else 16 columns at a time are turned around through shared memory, so that 16 lanes write one row's
+// neighbours (one by one, a warp's store would touch 32 sectors for 4 bytes each).
+template <int W>
+__device__ __forceinline__ void store_rows(const Args &a, int64_t at, int n, bool in, float *turn, int lane,
+                                           const uint64_t (&acc)[W / 2]) {
+  const int es = a.out_f32 ? 4 : 2;
+  uint8_t *d = static_cast<uint8_t *>(a.d) + at * es;
+  const bool vec = (a.ldd * es) % 16 == 0 && (a.d_expert * es) % 16 == 0;
+  if (vec) {
+    if (!in) return;
+    const bool wide = (reinterpret_cast<uintptr_t>(d) & 31) == 0;
+    if (a.out_f32) {
+#pragma unroll
+      for (int c = 0; c < W; c += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack2(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
+        float *o = reinterpret_cast<float *>(d) + c;
+        if (a.accumulate) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < n) v[i] += o[i];
+        }
+        if (c + 8 <= n) {
+          if (wide) {
+            const uint32_t w[8] = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]),
+                                   __float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+            st_global_v8(o, w);
+          } else {
+            reinterpret_cast<float4 *>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < n) o[i] = v[i];
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int c = 0; c < W; c += (W < 16 ? W : 16)) {
+      constexpr int N = W < 16 ? W : 16;
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        float lo, hi;
+        unpack2(acc[c / 2 + i], lo, hi);
+        w[i] = pack_bf16x2(lo, hi);
+      }
+      uint16_t *o = reinterpret_cast<uint16_t *>(d) + c;
+      if (N == 16 && wide && c + 16 <= n) {
+        st_global_v8(o, w);
+      } else {
+#pragma unroll
+        for (int g = 0; g < N; g += 8) {
+          if (c + g + 8 <= n) {
+            *reinterpret_cast<uint4 *>(o + g) = make_uint4(w[g / 2], w[g / 2 + 1], w[g / 2 + 2], w[g / 2 + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c + g + i < n) o[g + i] = static_cast<uint16_t>(w[(g + i) / 2] >> (16 * (i & 1)));
+          }
+        }
+      }
+    }
+    return;
+  }
+  const uint32_t rows = __ballot_sync(0xFFFFFFFFu, in);
+  const int64_t at0 = __shfl_sync(0xFFFFFFFFu, at, 0);  // lane 0's row; the others follow at ldd
+#pragma unroll
+  for (int c = 0; c < W; c += 16) {
+    constexpr int N = W < 16 ? W : 16;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float lo, hi;
+      unpack2(acc[(c + i) / 2], lo, hi);
+      turn[lane * 17 + i] = lo;
+      turn[lane * 17 + i + 1] = hi;
+    }
+    __syncwarp();
+    const int j = lane & 15;
+    if (c + j < n && j < N) {
+#pragma unroll 4
+      for (int r = lane >> 4; r < 32; r += 2)
+        if (rows >> r & 1) store_one(a, at0 + r * a.ldd + c + j, turn[r * 17 + j]);
+    }
   }
 }
 
@@ -300,8 +345,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   int *bad = issued_count + 1;
   Tables tb;
   tb.ro = reinterpret_cast<int *>(ctrl + C::CTRL);
-  tb.tp = tb.ro + kMaxExperts + 4;
-  tb.kb = tb.tp + kMaxExperts + 4;
+  tb.tp = tb.kb = tb.ro + kMaxExperts + 4;
+  float *turn = reinterpret_cast<float *>(ctrl + C::CTRL + C::TABLE);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   constexpr bool SPLIT = C::MODE == kDense && C::SWAP;
@@ -356,8 +401,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
         if (e < a.experts) {
-          tb.tp[e + 1] = tiles + nt;
-          tb.kb[e + 1] = blocks + nb;
+          if (C::MODE == kGrouped) tb.tp[e + 1] = tiles + nt;
+          else tb.kb[e + 1] = blocks + nb;
         }
         tiles += __shfl_sync(0xFFFFFFFFu, nt, 31);
         blocks += __shfl_sync(0xFFFFFFFFu, nb, 31);
@@ -586,8 +631,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       if (!ok || splits > 1) continue;
       const int p = t.p0 + quad * 32 + lane, q = t.q0 + half * C::W;
-      if (p < t.p_end) {
-        if constexpr (C::SWAP) {
+      if constexpr (C::SWAP) {
+        if (p < t.p_end) {
           const int64_t at = static_cast<int64_t>(q) * a.ldd + p;
 #pragma unroll
           for (int i = 0; i < C::W; ++i) {
@@ -595,9 +640,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             unpack2(acc[i / 2], lo, hi);
             if (q + i < t.q_end) store_one(a, at + i * a.ldd, (i & 1) ? hi : lo);
           }
-        } else {
-          store_row<C::W>(a, t.expert * a.d_expert + static_cast<int64_t>(p) * a.ldd + q, t.q_end - q, acc);
         }
+      } else {
+        store_rows<C::W>(a, t.expert * a.d_expert + static_cast<int64_t>(p) * a.ldd + q, t.q_end - q, p < t.p_end,
+                         turn + (warp - 4) * 32 * 17, lane, acc);
       }
     }
   }

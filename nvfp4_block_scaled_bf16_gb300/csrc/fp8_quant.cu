@@ -3,8 +3,8 @@
 //
 // A block with largest magnitude amax (at least 2^-100) has scale s = fl(amax / 448) and codes
 // e4m3(fl(x * fl(448 / amax))): every step is one fp32 rounding to nearest even, so the codes are the same
-// wherever a block is quantised.  Magnitudes are compared as integers (the bits of |x|), in which NaN lies above
-// infinity: a block that holds either gets a scale and codes that stand for nothing finite.
+// wherever a block is quantised.  A NaN outweighs
+// every magnitude: a block that holds one, or an infinity, gets a scale and codes that stand for nothing finite.
 //
 // All of it is bound by memory: a value is read once (2 or 4 bytes) and written once or twice (1 byte each).
 #include "host.h"
@@ -16,6 +16,33 @@ namespace {
 constexpr int kQuantThreads = 256;
 constexpr int kMaxQuantExperts = 1024;
 constexpr uint32_t kTinyBits = 27u << 23;  // 2^-100
+
+// The larger magnitude, NaN above all; the sign of the result means nothing.  fp32, or two bf16 to a word.
+template <bool F32>
+__device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (F32) {
+    float f;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    r = __float_as_uint(f);
+  } else {
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  }
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float f) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(f));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
 
 // Sixteen consecutive values of a row, as loaded.
 template <bool F32>
@@ -54,17 +81,18 @@ struct Vals {
   }
   // the bits of the largest magnitude, as fp32
   __device__ __forceinline__ uint32_t amax() const {
-    if constexpr (F32) {
-      uint32_t m = 0;
+    uint32_t m = w[0];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
-      return m;
-    } else {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-      return max(m & 0xFFFF0000u, m << 16);
-    }
+    for (int i = 1; i < (F32 ? 16 : 8); ++i) m = mag_max<F32>(m, w[i]);
+    if constexpr (F32) return m & 0x7FFFFFFFu;
+    return mag_max<true>(m & 0xFFFF0000u, m << 16) & 0x7FFFFFFFu;
+  }
+  // values 2 i and 2 i + 1, as a pair
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    uint64_t r;
+    if constexpr (F32) asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(w[2 * i]), "r"(w[2 * i + 1]));
+    else asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(w[i] << 16), "r"(w[i] & 0xFFFF0000u));
+    return r;
   }
 };
 
@@ -74,22 +102,29 @@ __device__ __forceinline__ void divided(uint32_t amax_bits, float &scale, float 
   factor = __fdiv_rn(448.0f, a);
 }
 
-// Two fp32 -> two e4m3 codes (RNE, saturating; NaN stays NaN), `lo` in the low byte.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t h;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
-  return h;
-}
+// Four fp32 -> four e4m3 codes (RNE, saturating; NaN stays NaN), in byte order.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+      " mov.b32 %0, {lo, hi};\n}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
+// The codes of a row's sixteen values under factor f.
 template <bool F32>
 __device__ __forceinline__ uint4 codes16(const Vals<F32> &v, float f) {
+  const uint64_t f2 = both(f);
   uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = e4m3x4(__fmul_rn(v.at(4 * i), f), __fmul_rn(v.at(4 * i + 1), f), __fmul_rn(v.at(4 * i + 2), f),
-                  __fmul_rn(v.at(4 * i + 3), f));
+  for (int i = 0; i < 4; ++i) {
+    float y[4];
+    split(mul_pair(v.pair(2 * i), f2), y[0], y[1]);
+    split(mul_pair(v.pair(2 * i + 1), f2), y[2], y[3]);
+    o[i] = e4m3x4(y[0], y[1], y[2], y[3]);
+  }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -160,14 +195,33 @@ struct TileArgs {
   unsigned int *status;
 };
 
-// A warp holds 16 rows of the tile, a thread 4 rows x 16 columns.  The codes along the columns go through shared
-// memory, four rows of a column to a word; the word's place is turned by its column group, so that the 32 lanes'
-// words fall into 32 banks, and a column's 128 bytes leave as eight 16-byte stores side by side.
+// One thread's part of a lane-transposed maximum: N values in each of the lanes that differ in the bits lo .. 2 lo ..
+// (log2 N of them) come back as one value a lane, the maximum over those lanes of value
+// (lane / lo) mod N with its bits reversed; an exchange halves the values that a lane still holds.
+template <bool F32, int N>
+__device__ __forceinline__ void exchange_max(uint32_t (&v)[N], int keep, int mask, int lane) {
+  const bool up = (lane & mask) != 0;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    if (i < keep) {
+      const uint32_t send = up ? v[i] : v[i + keep], mine = up ? v[i + keep] : v[i];
+      v[i] = mag_max<F32>(mine, __shfl_xor_sync(0xFFFFFFFFu, send, mask));
+    }
+  }
+}
+
+// A warp holds 16 rows of the tile, a thread 4 rows x 16 columns (lane: column group cg = lane mod 8, row group
+// rg = lane / 8).  The codes along the columns go through shared memory, four rows of a column to a word; the
+// word's place is turned by its column group, so that the 32 lanes' words fall into 32 banks, and a column's 128
+// bytes leave as eight 16-byte stores side by side.  A division for a row's scale or factor is done by one of the
+// eight lanes that share the row.
 template <bool F32, int ALONG>
-__global__ void __launch_bounds__(kQuantThreads) fp8_tile_kernel(const TileArgs a) {
-  __shared__ uint32_t s_max[8][F32 ? 128 : 64];
+__global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_tile_kernel(const TileArgs a) {
+  constexpr int NW = F32 ? 16 : 8;  // words of a thread's 16 columns
+  __shared__ uint32_t s_max[8][8 * NW];
   __shared__ __align__(16) float s_fac[128];
-  __shared__ __align__(16) uint32_t s_t[128 * 32];
+  __shared__ __align__(16) uint32_t s_t[2][128 * 32];
+  __shared__ int s_scan[8];
   __shared__ int s_row0, s_rows;
   pdl_trigger();
   pdl_wait();
@@ -181,56 +235,58 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_tile_kernel(const TileArgs 
     row0 = mat * a.m + mblk * 128;
     rows = min(static_cast<int64_t>(128), a.m - mblk * 128);
   } else if (a.row_offsets) {
-    // the expert whose padded rows hold this block: a warp's running sum over the experts
-    if (warp == 0) {
-      int64_t first = 0;  // first block of expert e0
-      bool found = false, bad = false;
-      if (lane == 0) s_rows = 0;
-      __syncwarp();
-      for (int e0 = 0; e0 < a.experts && !found; e0 += 32) {
-        const int e = e0 + lane;
-        int64_t lo = 0, hi = 0;
-        if (e < a.experts) {
-          lo = a.row_offsets[e];
-          hi = a.row_offsets[e + 1];
-        }
+    // the expert whose padded rows hold this block: a running sum over the experts, 256 at a time
+    if (tid == 0) s_rows = 0;
+    int64_t first = 0;
+    bool bad = false;
+    for (int e0 = 0; e0 < a.experts; e0 += kQuantThreads) {
+      const int e = e0 + tid;
+      int64_t lo = 0, hi = 0;
+      if (e < a.experts) {
+        lo = a.row_offsets[e];
+        hi = a.row_offsets[e + 1];
         bad = bad || lo < 0 || hi < lo || hi > a.m || (e == 0 && lo != 0);
-        if (__any_sync(0xFFFFFFFFu, bad)) break;
-        const int nb = static_cast<int>((hi - lo + 127) / 128);
-        int incl = nb;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-          if (lane >= o) incl += n;
-        }
-        const int64_t mine = first + incl - nb;
-        const bool here = nb > 0 && blk >= mine && blk < mine + nb;
-        if (here) {
-          s_row0 = static_cast<int>(lo + (blk - mine) * 128);
-          s_rows = static_cast<int>(min(static_cast<int64_t>(128), hi - lo - (blk - mine) * 128));
-        }
-        found = __any_sync(0xFFFFFFFFu, here);
-        first += __shfl_sync(0xFFFFFFFFu, incl, 31);
       }
-      if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(a.status, 2u);
+      const int nb = bad ? 0 : static_cast<int>((hi - lo + 127) / 128);
+      int incl = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += n;
+      }
+      if (lane == 31) s_scan[warp] = incl;
+      __syncthreads();
+      int before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const int n = s_scan[w];
+        before += w < warp ? n : 0;
+        all += n;
+      }
+      const int64_t mine = first + before + incl - nb;
+      if (nb > 0 && blk >= mine && blk < mine + nb) {
+        s_row0 = static_cast<int>(lo + (blk - mine) * 128);
+        s_rows = static_cast<int>(min(static_cast<int64_t>(128), hi - lo - (blk - mine) * 128));
+      }
+      first += all;
+      __syncthreads();
     }
-    __syncthreads();
+    const bool any_bad = __syncthreads_or(bad);
+    if (any_bad && tid == 0 && blk == 0 && blockIdx.y == 0) atomicOr(a.status, 2u);
     row0 = s_row0;
-    rows = s_rows;  // 0: past the last expert (or malformed offsets): the block is written as zeros
+    rows = any_bad ? 0 : s_rows;  // 0: past the last expert (or malformed offsets): the block is written as zeros
     if (rows == 0) row0 = 0;
   } else {
     row0 = blk * 128;
     rows = min(static_cast<int64_t>(128), a.m - row0);
   }
   // this thread's four rows
+  const int r0 = warp * 16 + rg * 4;
   const uint8_t *xp[4];
-  bool in[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = warp * 16 + rg * 4 + i;
-    in[i] = r < rows;
-    int64_t xr = in[i] ? row0 + r : 0;
-    if (ALONG != kBlock && a.src && in[i]) {
+    int64_t xr = r0 + i < rows ? row0 + r0 + i : -1;
+    if (ALONG != kBlock && a.src && xr >= 0) {
       xr = a.src[xr];
       if (xr < 0 || xr >= a.x_rows) {
         if (blockIdx.y == 0 && cg == 0) atomicOr(a.status, 8u);
@@ -239,119 +295,122 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_tile_kernel(const TileArgs 
     }
     xp[i] = xr < 0 ? nullptr : static_cast<const uint8_t *>(a.x) + (xr * a.ldx + cg * 16) * (F32 ? 4 : 2);
   }
-  Vals<F32> v[4];
-  auto load = [&](int b) {
-    const int c = b * 128;
+  const int b0 = blockIdx.y * a.chain, b1 = min(a.kb, b0 + a.chain);
+  for (int b = b0; b < b1; ++b) {
+    const int c0 = b * 128;
+    const bool in_k = c0 + cg * 16 < a.k;
+    Vals<F32> v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[i].zero();
-      if (in[i] && xp[i] && c + cg * 16 < a.k) {
-        const uint8_t *p = xp[i] + static_cast<int64_t>(c) * (F32 ? 4 : 2);
+      if (xp[i] && in_k) {
+        const uint8_t *p = xp[i] + static_cast<int64_t>(c0) * (F32 ? 4 : 2);
         if (a.wide) v[i].load(p);
         else v[i].load16(p);
       }
     }
-  };
-  const int b0 = blockIdx.y * a.chain, b1 = min(a.kb, b0 + a.chain);
-  for (int b = b0; b < b1; ++b) {
-    load(b);
-    const int c0 = b * 128;
     float fb = 0.0f;  // kBlock: the tile's factor
     if constexpr (ALONG == kBlock) {
       uint32_t am = max(max(v[0].amax(), v[1].amax()), max(v[2].amax(), v[3].amax()));
       am = __reduce_max_sync(0xFFFFFFFFu, am);
-      if (lane == 0) s_max[warp][0] = am;
+      if (lane == 0) s_max[warp][b & 1] = am;
       __syncthreads();
       am = 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) am = max(am, s_max[w][0]);
-      float s;
-      divided(am, s, fb);
+      for (int w = 0; w < 8; ++w) am = max(am, s_max[w][b & 1]);
+      const float top = __uint_as_float(max(am, kTinyBits));
+      fb = __fdiv_rn(448.0f, top);
       if (tid == 0) {
+        const float s = __fdiv_rn(top, 448.0f);
         a.sf[(mat * a.row_blocks + mblk) * a.kb + b] = s;
         if (a.qt) a.sft[(mat * a.kb + b) * a.row_blocks + mblk] = s;
       }
     }
-    if constexpr (ALONG != kColumns) {
+    float fr[4] = {fb, fb, fb, fb};  // the rows' factors
+    if constexpr (ALONG == kBoth) {
+      // largest magnitudes of the four rows over their eight lanes: lane cg ends with row 2 (cg bit 0) + (cg bit 1)
+      uint32_t am[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f = fb;
-        if constexpr (ALONG == kBoth) {
-          uint32_t am = v[i].amax();
+      for (int i = 0; i < 4; ++i) am[i] = v[i].amax();
+      exchange_max<true>(am, 2, 1, lane);
+      exchange_max<true>(am, 1, 2, lane);
+      const uint32_t m = mag_max<true>(am[0], __shfl_xor_sync(0xFFFFFFFFu, am[0], 4)) & 0x7FFFFFFFu;
+      const float top = __uint_as_float(max(m, kTinyBits));
+      // lanes 0 to 3 of the eight divide for the scales, 4 to 7 for the factors
+      const float d = __fdiv_rn((cg & 4) ? 448.0f : top, (cg & 4) ? top : 448.0f);
+      const int row = 2 * (cg & 1) + ((cg >> 1) & 1);
+      if (cg < 4 && r0 + row < rows) a.sf[static_cast<int64_t>(b) * a.m + row0 + r0 + row] = d;
 #pragma unroll
-          for (int o = 1; o < 8; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-          float s;
-          divided(am, s, f);
-          if (in[i] && cg == 0) a.sf[static_cast<int64_t>(b) * a.m + row0 + warp * 16 + rg * 4 + i] = s;
-        }
-        if (in[i] && c0 + cg * 16 < a.k)
-          *reinterpret_cast<uint4 *>(a.q + (row0 + warp * 16 + rg * 4 + i) * a.k + c0 + cg * 16) = codes16<F32>(v[i], f);
-      }
+      for (int i = 0; i < 4; ++i) fr[i] = __shfl_sync(0xFFFFFFFFu, d, (lane & 24) | 4 | (i >> 1) | ((i & 1) << 1));
     }
-    float f[16];
-    if constexpr (ALONG == kBlock) {
-      if (!a.qt) {
-        __syncthreads();  // s_max is written again by the next tile
-        continue;
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) f[j] = fb;
-    } else {
+    const bool turned = ALONG != kBlock || a.qt != nullptr;
+    if constexpr (ALONG != kBlock) {
       // largest magnitude of each column: over the thread's rows, the warp's four row groups, the warps
-      constexpr int NW = F32 ? 16 : 8;
+      uint32_t am[NW];
 #pragma unroll
-      for (int j = 0; j < NW; ++j) {
-        uint32_t am = 0;
+      for (int j = 0; j < NW; ++j)
+        am[j] = mag_max<F32>(mag_max<F32>(v[0].w[j], v[1].w[j]), mag_max<F32>(v[2].w[j], v[3].w[j]));
+      exchange_max<F32>(am, NW / 2, 8, lane);
+      exchange_max<F32>(am, NW / 4, 16, lane);
+      // rg bit 0 chose the upper half of the words, bit 1 the upper half of that
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (F32) am = max(am, v[i].w[j] & 0x7FFFFFFFu);
-          else am = __vmaxu2(am, v[i].w[j] & 0x7FFF7FFFu);
-        }
-#pragma unroll
-        for (int o = 8; o < 32; o <<= 1) {
-          const uint32_t n = __shfl_xor_sync(0xFFFFFFFFu, am, o);
-          if constexpr (F32) am = max(am, n);
-          else am = __vmaxu2(am, n);
-        }
-        if (rg == 0) s_max[warp][cg * NW + j] = am;
-      }
+      for (int j = 0; j < NW / 4; ++j) s_max[warp][cg * NW + (rg & 1) * (NW / 2) + (rg >> 1) * (NW / 4) + j] = am[j];
       __syncthreads();
       if (tid < 128) {
-        uint32_t am = 0;
-        if constexpr (F32) {
+        uint32_t m = 0;
 #pragma unroll
-          for (int w = 0; w < 8; ++w) am = max(am, s_max[w][tid]);
-        } else {
-#pragma unroll
-          for (int w = 0; w < 8; ++w) am = __vmaxu2(am, s_max[w][tid / 2]);
-          am = (tid & 1) ? (am & 0xFFFF0000u) : (am << 16);
-        }
+        for (int w = 0; w < 8; ++w) m = mag_max<F32>(m, s_max[w][F32 ? tid : tid / 2]);
+        if constexpr (!F32) m = (tid & 1) ? (m & 0xFFFF0000u) : (m << 16);
         float s, fc;
-        divided(am, s, fc);
+        divided(m & 0x7FFFFFFFu, s, fc);
         s_fac[tid] = fc;
         if (c0 + tid < a.k) a.sft[blk * a.k + c0 + tid] = s;
       }
       __syncthreads();
+    }
+    // four columns at a time: their part of the rows' codes, and the four rows of each column's
+    uint32_t *turn = s_t[b & 1];
+    uint32_t o[4][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 t = *reinterpret_cast<const float4 *>(&s_fac[cg * 16 + 4 * j]);
-        f[4 * j] = t.x;
-        f[4 * j + 1] = t.y;
-        f[4 * j + 2] = t.z;
-        f[4 * j + 3] = t.w;
+    for (int g = 0; g < 4; ++g) {
+      uint64_t x[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i][0] = v[i].pair(2 * g);
+        x[i][1] = v[i].pair(2 * g + 1);
+        if constexpr (ALONG != kColumns) {
+          float y[4];
+          split(mul_pair(x[i][0], both(fr[i])), y[0], y[1]);
+          split(mul_pair(x[i][1], both(fr[i])), y[2], y[3]);
+          o[i][g] = e4m3x4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      if (turned) {
+        ulonglong2 f = make_ulonglong2(both(fb), both(fb));  // the columns' factors
+        if constexpr (ALONG != kBlock) f = *reinterpret_cast<const ulonglong2 *>(&s_fac[cg * 16 + 4 * g]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float lo[4], hi[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) split(mul_pair(x[i][j], j ? f.y : f.x), lo[i], hi[i]);
+          const int c = cg * 16 + 4 * g + 2 * j;
+          turn[c * 32 + ((warp * 4 + rg) ^ (cg * 4))] = e4m3x4(lo[0], lo[1], lo[2], lo[3]);
+          turn[(c + 1) * 32 + ((warp * 4 + rg) ^ (cg * 4))] = e4m3x4(hi[0], hi[1], hi[2], hi[3]);
+        }
       }
     }
+    if constexpr (ALONG != kColumns) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t w = e4m3x4(__fmul_rn(v[0].at(j), f[j]), __fmul_rn(v[1].at(j), f[j]), __fmul_rn(v[2].at(j), f[j]),
-                                __fmul_rn(v[3].at(j), f[j]));
-      s_t[(cg * 16 + j) * 32 + ((warp * 4 + rg) ^ (cg * 4))] = w;
+      for (int i = 0; i < 4; ++i)
+        if (r0 + i < rows && in_k)
+          *reinterpret_cast<uint4 *>(a.q + (row0 + r0 + i) * a.k + c0 + cg * 16) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
     }
-    __syncthreads();
+    if (!turned) continue;
+    __syncthreads();  // (the other of the two is written next, and this one again two tiles on, behind its barriers)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = i * 32 + tid / 8, ch = tid % 8;  // column, 16-byte piece of its 128 rows
-      const uint4 w = *reinterpret_cast<const uint4 *>(&s_t[c * 32 + ((ch * 4) ^ ((c / 16) * 4))]);
+      const uint4 w = *reinterpret_cast<const uint4 *>(&turn[c * 32 + ((ch * 4) ^ ((c / 16) * 4))]);
       if (c0 + c < a.k) {
         if constexpr (ALONG == kBlock) {
           if (mblk * 128 + ch * 16 < a.m)
@@ -361,7 +420,6 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_tile_kernel(const TileArgs 
         }
       }
     }
-    __syncthreads();
   }
 }
 
@@ -384,7 +442,7 @@ int wide_rows(const void *x, int x_type, int64_t ldx) {
 template <int ALONG>
 cudaError_t launch_tiles(int x_type, TileArgs &a, int64_t blocks, const DeviceInfo &dev, uint32_t flags, nvfp4_stream_t s) {
   // tiles that a CTA takes in turn: one while that fills the device, then as many as leave it four rounds
-  const int64_t tiles = blocks * a.kb, want = static_cast<int64_t>(dev.sm_count) * 16;
+  const int64_t tiles = blocks * a.kb, want = static_cast<int64_t>(dev.sm_count) * 8;
   int64_t chain = tiles / want;
   chain = chain < 1 ? 1 : chain > 8 ? 8 : chain;
   a.chain = static_cast<int>(chain);
