@@ -9,7 +9,6 @@ libnvfp4.so is missing (build it with ``python nvfp4_block_scaled_bf16_gb300/bui
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -182,11 +181,6 @@ def _scratch(nbytes: int, device, stream):
         return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
     with _on(stream):
         return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
-
-
-def _on_made(stream):
-    """A context for outputs that are made for the launch stream: their memory then belongs to it (see _contig)."""
-    return contextlib.nullcontext() if stream is None else _on(stream)
 
 
 def sf_bytes(rows: int, k: int, sf_vec: int = 16) -> int:
@@ -851,21 +845,27 @@ def _type_of(t, name):
     return xt
 
 
-def _dense(t, dtype, name, shape):
-    """A contiguous tensor of this shape on the current device."""
+def _dense(t, dtype, name, shape, dev):
+    """A contiguous tensor of this type and shape on device `dev`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
     _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _made(t, dtype, name, shape, like):
-    """The output tensor `t`, or a new one."""
-    if t is None:
-        return like.new_empty(shape, dtype=dtype)
-    _dense(t, dtype, name, shape)
-    return t
+def _made(t, dtype, name, shape, dev, stream):
+    """The output tensor `t`, or a new one (made for the launch stream, so that its memory belongs to it: see _contig)."""
+    if t is not None:
+        _dense(t, dtype, name, shape, dev.index if dev.index is not None else -1)
+        return t
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def fp8_padded_rows(rows: int, experts: int = 0) -> int:
@@ -885,16 +885,17 @@ def fp8_quantize(x, src_rows=None, row_offsets=None, rows: bool = True, transpos
     xt = _type_of(x, "x")
     if x.dim() != 2:
         raise ValueError("x must have 2 dimensions")
-    if not rows and not transpose:
-        raise ValueError("rows or transpose: one at least")
     n, k = x.shape
+    dev = x.device
     ldx = _rows(x, x.dtype, "x", n, k, x.get_device())
     m, experts = n, 0
+    src_p = ro_p = q_p = sf_p = qt_p = sft_p = None
     if src_rows is not None:
         _need(src_rows, torch.int32, "src_rows", 1)
         if not src_rows.is_contiguous():
             raise ValueError("src_rows must be contiguous")
         m = src_rows.numel()
+        src_p = src_rows.data_ptr()
     if row_offsets is not None:
         if not transpose:
             raise ValueError("row_offsets belong to transpose")
@@ -902,22 +903,25 @@ def fp8_quantize(x, src_rows=None, row_offsets=None, rows: bool = True, transpos
         if not row_offsets.is_contiguous() or row_offsets.numel() < 2:
             raise ValueError("row_offsets must be contiguous and hold at least two entries")
         experts = row_offsets.numel() - 1
-    kb, out = -(-k // 128), ()
-    with _on_made(stream):
-        if rows:
-            q, sf = _made(q, E4M3, "q", (m, k), x), _made(sf, torch.float32, "sf", (kb, m), x)
-            out += (q, sf)
-        elif q is not None or sf is not None:
-            raise ValueError("q and sf belong to rows")
-        if transpose:
-            p = fp8_padded_rows(m, experts)
-            qt, sft = _made(qt, E4M3, "qt", (k, p), x), _made(sft, torch.float32, "sft", (p // 128, k), x)
-            out += (qt, sft)
-        elif qt is not None or sft is not None:
-            raise ValueError("qt and sft belong to transpose")
-    _check(_lib.fp8_quantize(_ptr(x), xt, n, k, ldx, _ptr(src_rows), m, _ptr(row_offsets), experts, _ptr(q), _ptr(sf),
-                             _ptr(qt), _ptr(sft), flags, _stream(stream)))
-    return out
+        ro_p = row_offsets.data_ptr()
+    if rows:
+        q = _made(q, E4M3, "q", (m, k), dev, stream)
+        sf = _made(sf, torch.float32, "sf", (-(-k // 128), m), dev, stream)
+        q_p, sf_p = q.data_ptr(), sf.data_ptr()
+    elif not transpose:
+        raise ValueError("rows or transpose: one at least")
+    elif q is not None or sf is not None:
+        raise ValueError("q and sf belong to rows")
+    if transpose:
+        p = -(-m // 128) + experts
+        qt = _made(qt, E4M3, "qt", (k, 128 * p), dev, stream)
+        sft = _made(sft, torch.float32, "sft", (p, k), dev, stream)
+        qt_p, sft_p = qt.data_ptr(), sft.data_ptr()
+    elif qt is not None or sft is not None:
+        raise ValueError("qt and sft belong to transpose")
+    _check(_lib.fp8_quantize(x.data_ptr(), xt, n, k, ldx, src_p, m, ro_p, experts, q_p, sf_p, qt_p, sft_p, flags,
+                             _stream(stream)))
+    return (q, sf, qt, sft) if rows and transpose else (q, sf) if rows else (qt, sft)
 
 
 def fp8_quantize_weight(w, transpose: bool = False, q=None, sf=None, qt=None, sft=None, flags: int = 0, stream=None):
@@ -937,29 +941,28 @@ def fp8_quantize_weight(w, transpose: bool = False, q=None, sf=None, qt=None, sf
         ldw = k
     else:
         ldw = _rows(w, w.dtype, "w", n, k, w.get_device())
-    nb, kb = -(-n // 128), -(-k // 128)
-    with _on_made(stream):
-        q, sf = _made(q, E4M3, "q", lead + (n, k), w), _made(sf, torch.float32, "sf", lead + (nb, kb), w)
-        if transpose:
-            qt, sft = _made(qt, E4M3, "qt", lead + (k, n), w), _made(sft, torch.float32, "sft", lead + (kb, nb), w)
-        elif qt is not None or sft is not None:
-            raise ValueError("qt and sft belong to transpose")
-    _check(_lib.fp8_quantize_weight(_ptr(w), wt, matrices, n, k, ldw, _ptr(q), _ptr(sf), _ptr(qt), _ptr(sft), flags,
-                                    _stream(stream)))
+    nb, kb, dev = -(-n // 128), -(-k // 128), w.device
+    q, sf = _made(q, E4M3, "q", lead + (n, k), dev, stream), _made(sf, torch.float32, "sf", lead + (nb, kb), dev, stream)
+    if transpose:
+        qt = _made(qt, E4M3, "qt", lead + (k, n), dev, stream)
+        sft = _made(sft, torch.float32, "sft", lead + (kb, nb), dev, stream)
+    elif qt is not None or sft is not None:
+        raise ValueError("qt and sft belong to transpose")
+    _check(_lib.fp8_quantize_weight(w.data_ptr(), wt, matrices, n, k, ldw, q.data_ptr(), sf.data_ptr(), _ptr(qt), _ptr(sft),
+                                    flags, _stream(stream)))
     return (q, sf, qt, sft) if transpose else (q, sf)
 
 
-def _product_out(d, out_dtype, accumulate, shape, like, stream):
+def _product_out(d, out_dtype, accumulate, shape, dev, stream):
     """(d, its NVFP4_DTYPE_*)."""
     if d is not None:
-        out_dtype = d.dtype
+        out_dtype = d.dtype if isinstance(d, torch.Tensor) else None
     elif accumulate:
         raise ValueError("accumulate needs d")
     dt = _STREAM_TYPES.get(out_dtype)
     if dt is None:
         raise TypeError(f"the result must be bfloat16 or float32, got {out_dtype}")
-    with _on_made(stream):
-        return _made(d, out_dtype, "d", shape, like), dt
+    return _made(d, out_dtype, "d", shape, dev, stream), dt
 
 
 def fp8_gemm(a, sfa, b, sfb, block_b: int = 128, out_dtype=torch.bfloat16, d=None, accumulate: bool = False, flags: int = 0,
@@ -970,19 +973,19 @@ def fp8_gemm(a, sfa, b, sfb, block_b: int = 128, out_dtype=torch.bfloat16, d=Non
     _need(a, E4M3, "a", 2)
     _need(b, E4M3, "b", 2)
     m, k = a.shape
-    n = b.shape[0]
-    if b.shape[1] != k:
+    n, kb = b.shape
+    if kb != k:
         raise ValueError("a and b disagree on K")
     if block_b not in (1, 128):
         raise ValueError(f"block_b must be 1 or 128, got {block_b}")
-    kb = -(-k // 128)
-    _dense(a, E4M3, "a", (m, k))
-    _dense(b, E4M3, "b", (n, k))
-    _dense(sfa, torch.float32, "sfa", (kb, m))
-    _dense(sfb, torch.float32, "sfb", (-(-n // 128), kb) if block_b == 128 else (kb, n))
-    d, dt = _product_out(d, out_dtype, accumulate, (m, n), a, stream)
-    _check(_lib.fp8_gemm(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), block_b, _ptr(d), dt, int(accumulate), m, n, k, flags,
-                         _stream(stream)))
+    if not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("a and b must be contiguous")
+    kb, dev = -(-k // 128), a.get_device()
+    _dense(sfa, torch.float32, "sfa", (kb, m), dev)
+    _dense(sfb, torch.float32, "sfb", (-(-n // 128), kb) if block_b == 128 else (kb, n), dev)
+    d, dt = _product_out(d, out_dtype, accumulate, (m, n), a.device, stream)
+    _check(_lib.fp8_gemm(a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), block_b, d.data_ptr(), dt,
+                         1 if accumulate else 0, m, n, k, flags, _stream(stream)))
     return d
 
 
@@ -992,20 +995,19 @@ def fp8_grouped_gemm(a, sfa, row_offsets, b, sfb, out_dtype=torch.bfloat16, d=No
     expert's stay as they were."""
     _need(a, E4M3, "a", 2)
     _need(b, E4M3, "b", 3)
-    _need(row_offsets, torch.int64, "row_offsets", 1)
     t, k = a.shape
-    experts, n, kb_ = b.shape
-    if kb_ != k or row_offsets.numel() != experts + 1:
-        raise ValueError("shape mismatch")
-    kb = -(-k // 128)
-    _dense(a, E4M3, "a", (t, k))
-    _dense(b, E4M3, "b", (experts, n, k))
-    _dense(row_offsets, torch.int64, "row_offsets", (experts + 1,))
-    _dense(sfa, torch.float32, "sfa", (kb, t))
-    _dense(sfb, torch.float32, "sfb", (experts, -(-n // 128), kb))
-    d, dt = _product_out(d, out_dtype, False, (t, n), a, stream)
-    _check(_lib.fp8_grouped_gemm(_ptr(a), _ptr(sfa), _ptr(row_offsets), experts, _ptr(b), _ptr(sfb), _ptr(d), dt, t, n, k,
-                                 flags, _stream(stream)))
+    experts, n, kb = b.shape
+    if kb != k:
+        raise ValueError("a and b disagree on K")
+    if not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("a and b must be contiguous")
+    kb, dev = -(-k // 128), a.get_device()
+    _dense(row_offsets, torch.int64, "row_offsets", (experts + 1,), dev)
+    _dense(sfa, torch.float32, "sfa", (kb, t), dev)
+    _dense(sfb, torch.float32, "sfb", (experts, -(-n // 128), kb), dev)
+    d, dt = _product_out(d, out_dtype, False, (t, n), a.device, stream)
+    _check(_lib.fp8_grouped_gemm(a.data_ptr(), sfa.data_ptr(), row_offsets.data_ptr(), experts, b.data_ptr(), sfb.data_ptr(),
+                                 d.data_ptr(), dt, t, n, k, flags, _stream(stream)))
     return d
 
 
@@ -1019,18 +1021,17 @@ def fp8_grouped_weight_grad(a, sfa, b, sfb, row_offsets, out_dtype=torch.bfloat1
     _need(b, E4M3, "b", 2)
     _need(row_offsets, torch.int64, "row_offsets", 1)
     n, p = a.shape
-    k = b.shape[0]
-    if b.shape[1] != p:
+    k, pb = b.shape
+    if pb != p:
         raise ValueError("a and b disagree on the rows")
-    experts = row_offsets.numel() - 1
-    _dense(a, E4M3, "a", (n, p))
-    _dense(b, E4M3, "b", (k, p))
-    _dense(row_offsets, torch.int64, "row_offsets", (experts + 1,))
-    _dense(sfa, torch.float32, "sfa", (p // 128, n))
-    _dense(sfb, torch.float32, "sfb", (p // 128, k))
-    d, dt = _product_out(d, out_dtype, accumulate, (experts, n, k), a, stream)
-    _check(_lib.fp8_grouped_weight_grad(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(row_offsets), experts, _ptr(d), dt,
-                                        int(accumulate), p, n, k, flags, _stream(stream)))
+    if not a.is_contiguous() or not b.is_contiguous() or not row_offsets.is_contiguous():
+        raise ValueError("a, b and row_offsets must be contiguous")
+    experts, dev = row_offsets.numel() - 1, a.get_device()
+    _dense(sfa, torch.float32, "sfa", (p // 128, n), dev)
+    _dense(sfb, torch.float32, "sfb", (p // 128, k), dev)
+    d, dt = _product_out(d, out_dtype, accumulate, (experts, n, k), a.device, stream)
+    _check(_lib.fp8_grouped_weight_grad(a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), row_offsets.data_ptr(),
+                                        experts, d.data_ptr(), dt, 1 if accumulate else 0, p, n, k, flags, _stream(stream)))
     return d
 
 
@@ -1046,15 +1047,15 @@ def moe_combine_backward(dout, y, pos, weights, dy=None, dweights=None, flags: i
         raise ValueError("y must be contiguous")
     rows, h = y.shape
     T, topk = pos.shape
+    dev = y.device
     ldo = _rows(dout, torch.bfloat16, "dout", T, h, y.get_device())
-    if tuple(weights.shape) != (T, topk):
+    if weights.shape != (T, topk):
         raise ValueError(f"weights must have shape {(T, topk)}, got {tuple(weights.shape)}")
     pos, weights = _contig(pos, stream), _contig(weights, stream)
-    with _on_made(stream):
-        dy = _made(dy, torch.bfloat16, "dy", (rows, h), y)
-        dweights = _made(dweights, torch.float32, "dweights", (T, topk), y)
-    _check(_lib.moe_combine_backward(_ptr(dout), ldo, _ptr(y), rows, _ptr(pos), _ptr(weights), T, topk, h, _ptr(dy),
-                                     _ptr(dweights), flags, _stream(stream)))
+    dy = _made(dy, torch.bfloat16, "dy", (rows, h), dev, stream)
+    dweights = _made(dweights, torch.float32, "dweights", (T, topk), dev, stream)
+    _check(_lib.moe_combine_backward(dout.data_ptr(), ldo, y.data_ptr(), rows, pos.data_ptr(), weights.data_ptr(), T, topk, h,
+                                     dy.data_ptr(), dweights.data_ptr(), flags, _stream(stream)))
     return dy, dweights
 
 
@@ -1068,9 +1069,8 @@ def moe_gather_backward(dxs, pos, dx=None, flags: int = 0, stream=None):
     rows, h = dxs.shape
     T, topk = pos.shape
     pos = _contig(pos, stream)
-    with _on_made(stream):
-        dx = _made(dx, torch.bfloat16, "dx", (T, h), dxs)
-    _check(_lib.moe_gather_backward(_ptr(dxs), rows, _ptr(pos), T, topk, h, _ptr(dx), flags, _stream(stream)))
+    dx = _made(dx, torch.bfloat16, "dx", (T, h), dxs.device, stream)
+    _check(_lib.moe_gather_backward(dxs.data_ptr(), rows, pos.data_ptr(), T, topk, h, dx.data_ptr(), flags, _stream(stream)))
     return dx
 
 

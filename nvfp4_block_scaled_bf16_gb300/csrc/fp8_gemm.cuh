@@ -98,6 +98,13 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t pdesc, uint64_t qdes
       "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // N consecutive tensor-memory columns of the warp's 32 lanes.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
@@ -473,31 +480,34 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ products
-      if (lane == 0) {
-        int stage = 0, ab = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int u = unit; u < total && ok; u += units) {
-          const Tile t = tile_at<C>(a, tb, u);
-          int k0, k1;
-          k_range(t, k0, k1);
-          for (int kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait(smem_u32(&full[stage]), phase, wc, kSiteMmaStage)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t pd = sdesc_k_sw128(smem_u32(smem + stage * C::STAGE));
-            const uint64_t qd = sdesc_k_sw128(smem_u32(smem + stage * C::STAGE + C::P_BYTES));
+      // The whole warp keeps the loop, so that descriptors stay in uniform registers; one lane issues.
+      int stage = 0, ab = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
+      for (int u = unit; u < total && ok; u += units) {
+        const Tile t = tile_at<C>(a, tb, u);
+        int k0, k1;
+        k_range(t, k0, k1);
+        for (int kb = k0; kb < k1; ++kb) {
+          ok = mbar_wait(smem_u32(&full[stage]), phase, wc, kSiteMmaStage);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t pd = desc0 + static_cast<uint32_t>(stage * (C::STAGE >> 4));
+          const uint64_t qd = pd + (C::P_BYTES >> 4);
+          const uint32_t d = tmem + ab * C::NT;
+          if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_f8(tmem + ab * C::NT, pd + 2 * i, qd + 2 * i, C::IDESC, i > 0 ? 1u : 0u);
+            for (int i = 0; i < 4; ++i) mma_f8(d, pd + 2 * i, qd + 2 * i, C::IDESC, i > 0 ? 1u : 0u);
             tc_commit(smem_u32(&done[stage]));
-            if (++stage == C::STAGES) {
-              stage = 0;
-              phase ^= 1;
-            }
-            if (++ab == C::NACC) ab = 0;
           }
+          __syncwarp();
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+          if (++ab == C::NACC) ab = 0;
         }
       }
     } else if (warp == 2) {

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_tile_kernel(co
         if constexpr (!F32) m = (tid & 1) ? (m & 0xFFFF0000u) : (m << 16);
         float s, fc;
         divided(m & 0x7FFFFFFFu, s, fc);
-        s_fac[tid] = fc;
+        s_fac[(tid & 12) * 8 + (tid >> 4) * 4 + (tid & 3)] = fc;  // the eight column groups' fours side by side
         if (c0 + tid < a.k) a.sft[blk * a.k + c0 + tid] = s;
       }
       __syncthreads();
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_tile_kernel(co
       }
       if (turned) {
         ulonglong2 f = make_ulonglong2(both(fb), both(fb));  // the columns' factors
-        if constexpr (ALONG != kBlock) f = *reinterpret_cast<const ulonglong2 *>(&s_fac[cg * 16 + 4 * g]);
+        if constexpr (ALONG != kBlock) f = *reinterpret_cast<const ulonglong2 *>(&s_fac[g * 32 + cg * 4]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float lo[4], hi[4];
