@@ -21,6 +21,14 @@ struct Call {
 fp8::Scales row_scales(const float *p, int64_t rows) { return fp8::Scales{p, 0, 1, rows}; }
 fp8::Scales block_scales(const float *p, int64_t nk) { return fp8::Scales{p, 0, nk, 1}; }
 
+// CTAs of a cluster that share a tile's K (SWAP): as many as leave no SM without one, at most 8.
+int swap_splits(int64_t tiles, int nk, int sms) {
+  int64_t s = tiles > 0 ? sms / tiles : 1;
+  if (s > 8) s = 8;
+  if (s > nk) s = nk;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
 template <class C>
 nvfp4_status_t run(const Call &c) {
   fp8::Args args = c.args;
@@ -35,13 +43,7 @@ nvfp4_status_t run(const Call &c) {
   args.q_tiles = static_cast<int>(ceil_div(q, C::NT));
   const int64_t tiles = static_cast<int64_t>(args.p_tiles) * args.q_tiles;
   if (tiles >= (1LL << 31)) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", c.name);
-  args.splits = 1;
-  if (C::SWAP) {
-    int64_t s = tiles > 0 ? c.dev->sm_count / tiles : 1;
-    if (s > 8) s = 8;
-    if (s > args.nk) s = args.nk;
-    args.splits = s < 1 ? 1 : static_cast<int>(s);
-  }
+  args.splits = C::SWAP ? swap_splits(tiles, args.nk, c.dev->sm_count) : 1;
   return fp8::launch_gemm<C>(c.name, C::SWAP ? c.b : c.a, p, C::SWAP ? c.a : c.b, q, c.k, tiles, args, *c.dev, c.flags,
                              c.stream);
 }
@@ -55,6 +57,33 @@ template <int NT>
 nvfp4_status_t run_rows(const Call &c) {
   return c.block_b == 128 ? run<fp8::Cfg<NT, false, true, false, fp8::kDense>>(c)
                           : run<fp8::Cfg<NT, false, true, true, fp8::kDense>>(c);
+}
+
+// Tiles of more than 128 tokens, by what they cost: rounds of tiles over the SMs times the time of a tile's blocks.
+// Measured (ns a block): tokens in the lanes 280, 310 and 500 at 64, 128 and 256 columns with a scale per block of
+// B, 310, 440 and 750 with one per row; the weight in the lanes (whose K a cluster can share) 310 and 440 at 64
+// and 128 columns, and 2500 ns to join a cluster's parts.
+enum Choice { kRows64, kRows128, kRows256, kSwap64, kSwap128 };
+Choice choose(int64_t m, int64_t n, int nk, bool per_row, int sms) {
+  const int64_t rows_ns[3] = {per_row ? 310 : 280, per_row ? 440 : 310, per_row ? 750 : 500}, swap_ns[2] = {310, 440};
+  Choice best = kRows256;
+  double least = 1e300;
+  for (int i = 0; i < 5; ++i) {
+    double cost;
+    if (i < 3) {
+      const int64_t tiles = ceil_div(m, 128) * ceil_div(n, 64LL << i);
+      cost = static_cast<double>(ceil_div(tiles, sms)) * nk * rows_ns[i];
+    } else {
+      const int64_t tiles = ceil_div(n, 128) * ceil_div(m, 64LL << (i - 3));
+      const int s = swap_splits(tiles, nk, sms);
+      cost = static_cast<double>(ceil_div(tiles, sms)) * ceil_div(nk, s) * swap_ns[i - 3] + (s > 1 ? 2500 : 0);
+    }
+    if (cost < least) {
+      least = cost;
+      best = static_cast<Choice>(i);
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -80,5 +109,11 @@ extern "C" nvfp4_status_t fp8_gemm(const uint8_t *a, const float *sfa, const uin
   if (m <= 32) return run_swap<32>(c);
   if (m <= 64) return run_swap<64>(c);
   if (m <= 128) return run_swap<128>(c);
-  return run_rows<256>(c);
+  switch (choose(m, n, c.args.nk, block_b == 1, dev.sm_count)) {
+    case kRows64: return run_rows<64>(c);
+    case kRows128: return run_rows<128>(c);
+    case kSwap64: return run_swap<64>(c);
+    case kSwap128: return run_swap<128>(c);
+    default: return run_rows<256>(c);
+  }
 }

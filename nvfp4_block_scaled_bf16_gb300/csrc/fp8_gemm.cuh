@@ -37,20 +37,22 @@ struct Cfg {
   static constexpr int STAGE = P_BYTES + Q_BYTES;
   static constexpr int STAGES_FIT = 200 * 1024 / STAGE;
   static constexpr int STAGES = STAGES_FIT > 12 ? 12 : STAGES_FIT;
-  // ring of the blocks' scales; not longer than the operands', so that a block's scales never arrive at a stage's
-  // barrier before the block that had the stage before it has gone through
-  static constexpr int SLOTS = STAGES < 8 ? STAGES : 8;
+  // Ring of the blocks' scales, which are asked for LEAD blocks before they are announced.  A block's scales are
+  // announced once the block SLOTS before the last one asked for has been read, so never at a stage's barrier
+  // before the block that had the stage before it has gone through.
+  static constexpr int SLOTS = 8, LEAD = 4;
+  static_assert(STAGES >= SLOTS - LEAD, "scales would overtake operands");
   static constexpr int NACC = NT >= 256 ? 2 : 4;
   static constexpr int TMEM = NACC * NT < 32 ? 32 : NACC * NT;
   static constexpr int SW = 8;     // scaling warps (behind 4 that feed)
   static constexpr int THREADS = 128 + 32 * SW;
   static constexpr int W = NT * 4 / SW;  // columns of one scaling warp
-  static constexpr int CH = W < 32 ? W : CV && W > 64 ? 16 : 32;
+  static constexpr int CH = W <= 32 ? W / 2 : CV && W > 64 ? 16 : 32;  // columns loaded at a time
   static constexpr int SC_P = PV ? 128 : 4;
   static constexpr int SC_Q = CV ? NT : 4;
   static constexpr int SC_BYTES = (SC_P + SC_Q) * 4;
   static constexpr int TABLE = MODE == kDense ? 0 : 2 * (kMaxExperts + 4) * 4;
-  static constexpr int TURN = SWAP ? 0 : SW * 32 * 17 * 4;  // where rows of D that are not aligned are turned around
+  static constexpr int TURN = SWAP ? 0 : SW * 32 * 9 * 4;  // where rows of D that are not aligned are turned around
   static constexpr int CTRL = 1024;
   static_assert(NACC <= STAGES, "a buffer's next block must have a stage of its own");
   static constexpr int SMEM = 1024 + STAGES * STAGE + SLOTS * SC_BYTES + TABLE + TURN + CTRL;
@@ -98,6 +100,12 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t pdesc, uint64_t qdes
       "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
 }
 
+// Lane 0's arrival, without a branch.
+__device__ __forceinline__ void arrive_lane0(uint32_t bar, int lane) {
+  asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(lane)
+               : "memory");
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -116,6 +124,10 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+  } else if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
   } else {
     static_assert(N == 8, "columns");
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -152,9 +164,10 @@ __device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const float *src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
 }
-// Arrives on `bar` once this thread's copies so far have landed (an arrival the barrier counts).
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 enum Site { kSiteLoad = 0, kSiteMmaStage = 2, kSiteScaleSlot = 4, kSiteAcc = 6 };
@@ -239,7 +252,7 @@ __device__ __forceinline__ void store_one(const Args &a, int64_t at, float v) {
 
 // A warp's 32 rows (one a lane) of W columns to D, the lane's row at element `at`, `n` columns and the row `in`
 // it.  Where every row of D starts on 16 bytes a lane writes its own row, 32 bytes at a time if it can (whole
-// sectors); else 16 columns at a time are turned around through shared memory, so that 16 lanes write one row's
+// sectors); else 8 columns at a time are turned around through shared memory, so that 8 lanes write one row's
 // neighbours (one by one, a warp's store would touch 32 sectors for 4 bytes each).
 template <int W>
 __device__ __forceinline__ void store_rows(const Args &a, int64_t at, int n, bool in, float *turn, int lane,
@@ -310,22 +323,21 @@ __device__ __forceinline__ void store_rows(const Args &a, int64_t at, int n, boo
   const uint32_t rows = __ballot_sync(0xFFFFFFFFu, in);
   const int64_t at0 = __shfl_sync(0xFFFFFFFFu, at, 0);  // lane 0's row; the others follow at ldd
 #pragma unroll
-  for (int c = 0; c < W; c += 16) {
-    constexpr int N = W < 16 ? W : 16;
+  for (int c = 0; c < W; c += 8) {
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
+    for (int i = 0; i < 8; i += 2) {
       float lo, hi;
       unpack2(acc[(c + i) / 2], lo, hi);
-      turn[lane * 17 + i] = lo;
-      turn[lane * 17 + i + 1] = hi;
+      turn[lane * 9 + i] = lo;
+      turn[lane * 9 + i + 1] = hi;
     }
     __syncwarp();
-    const int j = lane & 15;
-    if (c + j < n && j < N) {
+    const int j = lane & 7;
+    if (c + j < n) {
 #pragma unroll 4
-      for (int r = lane >> 4; r < 32; r += 2)
-        if (rows >> r & 1) store_one(a, at0 + r * a.ldd + c + j, turn[r * 17 + j]);
+      for (int r = lane >> 3; r < 32; r += 4)
+        if (rows >> r & 1) store_one(a, at0 + r * a.ldd + c + j, turn[r * 9 + j]);
     }
   }
 }
@@ -363,7 +375,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 1 + 32 + C::SW);
+      mbar_init(smem_u32(&full[i]), 2 + C::SW);
       mbar_init(smem_u32(&done[i]), 1);
     }
     for (int i = 0; i < C::SLOTS; ++i) mbar_init(smem_u32(&sempty[i]), C::SW);
@@ -510,55 +522,67 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (++ab == C::NACC) ab = 0;
         }
       }
-    } else if (warp == 2) {
-      // ------------------------------------------------------------ scales
-      int slot = 0, stage = 0;
-      uint32_t phase = 0;
+    } else {
+      // ------------------------------------------------------------ scales: warp 2 even blocks, warp 3 odd ones
+      const int mine = warp - 2;
+      int i = mine;    // this warp's next block
+      int block = 0;   // the tiles' next block
       bool ok = true;
+      // block i - SLOTS has been read
+      auto slot_free = [&]() -> bool {
+        const bool is = i < C::SLOTS || mbar_wait(smem_u32(&sempty[i % C::SLOTS]), (i / C::SLOTS - 1) & 1, wc, kSiteScaleSlot);
+        return __all_sync(0xFFFFFFFFu, is);
+      };
+      // what was asked for block i - LEAD has landed: announce it
+      auto announce = [&]() {
+        cp_async_commit();
+        if (i >= C::LEAD) {
+          cp_async_wait_group<C::LEAD / 2>();
+          __syncwarp();
+          arrive_lane0(smem_u32(&full[(i - C::LEAD) % C::STAGES]), lane);
+        }
+        i += 2;
+      };
+      constexpr int NP = C::PV ? 4 : 1, NQ = C::CV ? (C::NT + 31) / 32 : 1;
       for (int u = unit; u < total && ok; u += units) {
         const Tile t = tile_at<C>(a, tb, u);
         int k0, k1;
         k_range(t, k0, k1);
-        const float *sp = a.sp.p + t.expert * a.sp.es, *sq = a.sq.p + t.expert * a.sq.es;
-        for (int kb = k0; kb < k1; ++kb) {
-          if (!mbar_wait(smem_u32(&sempty[slot]), phase ^ 1, wc, kSiteScaleSlot)) {
-            ok = false;
-            break;
-          }
-          const int64_t b = t.kb0 + kb;
-          const uint32_t dst = smem_u32(scales) + slot * C::SC_BYTES;
-          if constexpr (C::PV) {
+        // where this lane's scales of the tile's rows lie
+        const float *pp[NP], *qp[NQ];
+        bool pin[NP], qin[NQ];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = t.p0 + i * 32 + lane;
-              const bool in = r < t.p_end;
-              cp_async_4(dst + (i * 32 + lane) * 4, sp + (in ? r : t.p0 < t.p_end ? t.p0 : 0) * a.sp.rs + b * a.sp.ks, in);
-            }
-          } else if (lane == 0) {
-            const bool in = t.p0 < t.p_end;
-            cp_async_4(dst, sp + (in ? t.p0 / 128 : 0) * a.sp.rs + b * a.sp.ks, in);
-          }
-          if constexpr (C::CV) {
-#pragma unroll
-            for (int i = 0; i < (C::NT + 31) / 32; ++i) {
-              const int c = i * 32 + lane;
-              const int r = t.q0 + c;
-              const bool in = r < t.q_end;
-              if (C::NT >= 32 || c < C::NT)
-                cp_async_4(dst + (C::SC_P + c) * 4, sq + (in ? r : t.q0) * a.sq.rs + b * a.sq.ks, in);
-            }
-          } else if (lane < (C::NT + 127) / 128) {
-            const int r = t.q0 + lane * 128;
-            const bool in = r < t.q_end;
-            cp_async_4(dst + (C::SC_P + lane) * 4, sq + (in ? r / 128 : 0) * a.sq.rs + b * a.sq.ks, in);
-          }
-          cp_async_arrive(smem_u32(&full[stage]));
-          if (++stage == C::STAGES) stage = 0;
-          if (++slot == C::SLOTS) {
-            slot = 0;
-            phase ^= 1;
-          }
+        for (int j = 0; j < NP; ++j) {
+          const int r = t.p0 + j * 32 + lane;
+          pin[j] = C::PV ? r < t.p_end : lane == 0;
+          pp[j] = a.sp.p + t.expert * a.sp.es + (C::PV ? (pin[j] ? r : 0) : t.p0 / 128) * a.sp.rs + t.kb0 * a.sp.ks;
         }
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+          const int r = t.q0 + (C::CV ? j * 32 + lane : lane * 128);
+          qin[j] = r < t.q_end && (C::CV ? (C::NT >= 32 || lane < C::NT) : lane < (C::NT + 127) / 128);
+          qp[j] = a.sq.p + t.expert * a.sq.es + (C::CV ? (qin[j] ? r : 0) : (qin[j] ? r / 128 : 0)) * a.sq.rs + t.kb0 * a.sq.ks;
+        }
+        for (int kb = k0; kb < k1; ++kb, ++block) {
+          if ((block & 1) != mine) continue;
+          ok = slot_free();
+          if (!ok) break;
+          const uint32_t dst = smem_u32(scales) + (i % C::SLOTS) * C::SC_BYTES + lane * 4;
+          // (rows past the end get zeros, lanes without a row nothing)
+#pragma unroll
+          for (int j = 0; j < NP; ++j)
+            if (C::PV || lane == 0) cp_async_4(dst + j * 128, pp[j] + kb * a.sp.ks, pin[j]);
+#pragma unroll
+          for (int j = 0; j < NQ; ++j)
+            if (C::CV ? (C::NT >= 32 || lane < C::NT) : lane < (C::NT + 127) / 128)
+              cp_async_4(dst + C::SC_P * 4 + j * 128, qp[j] + kb * a.sq.ks, qin[j]);
+          announce();
+        }
+      }
+      const int end = block + C::LEAD;
+      while (ok && i < end && block > 0) {  // the last blocks
+        ok = slot_free();
+        if (ok) announce();
       }
       cp_async_wait_all();
     }
@@ -578,31 +602,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       k_range(t, k0, k1);
 #pragma unroll
       for (int i = 0; i < C::W / 2; ++i) acc[i] = 0;
-      // A block's first columns are loaded before the last columns of the block before it are added, so that the
-      // waits and the loads' latency pass while the arithmetic units have work.
+      // The barrier of the next block is tested while the last columns but one are added, and its first columns are
+      // loaded before the last are: what the test, the loads and the scale take passes while there is work.
       constexpr int CHUNKS = C::W / C::CH;
-      constexpr bool AHEAD = CHUNKS > 1;
-      uint32_t r[AHEAD ? 2 : 1][C::CH];
+      static_assert(CHUNKS >= 2 && CHUNKS % 2 == 0, "chunks");
+      uint32_t r[2][C::CH];
       float f = 0.0f;
       const float *sc = scales;
-      // waits for the block's sums (and so its scales), and starts on its columns
-      auto begin = [&]() -> bool {
-        bool here = mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc);
-        here = __all_sync(0xFFFFFFFFu, here);  // the loads below are the whole warp's
-        if (!here) return false;
+      // starts on a block whose sums (and so its scales) are there
+      auto begin = [&]() {
         tc_fence_after();
         tmem_ld<C::CH>(t_lane + ab * C::NT, r[0]);
         sc = scales + slot * (C::SC_BYTES / 4);
         f = C::PV ? sc[quad * 32 + lane] : sc[0];
         if constexpr (!C::CV) f *= sc[C::SC_P + half * C::W / 128];
-        return true;
       };
-      if (k0 < k1) ok = begin();
+      // the whole warp goes on or gives up
+      auto wait_done = [&](bool ready) {
+        if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc));
+      };
+      if (k0 < k1) {
+        wait_done(false);
+        if (ok) begin();
+      }
       for (int kb = k0; kb < k1 && ok; ++kb) {
         const uint64_t f2 = pack2(f, f);
         const float *scb = sc;
         const int slot_b = slot, ab_b = ab;
         const int next = stage + C::NACC >= C::STAGES ? stage + C::NACC - C::STAGES : stage + C::NACC;  // the buffer's next block's stage
+        const bool more = kb + 1 < k1;
+        bool ready = false;
         if (++slot == C::SLOTS) slot = 0;
         if (++ab == C::NACC) ab = 0;
         if (++stage == C::STAGES) {
@@ -611,16 +640,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
+          if (i + 1 == CHUNKS && more) wait_done(ready);
           tmem_ld_wait();
           if (i + 1 < CHUNKS) {
             tmem_ld<C::CH>(t_lane + ab_b * C::NT + (i + 1) * C::CH, r[(i + 1) & 1]);
+            if (i + 2 == CHUNKS && more) ready = mbar_try_wait(smem_u32(&done[stage]), phase);
           } else {  // the last columns are in registers: the buffer may be overwritten
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full[next]));
-            if (AHEAD && kb + 1 < k1) ok = begin();
+            arrive_lane0(smem_u32(&full[next]), lane);
+            if (more && ok) begin();
           }
-          uint32_t (&v)[C::CH] = r[AHEAD ? (i & 1) : 0];
+          uint32_t (&v)[C::CH] = r[i & 1];
           uint64_t *sum = acc + i * C::CH / 2;
           if constexpr (C::CV) {
             const ulonglong2 *cs = reinterpret_cast<const ulonglong2 *>(scb + C::SC_P + half * C::W + i * C::CH);
@@ -636,8 +666,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sempty[slot_b]));
-        if (!AHEAD && kb + 1 < k1) ok = begin();
+        arrive_lane0(smem_u32(&sempty[slot_b]), lane);
       }
       if (!ok || splits > 1) continue;
       const int p = t.p0 + quad * 32 + lane, q = t.q0 + half * C::W;
@@ -653,7 +682,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       } else {
         store_rows<C::W>(a, t.expert * a.d_expert + static_cast<int64_t>(p) * a.ldd + q, t.q_end - q, p < t.p_end,
-                         turn + (warp - 4) * 32 * 17, lane, acc);
+                         turn + (warp - 4) * 32 * 9, lane, acc);
       }
     }
   }
