@@ -178,6 +178,23 @@ nvfp4_status_t encode_tmap_stages_u8(CUtensorMap *map, const void *base, uint64_
   return NVFP4_OK;
 }
 
+nvfp4_status_t encode_tmap_store_u8(CUtensorMap *map, void *base, uint64_t row_bytes, uint64_t rows, uint64_t depth,
+                                    uint64_t row_stride_bytes, uint64_t depth_stride_bytes, uint32_t box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
+  if (!encode) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  cuuint64_t dims[3] = {row_bytes, rows, depth};
+  cuuint64_t strides[2] = {row_stride_bytes, depth_stride_bytes};
+  cuuint32_t box[3] = {128, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled (store) failed (%d) for %llu x %llu x %llu bytes", static_cast<int>(r),
+                static_cast<unsigned long long>(depth), static_cast<unsigned long long>(rows),
+                static_cast<unsigned long long>(row_bytes));
+  return NVFP4_OK;
+}
+
 int resident_blocks(const void *fn, int threads) {
   struct Entry {
     const void *fn;

@@ -35,13 +35,14 @@ struct Cfg {
   static constexpr int P_BYTES = 128 * 128;
   static constexpr int Q_BYTES = NT * 128;
   static constexpr int STAGE = P_BYTES + Q_BYTES;
-  static constexpr int STAGES_FIT = 200 * 1024 / STAGE;
+  // Wide rows of D leave through shared memory as bulk copies, so that the scaling warps go on with the next tile: a
+  // warp's 32 rows x 256 bytes.  (Stored directly, 32 rows at a time by 32 bytes each, a 128 x 256 tile took 3200
+  // cycles.)
+  static constexpr bool BULK = !SWAP && NT == 256;
+  static constexpr int STAGES_FIT = (BULK ? 147456 : 200 * 1024) / STAGE;
   static constexpr int STAGES = STAGES_FIT > 12 ? 12 : STAGES_FIT;
-  // Ring of the blocks' scales, which are asked for LEAD blocks before they are announced.  A block's scales are
-  // announced once the block SLOTS before the last one asked for has been read, so never at a stage's barrier
-  // before the block that had the stage before it has gone through.
-  static constexpr int SLOTS = 8, LEAD = 4;
-  static_assert(STAGES >= SLOTS - LEAD, "scales would overtake operands");
+  // Ring of the blocks' scales, which are asked for LEAD blocks before they are announced.
+  static constexpr int SLOTS = BULK ? 6 : 8, LEAD = BULK ? 2 : 4;
   static constexpr int NACC = NT >= 256 ? 2 : 4;
   static constexpr int TMEM = NACC * NT < 32 ? 32 : NACC * NT;
   static constexpr int SW = 8;     // scaling warps (behind 4 that feed)
@@ -52,10 +53,11 @@ struct Cfg {
   static constexpr int SC_Q = CV ? NT : 4;
   static constexpr int SC_BYTES = (SC_P + SC_Q) * 4;
   static constexpr int TABLE = MODE == kDense ? 0 : 2 * (kMaxExperts + 4) * 4;
-  static constexpr int TURN = SWAP ? 0 : SW * 32 * 9 * 4;  // where rows of D that are not aligned are turned around
-  static constexpr int CTRL = 1024;
+  static constexpr int OUT = BULK ? 8 * 8192 : 0;
+  static constexpr int TURN = SWAP || BULK ? 0 : SW * 32 * 9 * 4;  // where rows of D that are not aligned are turned around (BULK: in OUT)
+  static constexpr int CTRL = 512;
   static_assert(NACC <= STAGES, "a buffer's next block must have a stage of its own");
-  static constexpr int SMEM = 1024 + STAGES * STAGE + SLOTS * SC_BYTES + TABLE + TURN + CTRL;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + OUT + SLOTS * SC_BYTES + TABLE + TURN + CTRL;
   // f8f6f4: fp32 sums (1 at bit 4), e4m3 operands (0 at bits 7 and 10), both K-major
   static constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
                                     (static_cast<uint32_t>(128 >> 4) << 24);
@@ -78,6 +80,7 @@ struct Args {
   int p_tiles, q_tiles;      // tiles along the static operands
   int splits;                // dense with SWAP: CTAs of a cluster that share a tile's K
   int out_f32, accumulate;
+  int bulk;                  // rows of D start on 16 bytes and are not accumulated: bulk copies
   const int64_t *row_offsets;
   int experts;
   int64_t total_rows;        // grouped: rows of A
@@ -170,7 +173,7 @@ __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-enum Site { kSiteLoad = 0, kSiteMmaStage = 2, kSiteScaleSlot = 4, kSiteAcc = 6 };
+enum Site { kSiteLoad = 0, kSiteMmaStage = 2, kSiteScaleSlot = 4, kSiteScaleStage = 5, kSiteAcc = 6 };
 
 // Tables of the grouped forms in shared memory: row offsets; first tile of each expert or (wgrad) its first
 // block along K.
@@ -239,6 +242,71 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t) 
   r.p_end = a.p_rows;
   r.q_end = a.q_rows;
   return r;
+}
+
+// Bulk stores of this thread: their sources have been read; they are complete.
+__device__ __forceinline__ void bulk_store_read(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// A warp's 32 rows of W = 128 columns through `stage` (8 KB) as boxes of 32 rows x 128 bytes; a row's sixteen-byte
+// pieces are turned by its number modulo 8 (the copies' 128-byte swizzle), which spreads 8 rows over all banks.
+// Rows and columns past D's ends are left out by the copy.
+template <int W>
+__device__ __forceinline__ void store_bulk(const CUtensorMap &map, int f32, int col, int row, int expert, uint32_t stage, int lane,
+                                           const uint64_t (&acc)[W / 2]) {
+  static_assert(W == 128, "two boxes of bf16, four of fp32");
+  const uint32_t mine = stage + lane * 128, turn = (lane & 7) * 16;
+  bulk_store_read(lane);
+  if (!f32) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack2(acc[c * 4 + i], lo, hi);
+        w[i] = pack_bf16x2(lo, hi);
+      }
+      sts128(mine + (c / 8) * 4096 + (((c % 8) * 16) ^ turn), w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(&map, stage, col * 2, row, expert);
+      tma_store_3d(&map, stage + 4096, col * 2 + 128, row, expert);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h) bulk_store_read(lane);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const uint64_t v0 = acc[h * 32 + c * 2], v1 = acc[h * 32 + c * 2 + 1];
+      sts128(mine + (c / 8) * 4096 + (((c % 8) * 16) ^ turn), static_cast<uint32_t>(v0), static_cast<uint32_t>(v0 >> 32),
+             static_cast<uint32_t>(v1), static_cast<uint32_t>(v1 >> 32));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(&map, stage, (col + h * 64) * 4, row, expert);
+      tma_store_3d(&map, stage + 4096, (col + h * 64) * 4 + 128, row, expert);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  }
 }
 
 __device__ __forceinline__ void store_one(const Args &a, int64_t at, float v) {
@@ -344,11 +412,13 @@ __device__ __forceinline__ void store_rows(const Args &a, int64_t at, int n, boo
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const Args a) {
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                    const __grid_constant__ CUtensorMap map_d, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   // the ring begins on a 1024-byte boundary (the swizzle's period)
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  float *scales = reinterpret_cast<float *>(smem + C::STAGES * C::STAGE);
+  uint8_t *out = smem + C::STAGES * C::STAGE;  // 1024-byte aligned too
+  float *scales = reinterpret_cast<float *>(out + C::OUT);
   uint8_t *ctrl = reinterpret_cast<uint8_t *>(scales) + C::SLOTS * C::SC_BYTES;
   // A block's products wait for one barrier and announce one: `full` collects the operands, the scales and the
   // scaling warps that emptied the block's buffer (NACC blocks before); `done` tells the loader that the stage and
@@ -365,7 +435,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   Tables tb;
   tb.ro = reinterpret_cast<int *>(ctrl + C::CTRL);
   tb.tp = tb.kb = tb.ro + kMaxExperts + 4;
-  float *turn = reinterpret_cast<float *>(ctrl + C::CTRL + C::TABLE);
+  float *turn = reinterpret_cast<float *>(C::BULK ? out : ctrl + C::CTRL + C::TABLE);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   constexpr bool SPLIT = C::MODE == kDense && C::SWAP;
@@ -533,13 +603,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const bool is = i < C::SLOTS || mbar_wait(smem_u32(&sempty[i % C::SLOTS]), (i / C::SLOTS - 1) & 1, wc, kSiteScaleSlot);
         return __all_sync(0xFFFFFFFFu, is);
       };
-      // what was asked for block i - LEAD has landed: announce it
+      // what was asked for block n = i - LEAD has landed: announce it, once the block that had its stage before is done
       auto announce = [&]() {
         cp_async_commit();
-        if (i >= C::LEAD) {
+        const int n = i - C::LEAD;
+        if (n >= 0) {
           cp_async_wait_group<C::LEAD / 2>();
+          if (n >= C::STAGES) {
+            const bool is = mbar_wait(smem_u32(&done[n % C::STAGES]), (n / C::STAGES - 1) & 1, wc, kSiteScaleStage);
+            ok = __all_sync(0xFFFFFFFFu, is);
+          }
           __syncwarp();
-          arrive_lane0(smem_u32(&full[(i - C::LEAD) % C::STAGES]), lane);
+          if (ok) arrive_lane0(smem_u32(&full[n % C::STAGES]), lane);
         }
         i += 2;
       };
@@ -563,7 +638,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           qin[j] = r < t.q_end && (C::CV ? (C::NT >= 32 || lane < C::NT) : lane < (C::NT + 127) / 128);
           qp[j] = a.sq.p + t.expert * a.sq.es + (C::CV ? (qin[j] ? r : 0) : (qin[j] ? r / 128 : 0)) * a.sq.rs + t.kb0 * a.sq.ks;
         }
-        for (int kb = k0; kb < k1; ++kb, ++block) {
+        for (int kb = k0; kb < k1 && ok; ++kb, ++block) {
           if ((block & 1) != mine) continue;
           ok = slot_free();
           if (!ok) break;
@@ -672,7 +747,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int p = t.p0 + quad * 32 + lane, q = t.q0 + half * C::W;
       if constexpr (C::SWAP) {
         if (p < t.p_end) {
-          const int64_t at = static_cast<int64_t>(q) * a.ldd + p;
+          const int64_t at = t.expert * a.d_expert + static_cast<int64_t>(q) * a.ldd + p;
 #pragma unroll
           for (int i = 0; i < C::W; ++i) {
             float lo, hi;
@@ -681,10 +756,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       } else {
+        if constexpr (C::BULK) {
+          const int p32 = t.p0 + quad * 32;
+          // (rows past an expert's last belong to the next one: only a warp whose rows are all inside, or end with D)
+          if (a.bulk && (C::MODE != kGrouped || p32 + 32 <= t.p_end)) {
+            if (p32 < t.p_end) store_bulk<C::W>(map_d, a.out_f32, q, p32, C::MODE == kWgrad ? t.expert : 0, smem_u32(out) + (warp - 4) * 8192, lane, acc);
+            continue;
+          }
+          bulk_store_read(lane);  // what is still being copied out of the place that is turned around in
+        }
         store_rows<C::W>(a, t.expert * a.d_expert + static_cast<int64_t>(p) * a.ldd + q, t.q_end - q, p < t.p_end,
-                         turn + (warp - 4) * 32 * 9, lane, acc);
+                         turn + (warp - 4) * (C::BULK ? 2048 : 32 * 9), lane, acc);
       }
     }
+  }
+
+  if constexpr (C::BULK) {
+    if (warp >= 4 && lane == 0) bulk_store_done();
   }
 
   // -------------------------------------------------------------- end
@@ -784,12 +872,22 @@ inline void fill_args(Args &a, void *d, int d_type, int accumulate, int64_t ldd,
 // grid is the smaller of that and what the device holds at once).
 template <class C>
 nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, const uint8_t *q, int64_t q_rows,
-                           int64_t k, int64_t tiles, const Args &args, const DeviceInfo &dev, uint32_t flags,
+                           int64_t k, int64_t tiles, const Args &given, const DeviceInfo &dev, uint32_t flags,
                            nvfp4_stream_t stream) {
   CUtensorMap mp, mq;
   nvfp4_status_t st = encode_tmap_2d_u8(&mp, p, k, p_rows, k, 128, 128, true);
   if (st == NVFP4_OK) st = encode_tmap_2d_u8(&mq, q, k, q_rows, k, 128, C::NT, true);
   if (st != NVFP4_OK) return st;
+  // D [experts (1 but for the weight gradients), rows, ldd]
+  Args args = given;
+  CUtensorMap md = mp;
+  const int64_t es = args.out_f32 ? 4 : 2;
+  args.bulk = C::BULK && !args.accumulate && args.ldd * es % 16 == 0 && args.d_expert * es % 16 == 0;
+  if (args.bulk) {
+    const int64_t rows = C::MODE == kWgrad ? args.p_rows : p_rows, depth = C::MODE == kWgrad ? args.experts : 1;
+    st = encode_tmap_store_u8(&md, args.d, args.ldd * es, rows, depth, args.ldd * es, rows * args.ldd * es, 32);
+    if (st != NVFP4_OK) return st;
+  }
   auto kern = fp8_gemm_kernel<C>;
   st = allow_smem(reinterpret_cast<const void *>(kern), C::SMEM, dev.device);
   if (st != NVFP4_OK) return st;
@@ -799,7 +897,7 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
   const int64_t cap = dev.sm_count / cluster * cluster;
   if (args.splits == 1 && grid > cap) grid = cap;
   cudaError_t e = launch(kern, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), C::SMEM, (cudaStream_t)stream,
-                         (flags & NVFP4_FLAG_PDL) != 0, cluster, mp, mq, args);
+                         (flags & NVFP4_FLAG_PDL) != 0, cluster, mp, mq, md, args);
   return check_launch(e, name);
 }
 

@@ -49,6 +49,11 @@ nvfp4_status_t encode_tmap_2d_u8(CUtensorMap *map, const void *base, uint64_t in
 nvfp4_status_t encode_tmap_stages_u8(CUtensorMap *map, const void *base, uint64_t k_bytes, uint64_t rows,
                                      uint32_t box_rows, uint32_t box_stages);
 
+// 3-D view of [depth, rows, row_bytes] bytes for storing boxes of box_rows rows of 128 bytes, staged in shared memory
+// with the 128-byte swizzle.  Strides are multiples of 16.
+nvfp4_status_t encode_tmap_store_u8(CUtensorMap *map, void *base, uint64_t row_bytes, uint64_t rows, uint64_t depth,
+                                    uint64_t row_stride_bytes, uint64_t depth_stride_bytes, uint32_t box_rows);
+
 // Raises the dynamic shared-memory limit of `fn` on the current device (once per device).
 nvfp4_status_t allow_smem(const void *fn, int bytes, int device);
 
