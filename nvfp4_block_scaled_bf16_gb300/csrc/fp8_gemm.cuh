@@ -25,15 +25,18 @@ enum Mode { kDense = 0, kGrouped = 1, kWgrad = 2 };
 
 constexpr int kMaxExperts = 1024;
 
-template <int NT_, bool SWAP_, bool PV_, bool CV_, int MODE_>
+template <int NT_, bool SWAP_, bool PV_, bool CV_, int MODE_, int CG_ = 1>
 struct Cfg {
   static constexpr int NT = NT_;         // columns of a tile (rows of Q)
   static constexpr bool SWAP = SWAP_;    // P is B
   static constexpr bool PV = PV_;        // P has a scale per row (else per 128 rows)
   static constexpr bool CV = CV_;        // Q has a scale per row
   static constexpr int MODE = MODE_;
+  static constexpr int CG = CG_;         // 2: a CTA pair shares a 256-row tile, each CTA holds half of Q's rows
+  static constexpr bool PAIR = CG == 2;
   static constexpr int P_BYTES = 128 * 128;
-  static constexpr int Q_BYTES = NT * 128;
+  static constexpr int Q_ROWS = NT / CG;
+  static constexpr int Q_BYTES = Q_ROWS * 128;
   static constexpr int STAGE = P_BYTES + Q_BYTES;
   // Wide rows of D leave through shared memory as bulk copies, so that the scaling warps go on with the next tile: a
   // warp's 32 rows x 256 bytes.  (Stored directly, 32 rows at a time by 32 bytes each, a 128 x 256 tile took 3200
@@ -60,12 +63,12 @@ struct Cfg {
   static constexpr int SMEM = 1024 + STAGES * STAGE + OUT + SLOTS * SC_BYTES + TABLE + TURN + CTRL;
   // f8f6f4: fp32 sums (1 at bit 4), e4m3 operands (0 at bits 7 and 10), both K-major
   static constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
-                                    (static_cast<uint32_t>(128 >> 4) << 24);
+                                    (static_cast<uint32_t>(128 * CG >> 4) << 24);
   static_assert(SMEM <= 232448, "smem");
 };
 
 // Where an operand's scales lie: of row r (or of its block of 128) and block b along K at
-// p + expert * es + r * rs + b * ks.
+// p + expert * es + r * rs + b * ks (rs = 1 where each row has one).
 struct Scales {
   const float *p;
   int64_t es, rs, ks;
@@ -96,17 +99,41 @@ struct Tile {
   int expert;
 };
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t pdesc, uint64_t qdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
 }
 
 // Lane 0's arrival, without a branch.
 __device__ __forceinline__ void arrive_lane0(uint32_t bar, int lane) {
   asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(lane)
                : "memory");
+}
+
+// The same on a stage's barrier, which in a pair is the first CTA's.
+template <bool PAIR>
+__device__ __forceinline__ void arrive_stage(uint32_t bar, int lane) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b32 r;\n setp.eq.s32 p, %1, 0;\n mapa.shared::cluster.u32 r, %0, 0;\n"
+        " @p mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(bar),
+        "r"(lane)
+        : "memory");
+  else
+    arrive_lane0(bar, lane);
+}
+template <bool PAIR>
+__device__ __forceinline__ bool try_done(uint32_t bar, uint32_t parity) {
+  return PAIR ? mbar_try_wait_cl(bar, parity) : mbar_try_wait(bar, parity);
 }
 
 // True in one lane of the (converged) warp.
@@ -183,11 +210,11 @@ struct Tables {
 
 template <class C>
 __device__ __forceinline__ int token_tile() {
-  return C::SWAP ? C::NT : 128;
+  return C::SWAP ? C::NT : 128 * C::CG;
 }
 
 template <class C>
-__device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t) {
+__device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t, int prank) {
   Tile r;
   r.expert = 0;
   r.kb0 = 0;
@@ -216,7 +243,7 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t) 
     } else {
       qi = l / tt;
       pi = l % tt;
-      r.p0 = r.py = tb.ro[lo] + pi * 128;
+      r.p0 = r.py = tb.ro[lo] + (pi * C::CG + prank) * 128;
       r.p_end = tb.ro[lo + 1];
       r.q0 = qi * C::NT;
       r.q_end = a.q_rows;
@@ -237,7 +264,7 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t) 
   const int gs = min(G, a.p_tiles - g * G);
   pi = g * G + l % gs;
   qi = l / gs;
-  r.p0 = r.py = pi * 128;
+  r.p0 = r.py = (pi * C::CG + prank) * 128;
   r.q0 = r.qy = qi * C::NT;
   r.p_end = a.p_rows;
   r.q_end = a.q_rows;
@@ -441,11 +468,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   constexpr bool SPLIT = C::MODE == kDense && C::SWAP;
   const int splits = SPLIT ? a.splits : 1;
   const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int unit = blockIdx.x / splits, units = gridDim.x / splits;
+  const int prank = C::PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cluster = C::PAIR ? 2 : splits;
+  const int unit = blockIdx.x / cluster, units = gridDim.x / cluster;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 2 + C::SW);
+      mbar_init(smem_u32(&full[i]), 1 + C::CG * (1 + C::SW));  // (a pair's: the first CTA's)
       mbar_init(smem_u32(&done[i]), 1);
     }
     for (int i = 0; i < C::SLOTS; ++i) mbar_init(smem_u32(&sempty[i]), C::SW);
@@ -458,8 +487,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     prefetch_tmap(&map_q);
   }
   if (warp == 1) {
-    tmem_alloc<1>(smem_u32(tmem_holder), C::TMEM);
-    tmem_relinquish<1>();
+    tmem_alloc<C::CG>(smem_u32(tmem_holder), C::TMEM);
+    tmem_relinquish<C::CG>();
   }
   pdl_trigger();
   pdl_wait();
@@ -503,7 +532,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (C::PAIR) cluster_sync();  // the CTAs arrive on each other's barriers
+  else __syncthreads();
   tc_fence_after();
   if constexpr (C::MODE == kDense) total = a.p_tiles * a.q_tiles;
   else if constexpr (C::MODE == kGrouped) total = tb.tp[a.experts];
@@ -527,7 +557,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   uint64_t acc[C::W / 2];  // pairs of columns
   if (warp < 4) {
-    if constexpr (C::NT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if constexpr (C::NT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ------------------------------------------------------------ operands
       if (lane == 0) {
@@ -535,21 +565,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         uint32_t phase = 0;
         bool ok = true;
         for (int u = unit; u < total && ok; u += units) {
-          const Tile t = tile_at<C>(a, tb, u);
+          const Tile t = tile_at<C>(a, tb, u, prank);
           int k0, k1;
           k_range(t, k0, k1);
           for (int kb = k0; kb < k1; ++kb) {
-            if (issued >= C::STAGES && !mbar_wait(smem_u32(&done[stage]), phase ^ 1, wc, kSiteLoad)) {
+            if (issued >= C::STAGES && !mbar_wait<C::PAIR>(smem_u32(&done[stage]), phase ^ 1, wc, kSiteLoad)) {
               ok = false;
               break;
             }
             const uint32_t bar = smem_u32(&full[stage]);
             const uint32_t dst = smem_u32(smem + stage * C::STAGE);
             const int x = (t.kb0 + kb) * 128;
-            mbar_arrive_expect_tx(bar, C::STAGE);
+            if (prank == 0) mbar_arrive_expect_tx(bar, C::CG * C::STAGE);
             if (!(a.skip_first_load && issued == 0)) {
-              tma_load_2d(dst, &map_p, bar, x, t.py);
-              tma_load_2d(dst + C::P_BYTES, &map_q, bar, x, t.qy);
+              if constexpr (C::PAIR) {
+                const uint32_t bar0 = map_to_rank(bar, 0);
+                tma_load_2d_pair(dst, &map_p, bar0, x, t.py);
+                tma_load_2d_pair(dst + C::P_BYTES, &map_q, bar0, x, t.qy + prank * C::Q_ROWS);
+              } else {
+                tma_load_2d(dst, &map_p, bar, x, t.py);
+                tma_load_2d(dst + C::P_BYTES, &map_q, bar, x, t.qy);
+              }
             }
             ++issued;
             if (++stage == C::STAGES) {
@@ -567,12 +603,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
-      for (int u = unit; u < total && ok; u += units) {
-        const Tile t = tile_at<C>(a, tb, u);
+      for (int u = unit; u < total && ok && prank == 0; u += units) {
+        const Tile t = tile_at<C>(a, tb, u, prank);
         int k0, k1;
         k_range(t, k0, k1);
         for (int kb = k0; kb < k1; ++kb) {
-          ok = mbar_wait(smem_u32(&full[stage]), phase, wc, kSiteMmaStage);
+          ok = mbar_wait<C::PAIR>(smem_u32(&full[stage]), phase, wc, kSiteMmaStage);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -581,8 +617,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint32_t d = tmem + ab * C::NT;
           if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_f8(d, pd + 2 * i, qd + 2 * i, C::IDESC, i > 0 ? 1u : 0u);
-            tc_commit(smem_u32(&done[stage]));
+            for (int i = 0; i < 4; ++i) mma_f8<C::PAIR>(d, pd + 2 * i, qd + 2 * i, C::IDESC, i > 0 ? 1u : 0u);
+            if constexpr (C::PAIR) tc_commit_pair_mc(smem_u32(&done[stage]), static_cast<uint16_t>(0x3));
+            else tc_commit(smem_u32(&done[stage]));
           }
           __syncwarp();
           if (++stage == C::STAGES) {
@@ -610,47 +647,43 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (n >= 0) {
           cp_async_wait_group<C::LEAD / 2>();
           if (n >= C::STAGES) {
-            const bool is = mbar_wait(smem_u32(&done[n % C::STAGES]), (n / C::STAGES - 1) & 1, wc, kSiteScaleStage);
+            const bool is = mbar_wait<C::PAIR>(smem_u32(&done[n % C::STAGES]), (n / C::STAGES - 1) & 1, wc, kSiteScaleStage);
             ok = __all_sync(0xFFFFFFFFu, is);
           }
           __syncwarp();
-          if (ok) arrive_lane0(smem_u32(&full[n % C::STAGES]), lane);
+          if (ok) arrive_stage<C::PAIR>(smem_u32(&full[n % C::STAGES]), lane);
         }
         i += 2;
       };
-      constexpr int NP = C::PV ? 4 : 1, NQ = C::CV ? (C::NT + 31) / 32 : 1;
       for (int u = unit; u < total && ok; u += units) {
-        const Tile t = tile_at<C>(a, tb, u);
+        const Tile t = tile_at<C>(a, tb, u, prank);
         int k0, k1;
         k_range(t, k0, k1);
-        // where this lane's scales of the tile's rows lie
-        const float *pp[NP], *qp[NQ];
-        bool pin[NP], qin[NQ];
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const int r = t.p0 + j * 32 + lane;
-          pin[j] = C::PV ? r < t.p_end : lane == 0;
-          pp[j] = a.sp.p + t.expert * a.sp.es + (C::PV ? (pin[j] ? r : 0) : t.p0 / 128) * a.sp.rs + t.kb0 * a.sp.ks;
-        }
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-          const int r = t.q0 + (C::CV ? j * 32 + lane : lane * 128);
-          qin[j] = r < t.q_end && (C::CV ? (C::NT >= 32 || lane < C::NT) : lane < (C::NT + 127) / 128);
-          qp[j] = a.sq.p + t.expert * a.sq.es + (C::CV ? (qin[j] ? r : 0) : (qin[j] ? r / 128 : 0)) * a.sq.rs + t.kb0 * a.sq.ks;
-        }
+        // where this lane's scales of the tile's rows lie (a scale per row: the rows' lie side by side)
+        const int pr = C::PV ? t.p0 + lane : 0, qr = t.q0 + (C::CV ? lane : lane * 128);
+        const float *pp = a.sp.p + t.expert * a.sp.es + (C::PV ? pr : t.p0 / 128 * a.sp.rs) + t.kb0 * a.sp.ks;
+        const float *qp = a.sq.p + t.expert * a.sq.es + (C::CV ? qr : qr / 128 * a.sq.rs) + t.kb0 * a.sq.ks;
         for (int kb = k0; kb < k1 && ok; ++kb, ++block) {
           if ((block & 1) != mine) continue;
           ok = slot_free();
           if (!ok) break;
           const uint32_t dst = smem_u32(scales) + (i % C::SLOTS) * C::SC_BYTES + lane * 4;
-          // (rows past the end get zeros, lanes without a row nothing)
+          const float *pb = pp + kb * a.sp.ks, *qb = qp + kb * a.sq.ks;
+          // (rows past the end get zeros, and nothing is read for them)
+          if constexpr (C::PV) {
 #pragma unroll
-          for (int j = 0; j < NP; ++j)
-            if (C::PV || lane == 0) cp_async_4(dst + j * 128, pp[j] + kb * a.sp.ks, pin[j]);
+            for (int j = 0; j < 4; ++j) cp_async_4(dst + j * 128, pr + j * 32 < t.p_end ? pb + j * 32 : a.sp.p, pr + j * 32 < t.p_end);
+          } else if (lane == 0) {
+            cp_async_4(dst, pb, true);
+          }
+          if constexpr (C::CV) {
 #pragma unroll
-          for (int j = 0; j < NQ; ++j)
-            if (C::CV ? (C::NT >= 32 || lane < C::NT) : lane < (C::NT + 127) / 128)
-              cp_async_4(dst + C::SC_P * 4 + j * 128, qp[j] + kb * a.sq.ks, qin[j]);
+            for (int j = 0; j < (C::NT + 31) / 32; ++j)
+              if (C::NT >= 32 || lane < C::NT)
+                cp_async_4(dst + C::SC_P * 4 + j * 128, qr + j * 32 < t.q_end ? qb + j * 32 : a.sq.p, qr + j * 32 < t.q_end);
+          } else if (lane < (C::NT + 127) / 128) {
+            cp_async_4(dst + C::SC_P * 4, qr < t.q_end ? qb : a.sq.p, qr < t.q_end);
+          }
           announce();
         }
       }
@@ -663,16 +696,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   } else {
     // -------------------------------------------------------------- scaling and sums
-    if constexpr (C::NT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (C::NT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * C::W;
     int slot = 0, ab = 0, stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    if (lane == 0)  // the buffers of the first blocks are empty
-      for (int i = 0; i < C::NACC; ++i) mbar_arrive(smem_u32(&full[i]));
+    for (int i = 0; i < C::NACC; ++i) arrive_stage<C::PAIR>(smem_u32(&full[i]), lane);  // the first blocks' buffers are empty
     for (int u = unit; u < total && ok; u += units) {
-      const Tile t = tile_at<C>(a, tb, u);
+      const Tile t = tile_at<C>(a, tb, u, prank);
       int k0, k1;
       k_range(t, k0, k1);
 #pragma unroll
@@ -694,7 +726,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       };
       // the whole warp goes on or gives up
       auto wait_done = [&](bool ready) {
-        if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc));
+        if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait<C::PAIR>(smem_u32(&done[stage]), phase, wc, kSiteAcc));
       };
       if (k0 < k1) {
         wait_done(false);
@@ -719,10 +751,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tmem_ld_wait();
           if (i + 1 < CHUNKS) {
             tmem_ld<C::CH>(t_lane + ab_b * C::NT + (i + 1) * C::CH, r[(i + 1) & 1]);
-            if (i + 2 == CHUNKS && more) ready = mbar_try_wait(smem_u32(&done[stage]), phase);
+            if (i + 2 == CHUNKS && more) ready = try_done<C::PAIR>(smem_u32(&done[stage]), phase);
           } else {  // the last columns are in registers: the buffer may be overwritten
             tc_fence_before();
-            arrive_lane0(smem_u32(&full[next]), lane);
+            arrive_stage<C::PAIR>(smem_u32(&full[next]), lane);
             if (more && ok) begin();
           }
           uint32_t (&v)[C::CH] = r[i & 1];
@@ -791,8 +823,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     }
-    if (threadIdx.x == 32) {
-      tc_commit(smem_u32(drain));
+    if (threadIdx.x == 32 && prank == 0) {
+      tc_commit<C::CG>(smem_u32(drain));
       const long long t0 = clock64();
       while (!mbar_try_wait(smem_u32(drain), 0) && clock64() - t0 < a.wait_limit) {
       }
@@ -814,7 +846,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
       cluster_sync();
-      const Tile t = tile_at<C>(a, tb, unit);
+      const Tile t = tile_at<C>(a, tb, unit, 0);
       const int cols = min(C::NT, t.q_end - t.q0);
       // 32 float4 a column
       for (int i = threadIdx.x + rank * C::THREADS; i < cols * 32; i += C::THREADS * splits) {
@@ -835,9 +867,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<1>(tmem, C::TMEM);
+    tmem_dealloc<C::CG>(tmem, C::TMEM);
   }
-  if (splits > 1) cluster_sync();  // no CTA leaves while another reads its memory
+  if (cluster > 1) cluster_sync();  // no CTA leaves while another reads its memory or arrives on its barriers
 }
 
 // What the products' entry points check and fill alike.  rows, cols: of the result; k: what is summed over.
@@ -876,7 +908,7 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
                            nvfp4_stream_t stream) {
   CUtensorMap mp, mq;
   nvfp4_status_t st = encode_tmap_2d_u8(&mp, p, k, p_rows, k, 128, 128, true);
-  if (st == NVFP4_OK) st = encode_tmap_2d_u8(&mq, q, k, q_rows, k, 128, C::NT, true);
+  if (st == NVFP4_OK) st = encode_tmap_2d_u8(&mq, q, k, q_rows, k, 128, C::Q_ROWS, true);
   if (st != NVFP4_OK) return st;
   // D [experts (1 but for the weight gradients), rows, ldd]
   Args args = given;
@@ -891,7 +923,7 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
   auto kern = fp8_gemm_kernel<C>;
   st = allow_smem(reinterpret_cast<const void *>(kern), C::SMEM, dev.device);
   if (st != NVFP4_OK) return st;
-  const int cluster = args.splits;
+  const int cluster = C::PAIR ? 2 : args.splits;
   int64_t grid = tiles * cluster;
   // split tiles: one per cluster (their partials are joined once); else persistent
   const int64_t cap = dev.sm_count / cluster * cluster;
