@@ -39,7 +39,7 @@ nvfp4_status_t run(const Call &c) {
   args.sq = C::SWAP ? sa : sb;
   args.p_rows = static_cast<int>(p);
   args.q_rows = static_cast<int>(q);
-  args.p_tiles = static_cast<int>(ceil_div(p, 128 * C::CG));
+  args.p_tiles = static_cast<int>(ceil_div(p, 128));
   args.q_tiles = static_cast<int>(ceil_div(q, C::NT));
   const int64_t tiles = static_cast<int64_t>(args.p_tiles) * args.q_tiles;
   if (tiles >= (1LL << 31)) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", c.name);
@@ -53,10 +53,10 @@ nvfp4_status_t run_swap(const Call &c) {
   return c.block_b == 128 ? run<fp8::Cfg<NT, true, false, true, fp8::kDense>>(c)
                           : run<fp8::Cfg<NT, true, true, true, fp8::kDense>>(c);
 }
-template <int NT, int CG = 1>
+template <int NT>
 nvfp4_status_t run_rows(const Call &c) {
-  return c.block_b == 128 ? run<fp8::Cfg<NT, false, true, false, fp8::kDense, CG>>(c)
-                          : run<fp8::Cfg<NT, false, true, true, fp8::kDense, CG>>(c);
+  return c.block_b == 128 ? run<fp8::Cfg<NT, false, true, false, fp8::kDense>>(c)
+                          : run<fp8::Cfg<NT, false, true, true, fp8::kDense>>(c);
 }
 
 // Tiles of more than 128 tokens, by what they cost: rounds of tiles over the SMs times the time of a tile's blocks.

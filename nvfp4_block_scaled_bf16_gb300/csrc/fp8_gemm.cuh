@@ -25,18 +25,15 @@ enum Mode { kDense = 0, kGrouped = 1, kWgrad = 2 };
 
 constexpr int kMaxExperts = 1024;
 
-template <int NT_, bool SWAP_, bool PV_, bool CV_, int MODE_, int CG_ = 1>
+template <int NT_, bool SWAP_, bool PV_, bool CV_, int MODE_>
 struct Cfg {
   static constexpr int NT = NT_;         // columns of a tile (rows of Q)
   static constexpr bool SWAP = SWAP_;    // P is B
   static constexpr bool PV = PV_;        // P has a scale per row (else per 128 rows)
   static constexpr bool CV = CV_;        // Q has a scale per row
   static constexpr int MODE = MODE_;
-  static constexpr int CG = CG_;         // 2: a CTA pair shares a 256-row tile, each CTA holds half of Q's rows
-  static constexpr bool PAIR = CG == 2;
   static constexpr int P_BYTES = 128 * 128;
-  static constexpr int Q_ROWS = NT / CG;
-  static constexpr int Q_BYTES = Q_ROWS * 128;
+  static constexpr int Q_BYTES = NT * 128;
   static constexpr int STAGE = P_BYTES + Q_BYTES;
   // Wide rows of D leave through shared memory as bulk copies, so that the scaling warps go on with the next tile: a
   // warp's 32 rows x 256 bytes.  (Stored directly, 32 rows at a time by 32 bytes each, a 128 x 256 tile took 3200
@@ -48,10 +45,10 @@ struct Cfg {
   static constexpr int SLOTS = BULK ? 6 : 8, LEAD = BULK ? 2 : 4;
   static constexpr int NACC = NT >= 256 ? 2 : 4;
   static constexpr int TMEM = NACC * NT < 32 ? 32 : NACC * NT;
-  static constexpr int SW = 8;     // scaling warps (behind 4 that feed)
+  static constexpr int SW = NT >= 256 ? 16 : 8;     // scaling warps (behind 4 that feed)
   static constexpr int THREADS = 128 + 32 * SW;
   static constexpr int W = NT * 4 / SW;  // columns of one scaling warp
-  static constexpr int CH = W <= 32 ? W / 2 : CV && W > 64 ? 16 : 32;  // columns loaded at a time
+  static constexpr int CH = W <= 32 ? W / 2 : NT >= 256 ? 16 : 32;  // columns loaded at a time
   static constexpr int SC_P = PV ? 128 : 4;
   static constexpr int SC_Q = CV ? NT : 4;
   static constexpr int SC_BYTES = (SC_P + SC_Q) * 4;
@@ -63,7 +60,7 @@ struct Cfg {
   static constexpr int SMEM = 1024 + STAGES * STAGE + OUT + SLOTS * SC_BYTES + TABLE + TURN + CTRL;
   // f8f6f4: fp32 sums (1 at bit 4), e4m3 operands (0 at bits 7 and 10), both K-major
   static constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
-                                    (static_cast<uint32_t>(128 * CG >> 4) << 24);
+                                    (static_cast<uint32_t>(128 >> 4) << 24);
   static_assert(SMEM <= 232448, "smem");
 };
 
@@ -99,41 +96,17 @@ struct Tile {
   int expert;
 };
 
-template <bool PAIR>
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t pdesc, uint64_t qdesc, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(accumulate));
 }
 
 // Lane 0's arrival, without a branch.
 __device__ __forceinline__ void arrive_lane0(uint32_t bar, int lane) {
   asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(lane)
                : "memory");
-}
-
-// The same on a stage's barrier, which in a pair is the first CTA's.
-template <bool PAIR>
-__device__ __forceinline__ void arrive_stage(uint32_t bar, int lane) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b32 r;\n setp.eq.s32 p, %1, 0;\n mapa.shared::cluster.u32 r, %0, 0;\n"
-        " @p mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(bar),
-        "r"(lane)
-        : "memory");
-  else
-    arrive_lane0(bar, lane);
-}
-template <bool PAIR>
-__device__ __forceinline__ bool try_done(uint32_t bar, uint32_t parity) {
-  return PAIR ? mbar_try_wait_cl(bar, parity) : mbar_try_wait(bar, parity);
 }
 
 // True in one lane of the (converged) warp.
@@ -210,11 +183,11 @@ struct Tables {
 
 template <class C>
 __device__ __forceinline__ int token_tile() {
-  return C::SWAP ? C::NT : 128 * C::CG;
+  return C::SWAP ? C::NT : 128;
 }
 
 template <class C>
-__device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t, int prank) {
+__device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t) {
   Tile r;
   r.expert = 0;
   r.kb0 = 0;
@@ -243,7 +216,7 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t, 
     } else {
       qi = l / tt;
       pi = l % tt;
-      r.p0 = r.py = tb.ro[lo] + (pi * C::CG + prank) * 128;
+      r.p0 = r.py = tb.ro[lo] + pi * 128;
       r.p_end = tb.ro[lo + 1];
       r.q0 = qi * C::NT;
       r.q_end = a.q_rows;
@@ -264,7 +237,7 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t, 
   const int gs = min(G, a.p_tiles - g * G);
   pi = g * G + l % gs;
   qi = l / gs;
-  r.p0 = r.py = (pi * C::CG + prank) * 128;
+  r.p0 = r.py = pi * 128;
   r.q0 = r.qy = qi * C::NT;
   r.p_end = a.p_rows;
   r.q_end = a.q_rows;
@@ -293,12 +266,12 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 template <int W>
 __device__ __forceinline__ void store_bulk(const CUtensorMap &map, int f32, int col, int row, int expert, uint32_t stage, int lane,
                                            const uint64_t (&acc)[W / 2]) {
-  static_assert(W == 128, "two boxes of bf16, four of fp32");
+  constexpr int BOXES = W / 64;  // of bf16; fp32 takes two rounds
   const uint32_t mine = stage + lane * 128, turn = (lane & 7) * 16;
   bulk_store_read(lane);
   if (!f32) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
+    for (int c = 0; c < 8 * BOXES; ++c) {
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -311,8 +284,8 @@ __device__ __forceinline__ void store_bulk(const CUtensorMap &map, int f32, int 
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_3d(&map, stage, col * 2, row, expert);
-      tma_store_3d(&map, stage + 4096, col * 2 + 128, row, expert);
+#pragma unroll
+      for (int i = 0; i < BOXES; ++i) tma_store_3d(&map, stage + i * 4096, col * 2 + i * 128, row, expert);
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
     return;
@@ -321,16 +294,16 @@ __device__ __forceinline__ void store_bulk(const CUtensorMap &map, int f32, int 
   for (int h = 0; h < 2; ++h) {
     if (h) bulk_store_read(lane);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const uint64_t v0 = acc[h * 32 + c * 2], v1 = acc[h * 32 + c * 2 + 1];
+    for (int c = 0; c < 8 * BOXES; ++c) {
+      const uint64_t v0 = acc[h * W / 4 + c * 2], v1 = acc[h * W / 4 + c * 2 + 1];
       sts128(mine + (c / 8) * 4096 + (((c % 8) * 16) ^ turn), static_cast<uint32_t>(v0), static_cast<uint32_t>(v0 >> 32),
              static_cast<uint32_t>(v1), static_cast<uint32_t>(v1 >> 32));
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_3d(&map, stage, (col + h * 64) * 4, row, expert);
-      tma_store_3d(&map, stage + 4096, (col + h * 64) * 4 + 128, row, expert);
+#pragma unroll
+      for (int i = 0; i < BOXES; ++i) tma_store_3d(&map, stage + i * 4096, (col + h * W / 2) * 4 + i * 128, row, expert);
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   }
@@ -468,13 +441,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   constexpr bool SPLIT = C::MODE == kDense && C::SWAP;
   const int splits = SPLIT ? a.splits : 1;
   const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int prank = C::PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-  const int cluster = C::PAIR ? 2 : splits;
-  const int unit = blockIdx.x / cluster, units = gridDim.x / cluster;
+  const int unit = blockIdx.x / splits, units = gridDim.x / splits;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 1 + C::CG * (1 + C::SW));  // (a pair's: the first CTA's)
+      mbar_init(smem_u32(&full[i]), 2 + C::SW);
       mbar_init(smem_u32(&done[i]), 1);
     }
     for (int i = 0; i < C::SLOTS; ++i) mbar_init(smem_u32(&sempty[i]), C::SW);
@@ -487,8 +458,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     prefetch_tmap(&map_q);
   }
   if (warp == 1) {
-    tmem_alloc<C::CG>(smem_u32(tmem_holder), C::TMEM);
-    tmem_relinquish<C::CG>();
+    tmem_alloc<1>(smem_u32(tmem_holder), C::TMEM);
+    tmem_relinquish<1>();
   }
   pdl_trigger();
   pdl_wait();
@@ -532,8 +503,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   }
   tc_fence_before();
-  if constexpr (C::PAIR) cluster_sync();  // the CTAs arrive on each other's barriers
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   if constexpr (C::MODE == kDense) total = a.p_tiles * a.q_tiles;
   else if constexpr (C::MODE == kGrouped) total = tb.tp[a.experts];
@@ -557,7 +527,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   uint64_t acc[C::W / 2];  // pairs of columns
   if (warp < 4) {
-    if constexpr (C::NT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (C::SW == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ------------------------------------------------------------ operands
       if (lane == 0) {
@@ -565,27 +535,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         uint32_t phase = 0;
         bool ok = true;
         for (int u = unit; u < total && ok; u += units) {
-          const Tile t = tile_at<C>(a, tb, u, prank);
+          const Tile t = tile_at<C>(a, tb, u);
           int k0, k1;
           k_range(t, k0, k1);
           for (int kb = k0; kb < k1; ++kb) {
-            if (issued >= C::STAGES && !mbar_wait<C::PAIR>(smem_u32(&done[stage]), phase ^ 1, wc, kSiteLoad)) {
+            if (issued >= C::STAGES && !mbar_wait(smem_u32(&done[stage]), phase ^ 1, wc, kSiteLoad)) {
               ok = false;
               break;
             }
             const uint32_t bar = smem_u32(&full[stage]);
             const uint32_t dst = smem_u32(smem + stage * C::STAGE);
             const int x = (t.kb0 + kb) * 128;
-            if (prank == 0) mbar_arrive_expect_tx(bar, C::CG * C::STAGE);
+            mbar_arrive_expect_tx(bar, C::STAGE);
             if (!(a.skip_first_load && issued == 0)) {
-              if constexpr (C::PAIR) {
-                const uint32_t bar0 = map_to_rank(bar, 0);
-                tma_load_2d_pair(dst, &map_p, bar0, x, t.py);
-                tma_load_2d_pair(dst + C::P_BYTES, &map_q, bar0, x, t.qy + prank * C::Q_ROWS);
-              } else {
-                tma_load_2d(dst, &map_p, bar, x, t.py);
-                tma_load_2d(dst + C::P_BYTES, &map_q, bar, x, t.qy);
-              }
+              tma_load_2d(dst, &map_p, bar, x, t.py);
+              tma_load_2d(dst + C::P_BYTES, &map_q, bar, x, t.qy);
             }
             ++issued;
             if (++stage == C::STAGES) {
@@ -603,12 +567,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
-      for (int u = unit; u < total && ok && prank == 0; u += units) {
-        const Tile t = tile_at<C>(a, tb, u, prank);
+      for (int u = unit; u < total && ok; u += units) {
+        const Tile t = tile_at<C>(a, tb, u);
         int k0, k1;
         k_range(t, k0, k1);
         for (int kb = k0; kb < k1; ++kb) {
-          ok = mbar_wait<C::PAIR>(smem_u32(&full[stage]), phase, wc, kSiteMmaStage);
+          ok = mbar_wait(smem_u32(&full[stage]), phase, wc, kSiteMmaStage);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -617,9 +581,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint32_t d = tmem + ab * C::NT;
           if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_f8<C::PAIR>(d, pd + 2 * i, qd + 2 * i, C::IDESC, i > 0 ? 1u : 0u);
-            if constexpr (C::PAIR) tc_commit_pair_mc(smem_u32(&done[stage]), static_cast<uint16_t>(0x3));
-            else tc_commit(smem_u32(&done[stage]));
+            for (int i = 0; i < 4; ++i) mma_f8(d, pd + 2 * i, qd + 2 * i, C::IDESC, i > 0 ? 1u : 0u);
+            tc_commit(smem_u32(&done[stage]));
           }
           __syncwarp();
           if (++stage == C::STAGES) {
@@ -647,16 +610,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (n >= 0) {
           cp_async_wait_group<C::LEAD / 2>();
           if (n >= C::STAGES) {
-            const bool is = mbar_wait<C::PAIR>(smem_u32(&done[n % C::STAGES]), (n / C::STAGES - 1) & 1, wc, kSiteScaleStage);
+            const bool is = mbar_wait(smem_u32(&done[n % C::STAGES]), (n / C::STAGES - 1) & 1, wc, kSiteScaleStage);
             ok = __all_sync(0xFFFFFFFFu, is);
           }
           __syncwarp();
-          if (ok) arrive_stage<C::PAIR>(smem_u32(&full[n % C::STAGES]), lane);
+          if (ok) arrive_lane0(smem_u32(&full[n % C::STAGES]), lane);
         }
         i += 2;
       };
       for (int u = unit; u < total && ok; u += units) {
-        const Tile t = tile_at<C>(a, tb, u, prank);
+        const Tile t = tile_at<C>(a, tb, u);
         int k0, k1;
         k_range(t, k0, k1);
         // where this lane's scales of the tile's rows lie (a scale per row: the rows' lie side by side)
@@ -696,19 +659,63 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   } else {
     // -------------------------------------------------------------- scaling and sums
-    if constexpr (C::NT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (C::SW == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * C::W;
     int slot = 0, ab = 0, stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int i = 0; i < C::NACC; ++i) arrive_stage<C::PAIR>(smem_u32(&full[i]), lane);  // the first blocks' buffers are empty
+    for (int i = 0; i < C::NACC; ++i) arrive_lane0(smem_u32(&full[i]), lane);  // the first blocks' buffers are empty
     for (int u = unit; u < total && ok; u += units) {
-      const Tile t = tile_at<C>(a, tb, u, prank);
+      const Tile t = tile_at<C>(a, tb, u);
       int k0, k1;
       k_range(t, k0, k1);
 #pragma unroll
       for (int i = 0; i < C::W / 2; ++i) acc[i] = 0;
+      if constexpr (C::SW == 16) {
+        for (int kb = k0; kb < k1; ++kb) {
+          const bool ready = mbar_try_wait(smem_u32(&done[stage]), phase);
+          if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc));
+          if (!ok) break;
+          tc_fence_after();
+          const float *sc = scales + slot * (C::SC_BYTES / 4);
+          float f = C::PV ? sc[quad * 32 + lane] : sc[0];
+          if constexpr (!C::CV) f *= sc[C::SC_P + half * C::W / 128];
+          const uint64_t f2 = pack2(f, f);
+#pragma unroll
+          for (int c = 0; c < C::W; c += C::CH) {
+            uint32_t v[C::CH];
+            tmem_ld<C::CH>(t_lane + ab * C::NT + c, v);
+            tmem_ld_wait();
+            if (c + C::CH == C::W) {
+              tc_fence_before();
+              const int next = stage + C::NACC >= C::STAGES ? stage + C::NACC - C::STAGES : stage + C::NACC;
+              arrive_lane0(smem_u32(&full[next]), lane);
+            }
+            uint64_t *sum = acc + c / 2;
+            if constexpr (C::CV) {
+              const ulonglong2 *cs = reinterpret_cast<const ulonglong2 *>(sc + C::SC_P + half * C::W + c);
+#pragma unroll
+              for (int j = 0; j < C::CH; j += 4) {
+                const ulonglong2 s = cs[j / 4];
+                sum[j / 2] = fma2(mul2f(pack2u(v[j], v[j + 1]), s.x), f2, sum[j / 2]);
+                sum[j / 2 + 1] = fma2(mul2f(pack2u(v[j + 2], v[j + 3]), s.y), f2, sum[j / 2 + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < C::CH; j += 2) sum[j / 2] = fma2(pack2u(v[j], v[j + 1]), f2, sum[j / 2]);
+            }
+          }
+          __syncwarp();
+          arrive_lane0(smem_u32(&sempty[slot]), lane);
+          if (++slot == C::SLOTS) slot = 0;
+          if (++ab == C::NACC) ab = 0;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      } else {
       // The barrier of the next block is tested while the last columns but one are added, and its first columns are
       // loaded before the last are: what the test, the loads and the scale take passes while there is work.
       constexpr int CHUNKS = C::W / C::CH;
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       };
       // the whole warp goes on or gives up
       auto wait_done = [&](bool ready) {
-        if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait<C::PAIR>(smem_u32(&done[stage]), phase, wc, kSiteAcc));
+        if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc));
       };
       if (k0 < k1) {
         wait_done(false);
@@ -751,10 +758,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tmem_ld_wait();
           if (i + 1 < CHUNKS) {
             tmem_ld<C::CH>(t_lane + ab_b * C::NT + (i + 1) * C::CH, r[(i + 1) & 1]);
-            if (i + 2 == CHUNKS && more) ready = try_done<C::PAIR>(smem_u32(&done[stage]), phase);
+            if (i + 2 == CHUNKS && more) ready = mbar_try_wait(smem_u32(&done[stage]), phase);
           } else {  // the last columns are in registers: the buffer may be overwritten
             tc_fence_before();
-            arrive_stage<C::PAIR>(smem_u32(&full[next]), lane);
+            arrive_lane0(smem_u32(&full[next]), lane);
             if (more && ok) begin();
           }
           uint32_t (&v)[C::CH] = r[i & 1];
@@ -775,6 +782,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         arrive_lane0(smem_u32(&sempty[slot_b]), lane);
       }
+      }
       if (!ok || splits > 1) continue;
       const int p = t.p0 + quad * 32 + lane, q = t.q0 + half * C::W;
       if constexpr (C::SWAP) {
@@ -792,13 +800,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const int p32 = t.p0 + quad * 32;
           // (rows past an expert's last belong to the next one: only a warp whose rows are all inside, or end with D)
           if (a.bulk && (C::MODE != kGrouped || p32 + 32 <= t.p_end)) {
-            if (p32 < t.p_end) store_bulk<C::W>(map_d, a.out_f32, q, p32, C::MODE == kWgrad ? t.expert : 0, smem_u32(out) + (warp - 4) * 8192, lane, acc);
+            if (p32 < t.p_end) store_bulk<C::W>(map_d, a.out_f32, q, p32, C::MODE == kWgrad ? t.expert : 0, smem_u32(out) + (warp - 4) * (65536 / C::SW), lane, acc);
             continue;
           }
           bulk_store_read(lane);  // what is still being copied out of the place that is turned around in
         }
         store_rows<C::W>(a, t.expert * a.d_expert + static_cast<int64_t>(p) * a.ldd + q, t.q_end - q, p < t.p_end,
-                         turn + (warp - 4) * (C::BULK ? 2048 : 32 * 9), lane, acc);
+                         turn + (warp - 4) * (C::BULK ? 16384 / C::SW : 32 * 9), lane, acc);
       }
     }
   }
@@ -823,8 +831,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     }
-    if (threadIdx.x == 32 && prank == 0) {
-      tc_commit<C::CG>(smem_u32(drain));
+    if (threadIdx.x == 32) {
+      tc_commit(smem_u32(drain));
       const long long t0 = clock64();
       while (!mbar_try_wait(smem_u32(drain), 0) && clock64() - t0 < a.wait_limit) {
       }
@@ -846,7 +854,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
       cluster_sync();
-      const Tile t = tile_at<C>(a, tb, unit, 0);
+      const Tile t = tile_at<C>(a, tb, unit);
       const int cols = min(C::NT, t.q_end - t.q0);
       // 32 float4 a column
       for (int i = threadIdx.x + rank * C::THREADS; i < cols * 32; i += C::THREADS * splits) {
@@ -867,9 +875,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<C::CG>(tmem, C::TMEM);
+    tmem_dealloc<1>(tmem, C::TMEM);
   }
-  if (cluster > 1) cluster_sync();  // no CTA leaves while another reads its memory or arrives on its barriers
+  if (splits > 1) cluster_sync();  // no CTA leaves while another reads its memory
 }
 
 // What the products' entry points check and fill alike.  rows, cols: of the result; k: what is summed over.
@@ -908,7 +916,7 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
                            nvfp4_stream_t stream) {
   CUtensorMap mp, mq;
   nvfp4_status_t st = encode_tmap_2d_u8(&mp, p, k, p_rows, k, 128, 128, true);
-  if (st == NVFP4_OK) st = encode_tmap_2d_u8(&mq, q, k, q_rows, k, 128, C::Q_ROWS, true);
+  if (st == NVFP4_OK) st = encode_tmap_2d_u8(&mq, q, k, q_rows, k, 128, C::NT, true);
   if (st != NVFP4_OK) return st;
   // D [experts (1 but for the weight gradients), rows, ldd]
   Args args = given;
@@ -923,7 +931,7 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
   auto kern = fp8_gemm_kernel<C>;
   st = allow_smem(reinterpret_cast<const void *>(kern), C::SMEM, dev.device);
   if (st != NVFP4_OK) return st;
-  const int cluster = C::PAIR ? 2 : args.splits;
+  const int cluster = args.splits;
   int64_t grid = tiles * cluster;
   // split tiles: one per cluster (their partials are joined once); else persistent
   const int64_t cap = dev.sm_count / cluster * cluster;

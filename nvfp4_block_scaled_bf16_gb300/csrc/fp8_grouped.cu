@@ -19,7 +19,7 @@ nvfp4_status_t grouped(const char *name, const uint8_t *a, const float *sfa, con
   args.q_tiles = static_cast<int>(ceil_div(n, C::NT));
   args.splits = 1;
   // sum over experts of ceil(rows / tile) <= min(rows, ceil(t / tile) + experts)
-  const int64_t tt = C::SWAP ? C::NT : 128 * C::CG;
+  const int64_t tt = C::SWAP ? C::NT : 128;
   int64_t bound = ceil_div(t, tt) + experts;
   if (bound > t) bound = t;
   bound *= C::SWAP ? args.p_tiles : args.q_tiles;
@@ -101,7 +101,7 @@ extern "C" nvfp4_status_t fp8_grouped_weight_grad(const uint8_t *a, const float 
   args.sq = fp8::Scales{sfb, 0, 1, k};
   args.p_rows = static_cast<int>(n);
   args.q_rows = static_cast<int>(k);
-  args.p_tiles = static_cast<int>(ceil_div(n, 128 * Grad::CG));
+  args.p_tiles = static_cast<int>(ceil_div(n, 128));
   args.q_tiles = static_cast<int>(ceil_div(k, Grad::NT));
   args.d_expert = n * k;
   args.row_offsets = row_offsets;
