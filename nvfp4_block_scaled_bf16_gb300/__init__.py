@@ -857,6 +857,12 @@ def _dense(t, dtype, name, shape, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _is(t, dtype, dim, dev):
+    """Whether `t` is a contiguous tensor of this type on device `dev` (one test for a small call; where it fails,
+    _need and the others say why)."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == dim and t.is_contiguous()
+
+
 def _made(t, dtype, name, shape, dev, stream):
     """The output tensor `t`, or a new one (made for the launch stream, so that its memory belongs to it: see _contig)."""
     if t is not None:
@@ -881,13 +887,17 @@ def fp8_quantize(x, src_rows=None, row_offsets=None, rows: bool = True, transpos
     (transpose=True): qt [k, P], sft [P/128, k] with P = fp8_padded_rows(m, experts); with row_offsets (int64
     [E+1]) each expert's rows begin at a multiple of 128 there.  src_rows (int32 [m]): row r of the result is
     x[src_rows[r]] (without it m = n).  Returns (q, sf), (qt, sft) or (q, sf, qt, sft); x is read once."""
-    _check_device(x, "x")
-    xt = _type_of(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must have 2 dimensions")
-    n, k = x.shape
+    if _is(x, torch.bfloat16, 2, _current_device()):
+        xt, (n, k) = 0, x.shape
+        ldx = k
+    else:
+        _check_device(x, "x")
+        xt = _type_of(x, "x")
+        if x.dim() != 2:
+            raise ValueError("x must have 2 dimensions")
+        n, k = x.shape
+        ldx = _rows(x, x.dtype, "x", n, k, x.get_device())
     dev = x.device
-    ldx = _rows(x, x.dtype, "x", n, k, x.get_device())
     m, experts = n, 0
     src_p = ro_p = q_p = sf_p = qt_p = sft_p = None
     if src_rows is not None:
@@ -953,6 +963,16 @@ def fp8_quantize_weight(w, transpose: bool = False, q=None, sf=None, qt=None, sf
     return (q, sf, qt, sft) if transpose else (q, sf)
 
 
+def _codes(a, da, b, db):
+    """Checks a product's codes; returns their device."""
+    dev = _current_device()
+    if not (_is(a, E4M3, da, dev) and _is(b, E4M3, db, dev)):
+        _need(a, E4M3, "a", da)
+        _need(b, E4M3, "b", db)
+        raise ValueError("a and b must be contiguous")
+    return dev
+
+
 def _product_out(d, out_dtype, accumulate, shape, dev, stream):
     """(d, its NVFP4_DTYPE_*)."""
     if d is not None:
@@ -970,17 +990,14 @@ def fp8_gemm(a, sfa, b, sfb, block_b: int = 128, out_dtype=torch.bfloat16, d=Non
     """D[m, n] = deq(a) @ deq(b)^T; a [m, k] and b [n, k] e4m3, sfa fp32 [ceil(k/128), m] (fp8_quantize), sfb
     fp32 [ceil(n/128), ceil(k/128)] (block_b=128, fp8_quantize_weight) or [ceil(k/128), n] (block_b=1,
     fp8_quantize).  D is bf16 or fp32; accumulate adds to an fp32 d."""
-    _need(a, E4M3, "a", 2)
-    _need(b, E4M3, "b", 2)
+    dev = _codes(a, 2, b, 2)
     m, k = a.shape
     n, kb = b.shape
     if kb != k:
         raise ValueError("a and b disagree on K")
     if block_b not in (1, 128):
         raise ValueError(f"block_b must be 1 or 128, got {block_b}")
-    if not a.is_contiguous() or not b.is_contiguous():
-        raise ValueError("a and b must be contiguous")
-    kb, dev = -(-k // 128), a.get_device()
+    kb = -(-k // 128)
     _dense(sfa, torch.float32, "sfa", (kb, m), dev)
     _dense(sfb, torch.float32, "sfb", (-(-n // 128), kb) if block_b == 128 else (kb, n), dev)
     d, dt = _product_out(d, out_dtype, accumulate, (m, n), a.device, stream)
@@ -993,15 +1010,12 @@ def fp8_grouped_gemm(a, sfa, row_offsets, b, sfb, out_dtype=torch.bfloat16, d=No
     """Per expert e: D[rows of e] = deq(A_e) @ deq(B_e)^T; a e4m3 [t, k] with its rows sorted by expert (sfa
     [ceil(k/128), t]), b e4m3 [E, n, k] (sfb [E, ceil(n/128), ceil(k/128)]), D bf16 or fp32.  Rows past the last
     expert's stay as they were."""
-    _need(a, E4M3, "a", 2)
-    _need(b, E4M3, "b", 3)
+    dev = _codes(a, 2, b, 3)
     t, k = a.shape
     experts, n, kb = b.shape
     if kb != k:
         raise ValueError("a and b disagree on K")
-    if not a.is_contiguous() or not b.is_contiguous():
-        raise ValueError("a and b must be contiguous")
-    kb, dev = -(-k // 128), a.get_device()
+    kb = -(-k // 128)
     _dense(row_offsets, torch.int64, "row_offsets", (experts + 1,), dev)
     _dense(sfa, torch.float32, "sfa", (kb, t), dev)
     _dense(sfb, torch.float32, "sfb", (experts, -(-n // 128), kb), dev)
@@ -1017,16 +1031,15 @@ def fp8_grouped_weight_grad(a, sfa, b, sfb, row_offsets, out_dtype=torch.bfloat1
     (of the output's gradient) and b e4m3 [k, P] (of the input) with sfa [P/128, n], sfb [P/128, k], as
     fp8_quantize(transpose=True) gives them under the same row_offsets.  D [E, n, k] bf16 or fp32; accumulate adds
     to an fp32 d."""
-    _need(a, E4M3, "a", 2)
-    _need(b, E4M3, "b", 2)
-    _need(row_offsets, torch.int64, "row_offsets", 1)
+    dev = _codes(a, 2, b, 2)
+    if not _is(row_offsets, torch.int64, 1, dev):
+        _need(row_offsets, torch.int64, "row_offsets", 1)
+        raise ValueError("row_offsets must be contiguous")
     n, p = a.shape
     k, pb = b.shape
     if pb != p:
         raise ValueError("a and b disagree on the rows")
-    if not a.is_contiguous() or not b.is_contiguous() or not row_offsets.is_contiguous():
-        raise ValueError("a, b and row_offsets must be contiguous")
-    experts, dev = row_offsets.numel() - 1, a.get_device()
+    experts = row_offsets.numel() - 1
     _dense(sfa, torch.float32, "sfa", (p // 128, n), dev)
     _dense(sfb, torch.float32, "sfb", (p // 128, k), dev)
     d, dt = _product_out(d, out_dtype, accumulate, (experts, n, k), a.device, stream)
@@ -1040,18 +1053,20 @@ def moe_combine_backward(dout, y, pos, weights, dy=None, dweights=None, flags: i
     """Gradients of moe_combine: (dy bf16 [rows, h], dweights fp32 [T, topk]) with dy[pos[t, j]] = weights[t, j] *
     dout[t] and dweights[t, j] = dout[t] . y[pos[t, j]].  Rows of dy that no slot names stay as they were; no row
     may be named twice (moe_sort_by_expert's pos names none twice)."""
-    _need(y, torch.bfloat16, "y", 2)
-    _need(pos, torch.int32, "pos", 2)
-    _need(weights, torch.float32, "weights", 2)
-    if not y.is_contiguous():
-        raise ValueError("y must be contiguous")
+    cur = _current_device()
+    if not (_is(y, torch.bfloat16, 2, cur) and _is(pos, torch.int32, 2, cur) and _is(weights, torch.float32, 2, cur)):
+        _need(y, torch.bfloat16, "y", 2)
+        _need(pos, torch.int32, "pos", 2)
+        _need(weights, torch.float32, "weights", 2)
+        if not y.is_contiguous():
+            raise ValueError("y must be contiguous")
+        pos, weights = _contig(pos, stream), _contig(weights, stream)
     rows, h = y.shape
     T, topk = pos.shape
     dev = y.device
-    ldo = _rows(dout, torch.bfloat16, "dout", T, h, y.get_device())
+    ldo = _rows(dout, torch.bfloat16, "dout", T, h, cur)
     if weights.shape != (T, topk):
         raise ValueError(f"weights must have shape {(T, topk)}, got {tuple(weights.shape)}")
-    pos, weights = _contig(pos, stream), _contig(weights, stream)
     dy = _made(dy, torch.bfloat16, "dy", (rows, h), dev, stream)
     dweights = _made(dweights, torch.float32, "dweights", (T, topk), dev, stream)
     _check(_lib.moe_combine_backward(dout.data_ptr(), ldo, y.data_ptr(), rows, pos.data_ptr(), weights.data_ptr(), T, topk, h,
@@ -1062,13 +1077,15 @@ def moe_combine_backward(dout, y, pos, weights, dy=None, dweights=None, flags: i
 def moe_gather_backward(dxs, pos, dx=None, flags: int = 0, stream=None):
     """Gradient of moe_gather_rows under moe_sort_by_expert's src_rows: dx[t] = bf16(sum_j dxs[pos[t, j]]) (fp32, slot
     order)."""
-    _need(dxs, torch.bfloat16, "dxs", 2)
-    _need(pos, torch.int32, "pos", 2)
-    if not dxs.is_contiguous():
-        raise ValueError("dxs must be contiguous")
+    cur = _current_device()
+    if not (_is(dxs, torch.bfloat16, 2, cur) and _is(pos, torch.int32, 2, cur)):
+        _need(dxs, torch.bfloat16, "dxs", 2)
+        _need(pos, torch.int32, "pos", 2)
+        if not dxs.is_contiguous():
+            raise ValueError("dxs must be contiguous")
+        pos = _contig(pos, stream)
     rows, h = dxs.shape
     T, topk = pos.shape
-    pos = _contig(pos, stream)
     dx = _made(dx, torch.bfloat16, "dx", (T, h), dxs.device, stream)
     _check(_lib.moe_gather_backward(dxs.data_ptr(), rows, pos.data_ptr(), T, topk, h, dx.data_ptr(), flags, _stream(stream)))
     return dx
