@@ -24,6 +24,7 @@ namespace fp8 {
 enum Mode { kDense = 0, kGrouped = 1, kWgrad = 2 };
 
 constexpr int kMaxExperts = 1024;
+constexpr int kGroup = 8;          // tiles along P that are taken in turn
 
 template <int NT_, bool SWAP_, bool PV_, bool CV_, int MODE_>
 struct Cfg {
@@ -71,6 +72,21 @@ struct Scales {
   int64_t es, rs, ks;
 };
 
+// Division by a number that the host knows, for dividends below 2^31: the multiplication by a rounded-up reciprocal
+// of Granlund and Montgomery (a tile's place takes two divisions, and every warp asks for it).
+struct Divisor {
+  uint32_t d, mul, shift;
+  __host__ static Divisor of(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return Divisor{d, static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+  }
+  __device__ __forceinline__ int quotient(int n) const {
+    const uint32_t u = static_cast<uint32_t>(n);
+    return static_cast<int>((__umulhi(mul, u) + u) >> shift);
+  }
+};
+
 struct Args {
   Scales sp, sq;
   void *d;
@@ -78,6 +94,7 @@ struct Args {
   int p_rows, q_rows;        // dense and wgrad: rows of P and Q; grouped: rows of the weight in both
   int nk;                    // blocks along K (dense and grouped)
   int p_tiles, q_tiles;      // tiles along the static operands
+  Divisor per_expert, group; // p_tiles * q_tiles; kGroup * q_tiles
   int splits;                // dense with SWAP: CTAs of a cluster that share a tile's K
   int out_f32, accumulate;
   int bulk;                  // rows of D start on 16 bytes and are not accumulated: bulk copies
@@ -225,18 +242,16 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t) 
     return r;
   }
   if constexpr (C::MODE == kWgrad) {
-    const int per = a.p_tiles * a.q_tiles;
-    r.expert = t / per;
-    t -= r.expert * per;
+    r.expert = a.per_expert.quotient(t);
+    t -= r.expert * static_cast<int>(a.per_expert.d);
     r.kb0 = tb.kb[r.expert];
     r.nk = tb.kb[r.expert + 1] - r.kb0;
   }
-  // groups of 8 tiles along P: what runs at the same time shares both operands through L2
-  constexpr int G = 8;
-  const int g = t / (G * a.q_tiles), l = t - g * G * a.q_tiles;
-  const int gs = min(G, a.p_tiles - g * G);
-  pi = g * G + l % gs;
-  qi = l / gs;
+  // groups of tiles along P: what runs at the same time shares both operands through L2
+  const int g = a.group.quotient(t), l = t - g * static_cast<int>(a.group.d);
+  const int gs = min(kGroup, a.p_tiles - g * kGroup);
+  qi = gs == kGroup ? l / kGroup : l / gs;
+  pi = g * kGroup + l - qi * gs;
   r.p0 = r.py = pi * 128;
   r.q0 = r.qy = qi * C::NT;
   r.p_end = a.p_rows;
@@ -920,6 +935,10 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
   if (st != NVFP4_OK) return st;
   // D [experts (1 but for the weight gradients), rows, ldd]
   Args args = given;
+  if (C::MODE != kGrouped) {
+    args.per_expert = Divisor::of(static_cast<uint32_t>(args.p_tiles) * args.q_tiles);  // (the tiles are fewer than 2^31)
+    args.group = Divisor::of(static_cast<uint32_t>(kGroup) * args.q_tiles);
+  }
   CUtensorMap md = mp;
   const int64_t es = args.out_f32 ? 4 : 2;
   args.bulk = C::BULK && !args.accumulate && args.ldd * es % 16 == 0 && args.d_expert * es % 16 == 0;

@@ -31,7 +31,8 @@ nvfp4_status_t grouped(const char *name, const uint8_t *a, const float *sfa, con
 
 template <int NT>
 using Swapped = fp8::Cfg<NT, true, false, true, fp8::kGrouped>;
-using Rows = fp8::Cfg<256, false, true, false, fp8::kGrouped>;
+template <int NT>
+using Rows = fp8::Cfg<NT, false, true, false, fp8::kGrouped>;
 using Grad = fp8::Cfg<256, false, true, true, fp8::kWgrad>;
 
 nvfp4_status_t check_experts(const char *name, int experts, int64_t n) {
@@ -64,14 +65,18 @@ extern "C" nvfp4_status_t fp8_grouped_gemm(const uint8_t *a, const float *sfa, c
   args.row_offsets = row_offsets;
   args.experts = num_experts;
   args.total_rows = t;
+  // Few rows to an expert: the weight in the lanes and a narrow tile of tokens, for the weight is read from memory
+  // once whatever the tile (128 experts of 1536 x 2048, us: 2 rows to an expert 55, 8 rows 68, 16 rows 71; at 48 rows
+  // 64 columns of tokens took 87, the rows in the lanes 76).  Else the rows in the lanes, 256 columns of the weight to
+  // a tile, or 128 where so few tiles would leave SMs idle.
   const int64_t mean = ceil_div(t, num_experts);
   if (mean <= 8)
     return grouped<Swapped<16>>(name, a, sfa, b, sfb, args, t, n, k, num_experts, dev, flags, stream);
   if (mean <= 16)
     return grouped<Swapped<32>>(name, a, sfa, b, sfb, args, t, n, k, num_experts, dev, flags, stream);
-  if (mean <= 48)
-    return grouped<Swapped<64>>(name, a, sfa, b, sfb, args, t, n, k, num_experts, dev, flags, stream);
-  return grouped<Rows>(name, a, sfa, b, sfb, args, t, n, k, num_experts, dev, flags, stream);
+  if ((ceil_div(t, 128) + num_experts / 2) * ceil_div(n, 256) < dev.sm_count)
+    return grouped<Rows<128>>(name, a, sfa, b, sfb, args, t, n, k, num_experts, dev, flags, stream);
+  return grouped<Rows<256>>(name, a, sfa, b, sfb, args, t, n, k, num_experts, dev, flags, stream);
 }
 
 extern "C" nvfp4_status_t fp8_grouped_weight_grad(const uint8_t *a, const float *sfa, const uint8_t *b, const float *sfb,
