@@ -296,6 +296,14 @@ __global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_tile_kernel(co
     xp[i] = xr < 0 ? nullptr : static_cast<const uint8_t *>(a.x) + (xr * a.ldx + cg * 16) * (F32 ? 4 : 2);
   }
   const int b0 = blockIdx.y * a.chain, b1 = min(a.kb, b0 + a.chain);
+  // where this thread's codes go in the first tile: its rows', and its piece of the columns' (a column in 32)
+  uint8_t *qp = ALONG == kColumns ? nullptr : a.q + (row0 + r0) * a.k + b0 * 128 + cg * 16;
+  const int64_t ldt = ALONG == kBlock ? a.m : a.row_blocks * 128;
+  const int ch = tid % 8;  // 16-byte piece of a column's 128 rows
+  uint8_t *tp = nullptr;
+  if (ALONG != kBlock) tp = a.qt + (static_cast<int64_t>(b0) * 128 + tid / 8) * ldt + blk * 128 + ch * 16;
+  else if (a.qt) tp = a.qt + (mat * a.k + static_cast<int64_t>(b0) * 128 + tid / 8) * ldt + mblk * 128 + ch * 16;
+  const bool piece_in = ALONG != kBlock || mblk * 128 + ch * 16 < a.m;
   for (int b = b0; b < b1; ++b) {
     const int c0 = b * 128;
     const bool in_k = c0 + cg * 16 < a.k;
@@ -403,23 +411,18 @@ __global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_tile_kernel(co
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (r0 + i < rows && in_k)
-          *reinterpret_cast<uint4 *>(a.q + (row0 + r0 + i) * a.k + c0 + cg * 16) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+          *reinterpret_cast<uint4 *>(qp + static_cast<int64_t>(i) * a.k) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+      qp += 128;
     }
     if (!turned) continue;
     __syncthreads();  // (the other of the two is written next, and this one again two tiles on, behind its barriers)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int c = i * 32 + tid / 8, ch = tid % 8;  // column, 16-byte piece of its 128 rows
-      const uint4 w = *reinterpret_cast<const uint4 *>(&turn[c * 32 + ((ch * 4) ^ ((c / 16) * 4))]);
-      if (c0 + c < a.k) {
-        if constexpr (ALONG == kBlock) {
-          if (mblk * 128 + ch * 16 < a.m)
-            *reinterpret_cast<uint4 *>(a.qt + (mat * a.k + c0 + c) * a.m + mblk * 128 + ch * 16) = w;
-        } else {
-          *reinterpret_cast<uint4 *>(a.qt + static_cast<int64_t>(c0 + c) * a.row_blocks * 128 + blk * 128 + ch * 16) = w;
-        }
-      }
+      const int c = i * 32 + tid / 8;
+      if (c0 + c < a.k && piece_in)
+        *reinterpret_cast<uint4 *>(tp + i * 32 * ldt) = *reinterpret_cast<const uint4 *>(&turn[c * 32 + ((ch * 4) ^ ((c / 16) * 4))]);
     }
+    tp += 128 * ldt;
   }
 }
 
