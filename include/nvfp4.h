@@ -517,7 +517,7 @@ nvfp4_status_t sample_tokens(const void *logits, int logits_type, int64_t ld, co
  *               expert's are not quantised (q and sf stay as they were there).  Needs qt.  Malformed
  *               offsets: the columns of qt are zeros and nvfp4_check_status reports
  *               NVFP4_ERR_INVALID_ARG.
- *   q and qt 16-B aligned; 1 <= num_experts <= 1024; rows, k <= 2^31 - 512, k <= 2^23.
+ *   q and qt 16-B aligned; 1 <= num_experts <= 1024; rows <= 2^31 - 512, k <= 65535 * 128.
  * x is read once for both. */
 int64_t fp8_padded_rows(int64_t rows, int num_experts); /* round_up(rows, 128) + 128 * num_experts */
 nvfp4_status_t fp8_quantize(const void *x, int x_type, int64_t x_rows, int64_t k, int64_t ldx, const int32_t *src_rows,

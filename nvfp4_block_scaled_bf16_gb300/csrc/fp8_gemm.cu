@@ -42,7 +42,7 @@ nvfp4_status_t run(const Call &c) {
   args.p_tiles = static_cast<int>(ceil_div(p, 128));
   args.q_tiles = static_cast<int>(ceil_div(q, C::NT));
   const int64_t tiles = static_cast<int64_t>(args.p_tiles) * args.q_tiles;
-  if (tiles >= (1LL << 31)) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", c.name);
+  if (tiles >= (1LL << 31) - 1024) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", c.name);
   args.splits = C::SWAP ? swap_splits(tiles, args.nk, c.dev->sm_count) : 1;
   return fp8::launch_gemm<C>(c.name, C::SWAP ? c.b : c.a, p, C::SWAP ? c.a : c.b, q, c.k, tiles, args, *c.dev, c.flags,
                              c.stream);
@@ -60,12 +60,12 @@ nvfp4_status_t run_rows(const Call &c) {
 }
 
 // Tiles of more than 128 tokens, by what they cost: rounds of tiles over the SMs times the time of a tile's blocks.
-// Measured (ns a block): tokens in the lanes 280, 310 and 500 at 64, 128 and 256 columns with a scale per block of
-// B, 310, 440 and 750 with one per row; the weight in the lanes (whose K a cluster can share) 310 and 440 at 64
+// Measured (ns a block): tokens in the lanes 270, 310 and 460 at 64, 128 and 256 columns with a scale per block of
+// B, 310, 440 and 630 with one per row; the weight in the lanes (whose K a cluster can share) 310 and 440 at 64
 // and 128 columns, and 2500 ns to join a cluster's parts.
 enum Choice { kRows64, kRows128, kRows256, kSwap64, kSwap128 };
 Choice choose(int64_t m, int64_t n, int nk, bool per_row, int sms) {
-  const int64_t rows_ns[3] = {per_row ? 310 : 280, per_row ? 440 : 310, per_row ? 750 : 500}, swap_ns[2] = {310, 440};
+  const int64_t rows_ns[3] = {per_row ? 310 : 270, per_row ? 440 : 310, per_row ? 630 : 460}, swap_ns[2] = {310, 440};
   Choice best = kRows256;
   double least = 1e300;
   for (int i = 0; i < 5; ++i) {

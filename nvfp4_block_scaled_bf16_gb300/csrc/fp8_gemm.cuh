@@ -1,13 +1,18 @@
 // e4m3 products with one fp32 scale per block of 128 along K: D = sum over blocks b of
 // (sP[row, b] sQ[col, b]) * sum over the block's 128 elements of P[row, k] Q[col, k].
 //
-// The tensor core sums one 128-wide block at a time into a tensor-memory buffer of its own
-// (tcgen05.mma kind::f8f6f4, four instructions of K = 32), and eight warps scale that block's sums
-// in fp32 and add them to accumulators that stay in registers over the whole K: the factor of a
-// block is an fp32 number, which no scale format of the tensor core holds.  A 128 x 256 tile takes
-// the tensor core 512 cycles a block (8192 multiply-adds a cycle); its sums take 256 cycles to read
-// from tensor memory (128 lanes of 4 bytes a cycle) and 256 to scale and add (128 lanes), and with a
-// factor per column 256 more, so that the scaling of one block hides behind the products of the next.
+// The tensor core sums one 128-wide block at a time into a tensor-memory buffer of its own (tcgen05.mma kind::f8f6f4,
+// four instructions of K = 32), and scaling warps multiply that block's sums by its factor in fp32 and add them to
+// accumulators that stay in registers over the whole K: the factor is an fp32 number, which no scale format of the
+// tensor core holds.
+//
+// What bounds it, measured on 128 x 256 tiles (cycles a block).  The products alone take 512 (8192 multiply-adds a
+// cycle), reading the sums 136 (0.53 a column and quarter of the SM).  Scaling with scalar multiply-adds slows the
+// products to 930; with pairs (fma.rn.f32x2) they take 566 beside it, and the scaling 475, twice that with a factor per
+// column too.  What is left of the 900 that a block takes (4096 x 4864 x 7168 in 109 us, 2.6 PFLOP/s; 1270 with a
+// factor per column, 146 us) is the chain from a block's products through the scaling warps back to the buffer:
+// four warps to a scheduler hide more of it than two with more columns each (123 us) or than CTA pairs, which halve
+// the operands' traffic but lengthen the chain (111 us).
 //
 // The operand whose rows lie in the 128 tensor-memory lanes is P, the other (the columns) is Q.
 // Usually P is A (the tokens); with SWAP it is B (a weight), so that few tokens fill a narrow tile.
@@ -36,8 +41,7 @@ struct Cfg {
   static constexpr int P_BYTES = 128 * 128;
   static constexpr int Q_BYTES = NT * 128;
   static constexpr int STAGE = P_BYTES + Q_BYTES;
-  // Wide rows of D leave through shared memory as bulk copies, so that the scaling warps go on with the next tile: a
-  // warp's 32 rows x 256 bytes.  (Stored directly, 32 rows at a time by 32 bytes each, a 128 x 256 tile took 3200
+  // Wide rows of D leave through shared memory as bulk copies, so that the scaling warps go on with the next tile.  (Stored directly, 32 rows at a time by 32 bytes each, a 128 x 256 tile took 3200
   // cycles.)
   static constexpr bool BULK = !SWAP && NT == 256;
   static constexpr int STAGES_FIT = (BULK ? 147456 : 200 * 1024) / STAGE;
@@ -54,7 +58,7 @@ struct Cfg {
   static constexpr int SC_Q = CV ? NT : 4;
   static constexpr int SC_BYTES = (SC_P + SC_Q) * 4;
   static constexpr int TABLE = MODE == kDense ? 0 : 2 * (kMaxExperts + 4) * 4;
-  static constexpr int OUT = BULK ? 8 * 8192 : 0;
+  static constexpr int OUT = BULK ? 65536 : 0;  // 128 rows x 512 bytes
   static constexpr int TURN = SWAP || BULK ? 0 : SW * 32 * 9 * 4;  // where rows of D that are not aligned are turned around (BULK: in OUT)
   static constexpr int CTRL = 512;
   static_assert(NACC <= STAGES, "a buffer's next block must have a stage of its own");
@@ -275,11 +279,12 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// A warp's 32 rows of W = 128 columns through `stage` (8 KB) as boxes of 32 rows x 128 bytes; a row's sixteen-byte
-// pieces are turned by its number modulo 8 (the copies' 128-byte swizzle), which spreads 8 rows over all banks.
-// Rows and columns past D's ends are left out by the copy.
+// A warp's 32 rows of W columns through `stage` (64 columns of bf16 or 32 of fp32 to 4 KB) as boxes of 32 rows x 128
+// bytes; a row's sixteen-byte pieces are turned by its number modulo 8 (the copies' 128-byte swizzle), which spreads
+// 8 rows over all banks.  Rows and columns past D's ends (`end` columns) are left out by the copies, boxes that begin
+// past them are not sent.
 template <int W>
-__device__ __forceinline__ void store_bulk(const CUtensorMap &map, int f32, int col, int row, int expert, uint32_t stage, int lane,
+__device__ __forceinline__ void store_bulk(const CUtensorMap &map, int f32, int col, int end, int row, int expert, uint32_t stage, int lane,
                                            const uint64_t (&acc)[W / 2]) {
   constexpr int BOXES = W / 64;  // of bf16; fp32 takes two rounds
   const uint32_t mine = stage + lane * 128, turn = (lane & 7) * 16;
@@ -300,7 +305,8 @@ __device__ __forceinline__ void store_bulk(const CUtensorMap &map, int f32, int 
     __syncwarp();
     if (lane == 0) {
 #pragma unroll
-      for (int i = 0; i < BOXES; ++i) tma_store_3d(&map, stage + i * 4096, col * 2 + i * 128, row, expert);
+      for (int i = 0; i < BOXES; ++i)
+        if (col + i * 64 < end) tma_store_3d(&map, stage + i * 4096, (col + i * 64) * 2, row, expert);
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
     return;
@@ -318,7 +324,8 @@ __device__ __forceinline__ void store_bulk(const CUtensorMap &map, int f32, int 
     __syncwarp();
     if (lane == 0) {
 #pragma unroll
-      for (int i = 0; i < BOXES; ++i) tma_store_3d(&map, stage + i * 4096, (col + h * W / 2) * 4 + i * 128, row, expert);
+      for (int i = 0; i < BOXES; ++i)
+        if (col + h * W / 2 + i * 32 < end) tma_store_3d(&map, stage + i * 4096, (col + h * W / 2 + i * 32) * 4, row, expert);
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   }
@@ -688,6 +695,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < C::W / 2; ++i) acc[i] = 0;
       if constexpr (C::SW == 16) {
+        // four warps to a scheduler: one's waits pass while the others have work
         for (int kb = k0; kb < k1; ++kb) {
           const bool ready = mbar_try_wait(smem_u32(&done[stage]), phase);
           if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc));
@@ -731,74 +739,74 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       } else {
-      // The barrier of the next block is tested while the last columns but one are added, and its first columns are
-      // loaded before the last are: what the test, the loads and the scale take passes while there is work.
-      constexpr int CHUNKS = C::W / C::CH;
-      static_assert(CHUNKS >= 2 && CHUNKS % 2 == 0, "chunks");
-      uint32_t r[2][C::CH];
-      float f = 0.0f;
-      const float *sc = scales;
-      // starts on a block whose sums (and so its scales) are there
-      auto begin = [&]() {
-        tc_fence_after();
-        tmem_ld<C::CH>(t_lane + ab * C::NT, r[0]);
-        sc = scales + slot * (C::SC_BYTES / 4);
-        f = C::PV ? sc[quad * 32 + lane] : sc[0];
-        if constexpr (!C::CV) f *= sc[C::SC_P + half * C::W / 128];
-      };
-      // the whole warp goes on or gives up
-      auto wait_done = [&](bool ready) {
-        if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc));
-      };
-      if (k0 < k1) {
-        wait_done(false);
-        if (ok) begin();
-      }
-      for (int kb = k0; kb < k1 && ok; ++kb) {
-        const uint64_t f2 = pack2(f, f);
-        const float *scb = sc;
-        const int slot_b = slot, ab_b = ab;
-        const int next = stage + C::NACC >= C::STAGES ? stage + C::NACC - C::STAGES : stage + C::NACC;  // the buffer's next block's stage
-        const bool more = kb + 1 < k1;
-        bool ready = false;
-        if (++slot == C::SLOTS) slot = 0;
-        if (++ab == C::NACC) ab = 0;
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1;
+        // The barrier of the next block is tested while the last columns but one are added, and its first columns are
+        // loaded before the last are: what the test, the loads and the scale take passes while there is work.
+        constexpr int CHUNKS = C::W / C::CH;
+        static_assert(CHUNKS >= 2 && CHUNKS % 2 == 0, "chunks");
+        uint32_t r[2][C::CH];
+        float f = 0.0f;
+        const float *sc = scales;
+        // starts on a block whose sums (and so its scales) are there
+        auto begin = [&]() {
+          tc_fence_after();
+          tmem_ld<C::CH>(t_lane + ab * C::NT, r[0]);
+          sc = scales + slot * (C::SC_BYTES / 4);
+          f = C::PV ? sc[quad * 32 + lane] : sc[0];
+          if constexpr (!C::CV) f *= sc[C::SC_P + half * C::W / 128];
+        };
+        // the whole warp goes on or gives up
+        auto wait_done = [&](bool ready) {
+          if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc));
+        };
+        if (k0 < k1) {
+          wait_done(false);
+          if (ok) begin();
         }
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
-          if (i + 1 == CHUNKS && more) wait_done(ready);
-          tmem_ld_wait();
-          if (i + 1 < CHUNKS) {
-            tmem_ld<C::CH>(t_lane + ab_b * C::NT + (i + 1) * C::CH, r[(i + 1) & 1]);
-            if (i + 2 == CHUNKS && more) ready = mbar_try_wait(smem_u32(&done[stage]), phase);
-          } else {  // the last columns are in registers: the buffer may be overwritten
-            tc_fence_before();
-            arrive_lane0(smem_u32(&full[next]), lane);
-            if (more && ok) begin();
+        for (int kb = k0; kb < k1 && ok; ++kb) {
+          const uint64_t f2 = pack2(f, f);
+          const float *scb = sc;
+          const int slot_b = slot, ab_b = ab;
+          const int next = stage + C::NACC >= C::STAGES ? stage + C::NACC - C::STAGES : stage + C::NACC;  // the buffer's next block's stage
+          const bool more = kb + 1 < k1;
+          bool ready = false;
+          if (++slot == C::SLOTS) slot = 0;
+          if (++ab == C::NACC) ab = 0;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
           }
-          uint32_t (&v)[C::CH] = r[i & 1];
-          uint64_t *sum = acc + i * C::CH / 2;
-          if constexpr (C::CV) {
-            const ulonglong2 *cs = reinterpret_cast<const ulonglong2 *>(scb + C::SC_P + half * C::W + i * C::CH);
 #pragma unroll
-            for (int j = 0; j < C::CH; j += 4) {
-              const ulonglong2 s = cs[j / 4];
-              sum[j / 2] = fma2(mul2f(pack2u(v[j], v[j + 1]), s.x), f2, sum[j / 2]);
-              sum[j / 2 + 1] = fma2(mul2f(pack2u(v[j + 2], v[j + 3]), s.y), f2, sum[j / 2 + 1]);
+          for (int i = 0; i < CHUNKS; ++i) {
+            if (i + 1 == CHUNKS && more) wait_done(ready);
+            tmem_ld_wait();
+            if (i + 1 < CHUNKS) {
+              tmem_ld<C::CH>(t_lane + ab_b * C::NT + (i + 1) * C::CH, r[(i + 1) & 1]);
+              if (i + 2 == CHUNKS && more) ready = mbar_try_wait(smem_u32(&done[stage]), phase);
+            } else {  // the last columns are in registers: the buffer may be overwritten
+              tc_fence_before();
+              arrive_lane0(smem_u32(&full[next]), lane);
+              if (more && ok) begin();
             }
-          } else {
+            uint32_t (&v)[C::CH] = r[i & 1];
+            uint64_t *sum = acc + i * C::CH / 2;
+            if constexpr (C::CV) {
+              const ulonglong2 *cs = reinterpret_cast<const ulonglong2 *>(scb + C::SC_P + half * C::W + i * C::CH);
 #pragma unroll
-            for (int j = 0; j < C::CH; j += 2) sum[j / 2] = fma2(pack2u(v[j], v[j + 1]), f2, sum[j / 2]);
+              for (int j = 0; j < C::CH; j += 4) {
+                const ulonglong2 s = cs[j / 4];
+                sum[j / 2] = fma2(mul2f(pack2u(v[j], v[j + 1]), s.x), f2, sum[j / 2]);
+                sum[j / 2 + 1] = fma2(mul2f(pack2u(v[j + 2], v[j + 3]), s.y), f2, sum[j / 2 + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < C::CH; j += 2) sum[j / 2] = fma2(pack2u(v[j], v[j + 1]), f2, sum[j / 2]);
+            }
           }
+          __syncwarp();
+          arrive_lane0(smem_u32(&sempty[slot_b]), lane);
         }
-        __syncwarp();
-        arrive_lane0(smem_u32(&sempty[slot_b]), lane);
       }
-      }
-      if (!ok || splits > 1) continue;
+      if (!ok || splits > 1 || (a.accumulate && k0 == k1)) continue;
       const int p = t.p0 + quad * 32 + lane, q = t.q0 + half * C::W;
       if constexpr (C::SWAP) {
         if (p < t.p_end) {
@@ -815,13 +823,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const int p32 = t.p0 + quad * 32;
           // (rows past an expert's last belong to the next one: only a warp whose rows are all inside, or end with D)
           if (a.bulk && (C::MODE != kGrouped || p32 + 32 <= t.p_end)) {
-            if (p32 < t.p_end) store_bulk<C::W>(map_d, a.out_f32, q, p32, C::MODE == kWgrad ? t.expert : 0, smem_u32(out) + (warp - 4) * (65536 / C::SW), lane, acc);
+            if (p32 < t.p_end && q < t.q_end)
+              store_bulk<C::W>(map_d, a.out_f32, q, t.q_end, p32, C::MODE == kWgrad ? t.expert : 0,
+                               smem_u32(out) + (warp - 4) * (C::OUT / C::SW), lane, acc);
             continue;
           }
           bulk_store_read(lane);  // what is still being copied out of the place that is turned around in
         }
         store_rows<C::W>(a, t.expert * a.d_expert + static_cast<int64_t>(p) * a.ldd + q, t.q_end - q, p < t.p_end,
-                         turn + (warp - 4) * (C::BULK ? 16384 / C::SW : 32 * 9), lane, acc);
+                         turn + (warp - 4) * (C::BULK ? C::OUT / 4 / C::SW : 32 * 9), lane, acc);
       }
     }
   }

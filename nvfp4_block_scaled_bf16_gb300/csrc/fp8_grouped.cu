@@ -23,7 +23,7 @@ nvfp4_status_t grouped(const char *name, const uint8_t *a, const float *sfa, con
   int64_t bound = ceil_div(t, tt) + experts;
   if (bound > t) bound = t;
   bound *= C::SWAP ? args.p_tiles : args.q_tiles;
-  if (bound >= (1LL << 31)) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", name);
+  if (bound >= (1LL << 31) - 1024) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", name);
   const int64_t br = n * experts;
   return fp8::launch_gemm<C>(name, C::SWAP ? b : a, C::SWAP ? br : t, C::SWAP ? a : b, C::SWAP ? t : br, k, bound, args, dev,
                              flags, stream);
@@ -113,6 +113,6 @@ extern "C" nvfp4_status_t fp8_grouped_weight_grad(const uint8_t *a, const float 
   args.experts = num_experts;
   args.total_rows = padded_rows;
   const int64_t tiles = static_cast<int64_t>(args.p_tiles) * args.q_tiles * num_experts;
-  if (tiles >= (1LL << 31)) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", name);
+  if (tiles >= (1LL << 31) - 1024) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", name);
   return fp8::launch_gemm<Grad>(name, a, n, b, k, padded_rows, tiles, args, dev, flags, stream);
 }
