@@ -217,6 +217,38 @@ int resident_blocks(const void *fn, int threads) {
   return blocks;
 }
 
+int resident_clusters(const void *fn, int threads, int smem, int size, int device) {
+  struct Entry {
+    const void *fn;
+    int size, device, n;
+  };
+  static Entry cache[256];
+  static int entries = 0;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    for (int i = 0; i < entries; ++i)
+      if (cache[i].fn == fn && cache[i].size == size && cache[i].device == device) return cache[i].n;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(size);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // consume the error so later calls do not see it
+    return 0;
+  }
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (entries < 256) cache[entries++] = Entry{fn, size, device, n};
+  return n;
+}
+
 nvfp4_status_t allow_smem(const void *fn, int bytes, int device) {
   const unsigned long long ctx = current_context_id();
   if (ctx != 0) {

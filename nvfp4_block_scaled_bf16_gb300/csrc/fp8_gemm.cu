@@ -21,11 +21,21 @@ struct Call {
 fp8::Scales row_scales(const float *p, int64_t rows) { return fp8::Scales{p, 0, 1, rows}; }
 fp8::Scales block_scales(const float *p, int64_t nk) { return fp8::Scales{p, 0, nk, 1}; }
 
-// CTAs of a cluster that share a tile's K (SWAP): as many as leave no SM without one, at most 8.
-int swap_splits(int64_t tiles, int nk, int sms) {
-  int64_t s = tiles > 0 ? sms / tiles : 1;
+// CTAs of a cluster that share a tile's K (SWAP), at most 8 and no more than leave all clusters room at once.  One CTA
+// an SM: as many as that.  Two: as few as reach four fifths of the SMs (32 x 4096 x 7168: 4 CTAs a tile 10.4 us, 8
+// 12.0; 1 x 14336 x 4096: 1 14.4, 2 12.5).
+template <class C>
+int splits_of(const Call &c) {
+  if (!C::SWAP) return 1;
+  const int64_t tiles = ceil_div(c.n, 128) * ceil_div(c.m, C::NT);
+  const int sms = c.dev->sm_count;
+  if (tiles > sms) return 1;
+  int64_t s = C::CTAS == 1 ? sms / tiles : ceil_div(sms * 4LL, 5 * tiles);
   if (s > 8) s = 8;
-  if (s > nk) s = nk;
+  if (s > c.args.nk) s = c.args.nk;
+  const void *fn = reinterpret_cast<const void *>(fp8::fp8_gemm_kernel<C>);
+  if (s > 1 && allow_smem(fn, C::SMEM, c.dev->device) != NVFP4_OK) return 1;
+  while (s > 1 && tiles > resident_clusters(fn, C::THREADS, C::SMEM, static_cast<int>(s), c.dev->device)) --s;
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
@@ -43,47 +53,55 @@ nvfp4_status_t run(const Call &c) {
   args.q_tiles = static_cast<int>(ceil_div(q, C::NT));
   const int64_t tiles = static_cast<int64_t>(args.p_tiles) * args.q_tiles;
   if (tiles >= (1LL << 31) - 1024) return fail(NVFP4_ERR_INVALID_ARG, "%s: problem too large", c.name);
-  args.splits = C::SWAP ? swap_splits(tiles, args.nk, c.dev->sm_count) : 1;
+  args.splits = splits_of<C>(c);
   return fp8::launch_gemm<C>(c.name, C::SWAP ? c.b : c.a, p, C::SWAP ? c.a : c.b, q, c.k, tiles, args, *c.dev, c.flags,
                              c.stream);
 }
 
-template <int NT>
-nvfp4_status_t run_swap(const Call &c) {
-  return c.block_b == 128 ? run<fp8::Cfg<NT, true, false, true, fp8::kDense>>(c)
-                          : run<fp8::Cfg<NT, true, true, true, fp8::kDense>>(c);
-}
-template <int NT>
-nvfp4_status_t run_rows(const Call &c) {
-  return c.block_b == 128 ? run<fp8::Cfg<NT, false, true, false, fp8::kDense>>(c)
-                          : run<fp8::Cfg<NT, false, true, true, fp8::kDense>>(c);
-}
+template <int NT, bool PER_ROW>
+using Swap = fp8::Cfg<NT, true, PER_ROW, true, fp8::kDense>;
+template <int NT, bool PER_ROW>
+using Rows = fp8::Cfg<NT, false, true, PER_ROW, fp8::kDense>;
 
 // Tiles of more than 128 tokens, by what they cost: rounds of tiles over the SMs times the time of a tile's blocks.
 // Measured (ns a block): tokens in the lanes 270, 310 and 460 at 64, 128 and 256 columns with a scale per block of
 // B, 310, 440 and 630 with one per row; the weight in the lanes (whose K a cluster can share) 310 and 440 at 64
-// and 128 columns, and 2500 ns to join a cluster's parts.
-enum Choice { kRows64, kRows128, kRows256, kSwap64, kSwap128 };
-Choice choose(int64_t m, int64_t n, int nk, bool per_row, int sms) {
-  const int64_t rows_ns[3] = {per_row ? 310 : 270, per_row ? 440 : 310, per_row ? 630 : 460}, swap_ns[2] = {310, 440};
-  Choice best = kRows256;
+// and 128 columns, 1000 more for a wider tile's ends, and 1400 to join a cluster's parts.
+template <bool PER_ROW>
+nvfp4_status_t run_many(const Call &c) {
+  const int64_t rows_ns[3] = {PER_ROW ? 310 : 270, PER_ROW ? 440 : 310, PER_ROW ? 630 : 460}, swap_ns[2] = {310, 440};
+  const int splits[2] = {splits_of<Swap<64, PER_ROW>>(c), splits_of<Swap<128, PER_ROW>>(c)};
+  int best = 2;
   double least = 1e300;
   for (int i = 0; i < 5; ++i) {
-    double cost;
-    if (i < 3) {
-      const int64_t tiles = ceil_div(m, 128) * ceil_div(n, 64LL << i);
-      cost = static_cast<double>(ceil_div(tiles, sms)) * nk * rows_ns[i];
-    } else {
-      const int64_t tiles = ceil_div(n, 128) * ceil_div(m, 64LL << (i - 3));
-      const int s = swap_splits(tiles, nk, sms);
-      cost = static_cast<double>(ceil_div(tiles, sms)) * ceil_div(nk, s) * swap_ns[i - 3] + (s > 1 ? 2500 : 0);
-    }
+    const bool rows = i < 3;
+    const int64_t width = 64LL << (rows ? i : i - 3);
+    const int64_t tiles = rows ? ceil_div(c.m, 128) * ceil_div(c.n, width) : ceil_div(c.n, 128) * ceil_div(c.m, width);
+    const double rounds = static_cast<double>(ceil_div(tiles, c.dev->sm_count));
+    double cost = rows ? rounds * c.args.nk * rows_ns[i] : rounds * ceil_div(c.args.nk, splits[i - 3]) * swap_ns[i - 3];
+    if (!rows) cost += (splits[i - 3] > 1 ? 1400 : 0) + (i == 4 ? 1000 : 0);
     if (cost < least) {
       least = cost;
-      best = static_cast<Choice>(i);
+      best = i;
     }
   }
-  return best;
+  switch (best) {
+    case 0: return run<Rows<64, PER_ROW>>(c);
+    case 1: return run<Rows<128, PER_ROW>>(c);
+    case 2: return run<Rows<256, PER_ROW>>(c);
+    case 3: return run<Swap<64, PER_ROW>>(c);
+    default: return run<Swap<128, PER_ROW>>(c);
+  }
+}
+
+// Up to 128 tokens: the weight in the lanes, the narrowest tile that holds them.
+template <bool PER_ROW>
+nvfp4_status_t run_any(const Call &c) {
+  if (c.m <= 16) return run<Swap<16, PER_ROW>>(c);
+  if (c.m <= 32) return run<Swap<32, PER_ROW>>(c);
+  if (c.m <= 64) return run<Swap<64, PER_ROW>>(c);
+  if (c.m <= 128) return run<Swap<128, PER_ROW>>(c);
+  return run_many<PER_ROW>(c);
 }
 
 }  // namespace
@@ -105,15 +123,5 @@ extern "C" nvfp4_status_t fp8_gemm(const uint8_t *a, const float *sfa, const uin
   if (st != NVFP4_OK) return st;
   Call c{name, a, b, m, n, k, block_b, fp8::Args{}, &dev, flags, stream, sfa, sfb};
   fp8::fill_args(c.args, d, d_type, accumulate, n, k, dev, flags);
-  if (m <= 16) return run_swap<16>(c);
-  if (m <= 32) return run_swap<32>(c);
-  if (m <= 64) return run_swap<64>(c);
-  if (m <= 128) return run_swap<128>(c);
-  switch (choose(m, n, c.args.nk, block_b == 1, dev.sm_count)) {
-    case kRows64: return run_rows<64>(c);
-    case kRows128: return run_rows<128>(c);
-    case kSwap64: return run_swap<64>(c);
-    case kSwap128: return run_swap<128>(c);
-    default: return run_rows<256>(c);
-  }
+  return block_b == 128 ? run_any<false>(c) : run_any<true>(c);
 }

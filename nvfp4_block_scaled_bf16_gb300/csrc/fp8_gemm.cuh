@@ -44,7 +44,9 @@ struct Cfg {
   // Wide rows of D leave through shared memory as bulk copies, so that the scaling warps go on with the next tile.  (Stored directly, 32 rows at a time by 32 bytes each, a 128 x 256 tile took 3200
   // cycles.)
   static constexpr bool BULK = !SWAP && NT == 256;
-  static constexpr int STAGES_FIT = (BULK ? 147456 : 200 * 1024) / STAGE;
+  // Few tokens: two CTAs to an SM, so that the weight's split over CTAs leaves fewer SMs idle.
+  static constexpr int CTAS = SWAP && NT <= 32 ? 2 : 1;
+  static constexpr int STAGES_FIT = (BULK ? 147456 : 200 * 1024 / CTAS) / STAGE;
   static constexpr int STAGES = STAGES_FIT > 12 ? 12 : STAGES_FIT;
   // Ring of the blocks' scales, which are asked for LEAD blocks before they are announced.
   static constexpr int SLOTS = BULK ? 6 : 8, LEAD = BULK ? 2 : 4;
@@ -66,7 +68,7 @@ struct Cfg {
   // f8f6f4: fp32 sums (1 at bit 4), e4m3 operands (0 at bits 7 and 10), both K-major
   static constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
                                     (static_cast<uint32_t>(128 >> 4) << 24);
-  static_assert(SMEM <= 232448, "smem");
+  static_assert(CTAS * (SMEM + 1024) <= 233472, "smem");
 };
 
 // Where an operand's scales lie: of row r (or of its block of 128) and block b along K at
@@ -433,7 +435,7 @@ __device__ __forceinline__ void store_rows(const Args &a, int64_t at, int n, boo
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1)
+__global__ void __launch_bounds__(C::THREADS, C::CTAS)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_d, const Args a) {
   extern __shared__ uint8_t smem_raw[];
@@ -884,11 +886,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // 32 float4 a column
       for (int i = threadIdx.x + rank * C::THREADS; i < cols * 32; i += C::THREADS * splits) {
         const uint32_t off = smem_u32(red) + i * 16;
-        float4 s = ld_cluster_v4(map_to_rank(off, 0));
-        for (int r = 1; r < splits; ++r) {
-          const float4 v = ld_cluster_v4(map_to_rank(off, r));
-          s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-        }
+        float4 part[8];  // every CTA's, asked for together
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < splits) part[r] = ld_cluster_v4(map_to_rank(off, r));
+        float4 s = part[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < splits) s = make_float4(s.x + part[r].x, s.y + part[r].y, s.z + part[r].z, s.w + part[r].w);
         const int p = t.p0 + (i % 32) * 4;
         const int64_t at = static_cast<int64_t>(t.q0 + i / 32) * a.ldd + p;
         const float v[4] = {s.x, s.y, s.z, s.w};
@@ -963,7 +968,7 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
   const int cluster = args.splits;
   int64_t grid = tiles * cluster;
   // split tiles: one per cluster (their partials are joined once); else persistent
-  const int64_t cap = dev.sm_count / cluster * cluster;
+  const int64_t cap = static_cast<int64_t>(dev.sm_count) * C::CTAS / cluster * cluster;
   if (args.splits == 1 && grid > cap) grid = cap;
   cudaError_t e = launch(kern, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), C::SMEM, (cudaStream_t)stream,
                          (flags & NVFP4_FLAG_PDL) != 0, cluster, mp, mq, md, args);

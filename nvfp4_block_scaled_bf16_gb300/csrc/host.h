@@ -62,6 +62,11 @@ nvfp4_status_t allow_smem(const void *fn, int bytes, int device);
 // 1 if the query fails.
 int resident_blocks(const void *fn, int threads);
 
+// Clusters of `size` such blocks that the device holds at once (a cluster lies within a GPC, so they are fewer than
+// the SMs would suggest: 16 of 8 blocks do not fit 152 SMs); asked once per kernel, size and device.  0 if the query
+// fails.  `smem` must have been allowed.
+int resident_clusters(const void *fn, int threads, int smem, int size, int device);
+
 inline bool aligned(const void *p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
