@@ -9,10 +9,11 @@
 // What bounds it, measured on 128 x 256 tiles (cycles a block).  The products alone take 512 (8192 multiply-adds a
 // cycle), reading the sums 136 (0.53 a column and quarter of the SM).  Scaling with scalar multiply-adds slows the
 // products to 930; with pairs (fma.rn.f32x2) they take 566 beside it, and the scaling 475, twice that with a factor per
-// column too.  What is left of the 900 that a block takes (4096 x 4864 x 7168 in 109 us, 2.6 PFLOP/s; 1270 with a
-// factor per column, 146 us) is the chain from a block's products through the scaling warps back to the buffer:
-// four warps to a scheduler hide more of it than two with more columns each (123 us) or than CTA pairs, which halve
-// the operands' traffic but lengthen the chain (111 us).
+// column too.  What is left of the 850 that a block takes (4096 x 4864 x 7168 in 103 us, 2.8 PFLOP/s; 1200 with a
+// factor per column, 145 us) is the chain from a block's products through the scaling warps back to the buffer:
+// without the loads of one operand it is 99 us still.  Four warps to a scheduler hide more of it than two with more
+// columns each (123 us), than CTA pairs, which halve the operands' traffic but lengthen the chain (111 us), or than two
+// CTAs an SM with 128 columns each (141 us).
 //
 // The operand whose rows lie in the 128 tensor-memory lanes is P, the other (the columns) is Q.
 // Usually P is A (the tokens); with SWAP it is B (a weight), so that few tokens fill a narrow tile.
@@ -41,8 +42,8 @@ struct Cfg {
   static constexpr int P_BYTES = 128 * 128;
   static constexpr int Q_BYTES = NT * 128;
   static constexpr int STAGE = P_BYTES + Q_BYTES;
-  // Wide rows of D leave through shared memory as bulk copies, so that the scaling warps go on with the next tile.  (Stored directly, 32 rows at a time by 32 bytes each, a 128 x 256 tile took 3200
-  // cycles.)
+  // Wide rows of D leave through shared memory as bulk copies, so that the scaling warps go on with the next tile.
+  // (Stored directly, 32 rows at a time by 32 bytes each, a 128 x 256 tile took 3200 cycles.)
   static constexpr bool BULK = !SWAP && NT == 256;
   // Few tokens: two CTAs to an SM, so that the weight's split over CTAs leaves fewer SMs idle.
   static constexpr int CTAS = SWAP && NT <= 32 ? 2 : 1;
@@ -61,7 +62,8 @@ struct Cfg {
   static constexpr int SC_BYTES = (SC_P + SC_Q) * 4;
   static constexpr int TABLE = MODE == kDense ? 0 : 2 * (kMaxExperts + 4) * 4;
   static constexpr int OUT = BULK ? 65536 : 0;  // 128 rows x 512 bytes
-  static constexpr int TURN = SWAP || BULK ? 0 : SW * 32 * 9 * 4;  // where rows of D that are not aligned are turned around (BULK: in OUT)
+  // where rows of D that are not aligned are turned around (BULK: in OUT)
+  static constexpr int TURN = SWAP || BULK ? 0 : SW * 32 * 9 * 4;
   static constexpr int CTRL = 512;
   static_assert(NACC <= STAGES, "a buffer's next block must have a stage of its own");
   static constexpr int SMEM = 1024 + STAGES * STAGE + OUT + SLOTS * SC_BYTES + TABLE + TURN + CTRL;
@@ -174,11 +176,9 @@ __device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
-// (volatile: the compiler otherwise puts the sums of one chunk of columns off past the loads of the next, and
-// runs out of registers)
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
-  asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
 __device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
@@ -551,7 +551,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
   uint64_t acc[C::W / 2];  // pairs of columns
   if (warp < 4) {
-    if constexpr (C::SW == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // (640 threads of 96 registers: 4 warps at 40 and 16 at 104 are 95 of them.  With 56 instead of 40, which the
+    // scaling warps cannot use, the compiler spilled more of them: 107 and 156 us instead of 103 and 145.)
+    if constexpr (C::SW == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
       // ------------------------------------------------------------ operands
       if (lane == 0) {
