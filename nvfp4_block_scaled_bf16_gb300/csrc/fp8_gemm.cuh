@@ -9,7 +9,7 @@
 // What bounds it, measured on 128 x 256 tiles (cycles a block).  The products alone take 512 (8192 multiply-adds a
 // cycle), reading the sums 136 (0.53 a column and quarter of the SM).  Scaling with scalar multiply-adds slows the
 // products to 930; with pairs (fma.rn.f32x2) they take 566 beside it, and the scaling 475, twice that with a factor per
-// column too.  What is left of the 850 that a block takes (4096 x 4864 x 7168 in 103 us, 2.8 PFLOP/s; 1200 with a
+// column too.  What is left of the 850 that a block takes (4096 x 4864 x 7168 in 103 us, 2.8 PFLOP/s; 1250 with a
 // factor per column, 145 us) is the chain from a block's products through the scaling warps back to the buffer:
 // without the loads of one operand it is 99 us still.  Four warps to a scheduler hide more of it than two with more
 // columns each (123 us), than CTA pairs, which halve the operands' traffic but lengthen the chain (111 us), or than two
@@ -551,8 +551,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
   uint64_t acc[C::W / 2];  // pairs of columns
   if (warp < 4) {
-    // (640 threads of 96 registers: 4 warps at 40 and 16 at 104 are 95 of them.  With 56 instead of 40, which the
-    // scaling warps cannot use, the compiler spilled more of them: 107 and 156 us instead of 103 and 145.)
+    // (640 threads begin with 96 registers; 4 warps at 40 and 16 at 104 need 91 of them.  56 instead of 40 gives the
+    // scaling warps no less, but the compiler spilled more there: 107 and 156 us instead of 103 and 145.)
     if constexpr (C::SW == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
       // ------------------------------------------------------------ operands

@@ -3,10 +3,14 @@
 //
 // A block with largest magnitude amax (at least 2^-100) has scale s = fl(amax / 448) and codes
 // e4m3(fl(x * fl(448 / amax))): every step is one fp32 rounding to nearest even, so the codes are the same
-// wherever a block is quantised.  A NaN outweighs
-// every magnitude: a block that holds one, or an infinity, gets a scale and codes that stand for nothing finite.
+// wherever a block is quantised.  A NaN outweighs every magnitude: a block that holds one, or an infinity, gets a
+// scale and codes that stand for nothing finite.
 //
-// All of it is bound by memory: a value is read once (2 or 4 bytes) and written once or twice (1 byte each).
+// The least that any of it does is to move each value once in (2 or 4 bytes) and once or twice out (1 byte each).
+// Along the rows and per 128 x 128 block memory bounds it: 8192 x 7168 bf16 28 us (6.3 TB/s), fp32 4096 x 7168 24 us
+// (6.2); an fp32 weight of 4096 x 7168 and its transpose 30 us (5.8).  Both ways from one read is half bound by instructions
+// (two products, two conversions and the exchange of the columns' magnitudes a value): 4096 x 7168 bf16 23 us
+// (5.2 TB/s), and 32,768 rows of 2048 gathered from 4096, whose reads stay in L2, 51 us where the writes alone need 23.
 #include "host.h"
 #include "ptx.cuh"
 
