@@ -497,7 +497,7 @@ nvfp4_status_t sample_tokens(const void *logits, int logits_type, int64_t ld, co
  * (taken as at least 2^-100) gets
  *   s = fl(amax / 448),  codes e4m3(fl(x * fl(448 / amax)))  (RNE, saturating)
  * with fl one rounding to fp32, so that a code times s stands for x within 2^-4 of x where |x| is
- * at least amax * 2^-6 / 448, and within amax / 448 * 2^-10 below.  A block that holds an infinity or a NaN
+ * at least amax * 2^-6 / 448, and within amax / 448 * 2^-10 below (each but for the fp32 roundings).  A block that holds an infinity or a NaN
  * comes back as no finite number.  The sources quantise to 4 bits only; this is the 8-bit counterpart
  * of nvfp4_quantize, with blocks of the usual 128.
  *   x           bf16 or fp32 (x_type: NVFP4_DTYPE_*) [x_rows, k], row stride ldx >= k or 0 (one row for all);

@@ -1009,7 +1009,7 @@ def fp8_gemm(a, sfa, b, sfb, block_b: int = 128, out_dtype=torch.bfloat16, d=Non
 def fp8_grouped_gemm(a, sfa, row_offsets, b, sfb, out_dtype=torch.bfloat16, d=None, flags: int = 0, stream=None):
     """Per expert e: D[rows of e] = deq(A_e) @ deq(B_e)^T; a e4m3 [t, k] with its rows sorted by expert (sfa
     [ceil(k/128), t]), b e4m3 [E, n, k] (sfb [E, ceil(n/128), ceil(k/128)]), D bf16 or fp32.  Rows past the last
-    expert's stay as they were."""
+    expert's stay as they were (in a new D: whatever its memory held)."""
     dev = _codes(a, 2, b, 3)
     t, k = a.shape
     experts, n, kb = b.shape
@@ -1051,8 +1051,8 @@ def fp8_grouped_weight_grad(a, sfa, b, sfb, row_offsets, out_dtype=torch.bfloat1
 # ---------------------------------------------------------------- gradients of the MoE steps
 def moe_combine_backward(dout, y, pos, weights, dy=None, dweights=None, flags: int = 0, stream=None):
     """Gradients of moe_combine: (dy bf16 [rows, h], dweights fp32 [T, topk]) with dy[pos[t, j]] = weights[t, j] *
-    dout[t] and dweights[t, j] = dout[t] . y[pos[t, j]].  Rows of dy that no slot names stay as they were; no row
-    may be named twice (moe_sort_by_expert's pos names none twice)."""
+    dout[t] and dweights[t, j] = dout[t] . y[pos[t, j]].  Rows of dy that no slot names stay as they were (in a
+    new dy: whatever its memory held); no row may be named twice (moe_sort_by_expert's pos names none twice)."""
     cur = _current_device()
     if not (_is(y, torch.bfloat16, 2, cur) and _is(pos, torch.int32, 2, cur) and _is(weights, torch.float32, 2, cur)):
         _need(y, torch.bfloat16, "y", 2)

@@ -958,7 +958,8 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
   }
   CUtensorMap md = mp;
   const int64_t es = args.out_f32 ? 4 : 2;
-  args.bulk = C::BULK && !args.accumulate && args.ldd * es % 16 == 0 && args.d_expert * es % 16 == 0;
+  // (a copy's place in a row is 32 signed bits of bytes)
+  args.bulk = C::BULK && !args.accumulate && args.ldd * es % 16 == 0 && args.d_expert * es % 16 == 0 && args.ldd * es < (1LL << 31);
   if (args.bulk) {
     const int64_t rows = C::MODE == kWgrad ? args.p_rows : p_rows, depth = C::MODE == kWgrad ? args.experts : 1;
     st = encode_tmap_store_u8(&md, args.d, args.ldd * es, rows, depth, args.ldd * es, rows * args.ldd * es, 32);

@@ -87,6 +87,27 @@ def test_results_past_32_bit_offsets(nv):
     nv.check_status()
 
 
+def test_rows_of_more_than_2_gb(nv):
+    """A weight gradient whose rows are longer than 2^31 bytes: a bulk copy's place in such a row would not fit its 32
+    bits.  One expert of one row: D[0, c] = sum over r of a[0, r] b[c, r], ones and twos at known columns."""
+    k = 2 ** 29 + 64
+    if torch.cuda.mem_get_info()[0] < 90 * 2 ** 30:
+        pytest.skip("needs 90 GB")
+    one, two = 0x38, 0x40
+    a = torch.full((1, 128), one, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    b = torch.zeros((k, 128), dtype=torch.uint8, device="cuda")
+    at = torch.tensor([0, 1, 255, 256, 2 ** 28, 2 ** 29 - 1, 2 ** 29, 2 ** 29 + 1, k - 1], device="cuda")
+    b[at, 5] = two
+    b[at, 7] = one
+    sfa, sfb = torch.ones((1, 1), device="cuda"), torch.ones((1, k), device="cuda")
+    offsets = torch.tensor([0, 100], device="cuda")
+    d = torch.full((1, 1, k), -1.0, device="cuda")
+    nv.fp8_grouped_weight_grad(a, sfa, b.view(torch.float8_e4m3fn), sfb, offsets, d=d)
+    nv.check_status()
+    assert bool((d[0, 0, at] == 3.0).all())
+    assert int((d != 0).sum()) == at.numel()
+
+
 def test_misaligned_outputs_are_refused(nv):
     a, sa, b, sb = codes(1, 8, 128), scales(2, 1, 8), codes(3, 33, 128), scales(4, 1, 1)
     with pytest.raises(nv.NVFP4Error):
