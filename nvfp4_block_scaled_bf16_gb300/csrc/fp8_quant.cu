@@ -8,9 +8,10 @@
 //
 // The least that any of it does is to move each value once in (2 or 4 bytes) and once or twice out (1 byte each).
 // Along the rows and per 128 x 128 block memory bounds it: 8192 x 7168 bf16 28 us (6.3 TB/s), fp32 4096 x 7168 24 us
-// (6.2); an fp32 weight of 4096 x 7168 and its transpose 30 us (5.8).  Both ways from one read is half bound by instructions
-// (two products, two conversions and the exchange of the columns' magnitudes a value): 4096 x 7168 bf16 23 us
-// (5.2 TB/s), and 32,768 rows of 2048 gathered from 4096, whose reads stay in L2, 51 us where the writes alone need 23.
+// (6.2); an fp32 weight of 4096 x 7168 and its transpose 29 us (6.0).  Both ways from one read is half bound by
+// instructions (two products, two conversions and the exchange of the columns' magnitudes a value): 4096 x 7168 bf16
+// 22 us (5.3 TB/s), and 32,768 rows of 2048 gathered from 4096, whose reads stay in L2, 49 us where the writes alone
+// need 23.
 #include "host.h"
 #include "ptx.cuh"
 
@@ -284,6 +285,17 @@ __global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_tile_kernel(co
     row0 = blk * 128;
     rows = min(static_cast<int64_t>(128), a.m - row0);
   }
+  const int b0 = blockIdx.y * a.chain, b1 = min(a.kb, b0 + a.chain);
+  const int64_t ldt = ALONG == kBlock ? a.m : a.row_blocks * 128;
+  const int ch = tid % 8;  // 16-byte piece of a column's 128 rows
+  if (ALONG != kBlock && rows == 0) {  // zeros and their scale (one block in six where 128 experts share 32,768 rows)
+    const int64_t c1 = min(static_cast<int64_t>(a.k), static_cast<int64_t>(b1) * 128);
+    for (int64_t c = static_cast<int64_t>(b0) * 128 + tid / 8; c < c1; c += kQuantThreads / 8)
+      *reinterpret_cast<uint4 *>(a.qt + c * ldt + blk * 128 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
+    const float s = __fdiv_rn(__uint_as_float(kTinyBits), 448.0f);
+    for (int64_t c = static_cast<int64_t>(b0) * 128 + tid; c < c1; c += kQuantThreads) a.sft[blk * a.k + c] = s;
+    return;
+  }
   // this thread's four rows
   const int r0 = warp * 16 + rg * 4;
   const uint8_t *xp[4];
@@ -299,11 +311,8 @@ __global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_tile_kernel(co
     }
     xp[i] = xr < 0 ? nullptr : static_cast<const uint8_t *>(a.x) + (xr * a.ldx + cg * 16) * (F32 ? 4 : 2);
   }
-  const int b0 = blockIdx.y * a.chain, b1 = min(a.kb, b0 + a.chain);
   // where this thread's codes go in the first tile: its rows', and its piece of the columns' (a column in 32)
   uint8_t *qp = ALONG == kColumns ? nullptr : a.q + (row0 + r0) * a.k + b0 * 128 + cg * 16;
-  const int64_t ldt = ALONG == kBlock ? a.m : a.row_blocks * 128;
-  const int ch = tid % 8;  // 16-byte piece of a column's 128 rows
   uint8_t *tp = nullptr;
   if (ALONG != kBlock) tp = a.qt + (static_cast<int64_t>(b0) * 128 + tid / 8) * ldt + blk * 128 + ch * 16;
   else if (a.qt) tp = a.qt + (mat * a.k + static_cast<int64_t>(b0) * 128 + tid / 8) * ldt + mblk * 128 + ch * 16;
@@ -448,10 +457,12 @@ int wide_rows(const void *x, int x_type, int64_t ldx) {
 
 template <int ALONG>
 cudaError_t launch_tiles(int x_type, TileArgs &a, int64_t blocks, const DeviceInfo &dev, uint32_t flags, nvfp4_stream_t s) {
-  // tiles that a CTA takes in turn: one while that fills the device, then as many as leave it four rounds
-  const int64_t tiles = blocks * a.kb, want = static_cast<int64_t>(dev.sm_count) * 8;
+  // tiles that a CTA takes in turn, so that its rows' places are looked up once: at most 3, and no more than leave four
+  // CTAs an SM (32,768 rows of 2048 over 128 experts: 1 60 us, 2 52, 3 49, 4 50, 8 58)
+  const int64_t tiles = blocks * a.kb, want = static_cast<int64_t>(dev.sm_count) * 4;
   int64_t chain = tiles / want;
-  chain = chain < 1 ? 1 : chain > 8 ? 8 : chain;
+  chain = chain < 1 ? 1 : chain > 3 ? 3 : chain;
+  chain = ceil_div(a.kb, ceil_div(a.kb, chain));  // as many to every CTA
   a.chain = static_cast<int>(chain);
   auto kern = x_type == NVFP4_DTYPE_F32 ? fp8_tile_kernel<true, ALONG> : fp8_tile_kernel<false, ALONG>;
   return launch(kern, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(ceil_div(a.kb, chain))), dim3(kQuantThreads),
