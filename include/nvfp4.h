@@ -510,7 +510,7 @@ nvfp4_status_t sample_tokens(const void *logits, int logits_type, int64_t ld, co
  *               128 columns (a block of columns' scales lie together), or both NULL
  *   qt, sft     along the columns, transposed: e4m3 [k, P], fp32 [P/128, k] with
  *               P = fp8_padded_rows(rows, num_experts): one scale per column and 128 rows, or both NULL.
- *               Columns past the last row hold zeros.
+ *               Columns past the last row hold zeros (as codes of their block: beside a NaN they stand for NaN).
  *   row_offsets int64 [num_experts+1] on the device (as moe_sort_by_expert writes it; its last entry
  *               may be below rows) or NULL with num_experts 0.  Expert e's rows begin at column
  *               sum_{j<e} round_up(M_j, 128) of qt, so that no block spans two experts; rows past the last
