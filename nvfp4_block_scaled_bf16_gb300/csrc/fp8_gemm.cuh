@@ -103,6 +103,7 @@ struct Args {
   int nk;                    // blocks along K (dense and grouped)
   int p_tiles, q_tiles;      // tiles along the static operands
   Divisor per_expert, group; // p_tiles * q_tiles; kGroup * q_tiles
+  Divisor tail;              // tiles along P of the last, shorter group
   int splits;                // dense with SWAP: CTAs of a cluster that share a tile's K
   int out_f32, accumulate;
   int bulk;                  // rows of D start on 16 bytes and are not accumulated: bulk copies
@@ -256,7 +257,7 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const Tables &tb, int t) 
   // groups of tiles along P: what runs at the same time shares both operands through L2
   const int g = a.group.quotient(t), l = t - g * static_cast<int>(a.group.d);
   const int gs = min(kGroup, a.p_tiles - g * kGroup);
-  qi = gs == kGroup ? l / kGroup : l / gs;
+  qi = gs == kGroup ? l / kGroup : a.tail.quotient(l);
   pi = g * kGroup + l - qi * gs;
   r.p0 = r.py = pi * 128;
   r.q0 = r.qy = qi * C::NT;
@@ -955,6 +956,7 @@ nvfp4_status_t launch_gemm(const char *name, const uint8_t *p, int64_t p_rows, c
   if (C::MODE != kGrouped) {
     args.per_expert = Divisor::of(static_cast<uint32_t>(args.p_tiles) * args.q_tiles);  // (the tiles are fewer than 2^31)
     args.group = Divisor::of(static_cast<uint32_t>(kGroup) * args.q_tiles);
+    args.tail = Divisor::of(static_cast<uint32_t>(args.p_tiles % kGroup ? args.p_tiles % kGroup : 1));
   }
   CUtensorMap md = mp;
   const int64_t es = args.out_f32 ? 4 : 2;
