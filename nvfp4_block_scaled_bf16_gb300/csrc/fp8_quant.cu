@@ -10,7 +10,7 @@
 // Along the rows and per 128 x 128 block memory bounds it: 8192 x 7168 bf16 28 us (6.3 TB/s), fp32 4096 x 7168 24 us
 // (6.2); an fp32 weight of 4096 x 7168 and its transpose 29 us (6.0).  Both ways from one read is half bound by
 // instructions (two products, two conversions and the exchange of the columns' magnitudes a value): 4096 x 7168 bf16
-// 22 us (5.3 TB/s), and 32,768 rows of 2048 gathered from 4096, whose reads stay in L2, 49 us where the writes alone
+// 22 us (5.3 TB/s), and 32,768 rows of 2048 gathered from 4096, whose reads stay in L2, 47 us where the writes alone
 // need 23.
 #include "host.h"
 #include "ptx.cuh"
@@ -330,6 +330,14 @@ __global__ void __launch_bounds__(kQuantThreads, F32 ? 2 : 3) fp8_tile_kernel(co
         else v[i].load16(p);
       }
     }
+    // The next tile's rows into L1 meanwhile, where an expert's rows are read (32,768 of 2048 gathered from 4096: 49.4 ->
+    // 47.4 us, not gathered 55.6 -> 52.7).  Plain rows, more tiles at once, lost by it (4096 x 7168 22.4 -> 23.5 us).
+    if (ALONG != kBlock && a.row_offsets && b + 1 < b1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (xp[i] && c0 + 128 + cg * 16 < a.k)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(xp[i] + static_cast<int64_t>(c0 + 128) * (F32 ? 4 : 2)));
+    }
     float fb = 0.0f;  // kBlock: the tile's factor
     if constexpr (ALONG == kBlock) {
       uint32_t am = max(max(v[0].amax(), v[1].amax()), max(v[2].amax(), v[3].amax()));
@@ -458,7 +466,7 @@ int wide_rows(const void *x, int x_type, int64_t ldx) {
 template <int ALONG>
 cudaError_t launch_tiles(int x_type, TileArgs &a, int64_t blocks, const DeviceInfo &dev, uint32_t flags, nvfp4_stream_t s) {
   // tiles that a CTA takes in turn, so that its rows' places are looked up once: at most 3, and no more than leave four
-  // CTAs an SM (32,768 rows of 2048 over 128 experts: 1 60 us, 2 52, 3 49, 4 50, 8 58)
+  // CTAs an SM (32,768 rows of 2048 over 128 experts, without the prefetch: 1 60 us, 2 52, 3 49, 4 50, 8 58)
   const int64_t tiles = blocks * a.kb, want = static_cast<int64_t>(dev.sm_count) * 4;
   int64_t chain = tiles / want;
   chain = chain < 1 ? 1 : chain > 3 ? 3 : chain;
