@@ -885,7 +885,8 @@ def fp8_quantize(x, src_rows=None, row_offsets=None, rows: bool = True, transpos
 
     Along the rows (rows=True): q [m, k], sf [ceil(k/128), m].  Along the columns and transposed
     (transpose=True): qt [k, P], sft [P/128, k] with P = fp8_padded_rows(m, experts); with row_offsets (int64
-    [E+1]) each expert's rows begin at a multiple of 128 there.  src_rows (int32 [m]): row r of the result is
+    [E+1]) each expert's rows begin at a multiple of 128 there, and rows past the last expert's are not quantised (q and
+    sf stay as they were there; new ones hold whatever their memory held).  src_rows (int32 [m]): row r of the result is
     x[src_rows[r]] (without it m = n).  Returns (q, sf), (qt, sft) or (q, sf, qt, sft); x is read once."""
     if _is(x, torch.bfloat16, 2, _current_device()):
         xt, (n, k) = 0, x.shape
