@@ -536,7 +536,8 @@ nvfp4_status_t fp8_quantize_weight(const void *w, int w_type, int64_t matrices, 
 /* Product of two such matrices:
  *   D[i, j] = sum over blocks b of sa[i, b] * sb[j, b] * (sum over the block's k of A[i, k] B[j, k])
  * The sums inside a block are the tensor core's, the scaled sums over the blocks fp32; one rounding to
- * D's type at the end.
+ * D's type at the end.  The order of the two scales is the kernel's, but over all scales that the quantiser gives (2^-109
+ * to 2^120) a block's term leaves fp32's range only where sa * sb * its sum does.
  *   a, sfa   e4m3 [m, k] and fp32 [ceil(k/128), m], as fp8_quantize's q and sf
  *   b, sfb   e4m3 [n, k]; block_b = 128: fp32 [ceil(n/128), ceil(k/128)] (fp8_quantize_weight);
  *            block_b = 1: fp32 [ceil(k/128), n] (fp8_quantize)

@@ -59,7 +59,7 @@ struct Cfg {
   static constexpr int CH = W <= 32 ? W / 2 : NT >= 256 ? 16 : 32;  // columns loaded at a time
   static constexpr int SC_P = PV ? 128 : 4;
   static constexpr int SC_Q = CV ? NT : 4;
-  static constexpr int SC_BYTES = (SC_P + SC_Q) * 4;
+  static constexpr int SC_BYTES = (SC_P + SC_Q + (CV ? 4 : 0)) * 4;  // CV: and whether a column's scale is far out
   static constexpr int TABLE = MODE == kDense ? 0 : 2 * (kMaxExperts + 4) * 4;
   static constexpr int OUT = BULK ? 65536 : 0;  // 128 rows x 512 bytes
   // where rows of D that are not aligned are turned around (BULK: in OUT)
@@ -164,6 +164,20 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
                  : "r"(taddr));
   }
 }
+// Multiplies COLS consecutive tensor-memory columns of the warp's 32 lanes, each lane's by its own factor.
+template <int COLS>
+__device__ __forceinline__ void tmem_scale(uint32_t taddr, float factor) {
+#pragma unroll
+  for (int c = 0; c < COLS; c += 8) {
+    uint32_t v[8];
+    tmem_ld<8>(taddr + c, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), factor));
+    tmem_st_32x32b<8>(taddr + c, v);
+  }
+  tmem_st_wait();
+}
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -195,6 +209,61 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The factor f of a block's sums v in this lane: the scale of its row, and with !CV that of the warp's columns too (with
+// CV each column's comes from the table, v * column's scale * f).  The quantiser's scales lie in [2^-109, 2^120) and a
+// nonzero v in [2^-18, 2^24.7), so that v times one of them, or their product, may leave fp32 where v times both does not.
+// Where some lane's could (true is returned), the sums are multiplied by `first` and what is left is f:
+//   !CV: where the two scales' product is no normal number (but for a row's scale of zero: a row past the end) `first` is
+//        the lesser scale, f the greater;
+//   CV:  where a column's scale of more than 2^103 lets v * scale overflow too early (the warp that loads the scales
+//        says so behind them) `first` is the power of two in a row's scale below 1, f the rest of it, so that no result
+//        changes but those that overflowed.
+// The test costs the grouped products 5 to 9 % (32768 rows over 128 experts 124 -> 130 us, over 8 of 2048 x 1536 98 -> 106),
+// 256-column tiles with a scale per column up to 5 % (4096 x 4864 x 7168: 146 -> 152), the others 1 to 3 %.  Anything in the
+// loop over the columns costs more (4096 x 4096 x 7168, 104 us without, 105 with the test: a branch there 115, a second
+// product 146).
+template <class C>
+__device__ __forceinline__ bool block_factors(const float *sc, int quad, int half, int lane, float &f, float &first) {
+  const float sp = C::PV ? sc[quad * 32 + lane] : sc[0];
+  first = 1.0f;
+  if constexpr (C::CV) {
+    f = sp;
+    if (sc[C::SC_P + C::SC_Q] == 0.0f) return false;
+    const uint32_t bits = __float_as_uint(sp);
+    if (bits - 0x00800000u < 0x3F000000u) {  // a normal number below 1
+      first = __uint_as_float(bits & 0x7F800000u);
+      f = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
+    }
+  } else {
+    const float sq = sc[C::SC_P + half * C::W / 128];
+    f = sp * sq;
+    const bool far = __float_as_uint(f) - 0x00800000u >= 0x7F000000u && sp != 0.0f;
+    if (!__any_sync(0xFFFFFFFFu, far)) return false;
+    if (far) {  // (selects, not fminf: a NaN stays)
+      first = sp < sq ? sp : sq;
+      f = sp < sq ? sq : sp;
+    }
+  }
+  return true;
+}
+// Adds CH columns of a block's sums, times their factors, to the accumulators; cols: the columns' scales.
+template <class C>
+__device__ __forceinline__ void add_scaled(const uint32_t (&v)[C::CH], const float *cols, float f, uint64_t *sum) {
+  const uint64_t f2 = pack2(f, f);
+  if constexpr (C::CV) {
+    const ulonglong2 *cs = reinterpret_cast<const ulonglong2 *>(cols);
+#pragma unroll
+    for (int j = 0; j < C::CH; j += 4) {
+      const ulonglong2 s = cs[j / 4];
+      sum[j / 2] = fma2(mul2f(pack2u(v[j], v[j + 1]), s.x), f2, sum[j / 2]);
+      sum[j / 2 + 1] = fma2(mul2f(pack2u(v[j + 2], v[j + 3]), s.y), f2, sum[j / 2 + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C::CH; j += 2) sum[j / 2] = fma2(pack2u(v[j], v[j + 1]), f2, sum[j / 2]);
+  }
 }
 
 enum Site { kSiteLoad = 0, kSiteMmaStage = 2, kSiteScaleSlot = 4, kSiteScaleStage = 5, kSiteAcc = 6 };
@@ -641,6 +710,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             ok = __all_sync(0xFFFFFFFFu, is);
           }
           __syncwarp();
+          if constexpr (C::CV) {  // see block_factors
+            float *sc = scales + (n % C::SLOTS) * (C::SC_BYTES / 4);
+            float most = sc[C::SC_P + (C::NT < 32 ? lane % C::NT : lane)];
+#pragma unroll
+            for (int j = 1; j < C::NT / 32; ++j) most = fmaxf(most, sc[C::SC_P + j * 32 + lane]);
+            const bool far = __any_sync(0xFFFFFFFFu, most > 0x1p103f);
+            if (lane == 0) sc[C::SC_P + C::SC_Q] = far ? 1.0f : 0.0f;
+          }
           if (ok) arrive_lane0(smem_u32(&full[n % C::STAGES]), lane);
         }
         i += 2;
@@ -650,7 +727,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         int k0, k1;
         k_range(t, k0, k1);
         // where this lane's scales of the tile's rows lie (a scale per row: the rows' lie side by side)
-        const int pr = C::PV ? t.p0 + lane : 0, qr = t.q0 + (C::CV ? lane : lane * 128);
+        const int pr = C::PV ? t.p0 + lane : 0, qr = C::CV ? t.q0 + lane : min(t.q0 + lane * 128, t.q_end - 1);
         const float *pp = a.sp.p + t.expert * a.sp.es + (C::PV ? pr : t.p0 / 128 * a.sp.rs) + t.kb0 * a.sp.ks;
         const float *qp = a.sq.p + t.expert * a.sq.es + (C::CV ? qr : qr / 128 * a.sq.rs) + t.kb0 * a.sq.ks;
         for (int kb = k0; kb < k1 && ok; ++kb, ++block) {
@@ -672,7 +749,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               if (C::NT >= 32 || lane < C::NT)
                 cp_async_4(dst + C::SC_P * 4 + j * 128, qr + j * 32 < t.q_end ? qb + j * 32 : a.sq.p, qr + j * 32 < t.q_end);
           } else if (lane < (C::NT + 127) / 128) {
-            cp_async_4(dst + C::SC_P * 4, qr < t.q_end ? qb : a.sq.p, qr < t.q_end);
+            cp_async_4(dst + C::SC_P * 4, qb, true);
           }
           announce();
         }
@@ -702,14 +779,19 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       if constexpr (C::SW == 16) {
         // four warps to a scheduler: one's waits pass while the others have work
         for (int kb = k0; kb < k1; ++kb) {
+          if constexpr (C::CV) {  // (three counters fewer in 104 registers: weight gradients 229 -> 221 us, but others lose)
+            static_assert(C::SLOTS == 2 * C::STAGES && C::SLOTS % C::NACC == 0, "the slot gives a block's other places");
+            phase = slot >= C::STAGES ? 1u : 0u;
+            stage = slot >= C::STAGES ? slot - C::STAGES : slot;
+            ab = slot % C::NACC;
+          }
           const bool ready = mbar_try_wait(smem_u32(&done[stage]), phase);
           if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&done[stage]), phase, wc, kSiteAcc));
           if (!ok) break;
           tc_fence_after();
           const float *sc = scales + slot * (C::SC_BYTES / 4);
-          float f = C::PV ? sc[quad * 32 + lane] : sc[0];
-          if constexpr (!C::CV) f *= sc[C::SC_P + half * C::W / 128];
-          const uint64_t f2 = pack2(f, f);
+          float f, first;
+          if (block_factors<C>(sc, quad, half, lane, f, first)) tmem_scale<C::W>(t_lane + ab * C::NT, first);
 #pragma unroll
           for (int c = 0; c < C::W; c += C::CH) {
             uint32_t v[C::CH];
@@ -720,27 +802,17 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               const int next = stage + C::NACC >= C::STAGES ? stage + C::NACC - C::STAGES : stage + C::NACC;
               arrive_lane0(smem_u32(&full[next]), lane);
             }
-            uint64_t *sum = acc + c / 2;
-            if constexpr (C::CV) {
-              const ulonglong2 *cs = reinterpret_cast<const ulonglong2 *>(sc + C::SC_P + half * C::W + c);
-#pragma unroll
-              for (int j = 0; j < C::CH; j += 4) {
-                const ulonglong2 s = cs[j / 4];
-                sum[j / 2] = fma2(mul2f(pack2u(v[j], v[j + 1]), s.x), f2, sum[j / 2]);
-                sum[j / 2 + 1] = fma2(mul2f(pack2u(v[j + 2], v[j + 3]), s.y), f2, sum[j / 2 + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < C::CH; j += 2) sum[j / 2] = fma2(pack2u(v[j], v[j + 1]), f2, sum[j / 2]);
-            }
+            add_scaled<C>(v, sc + C::SC_P + half * C::W + c, f, acc + c / 2);
           }
           __syncwarp();
           arrive_lane0(smem_u32(&sempty[slot]), lane);
           if (++slot == C::SLOTS) slot = 0;
-          if (++ab == C::NACC) ab = 0;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1;
+          if constexpr (!C::CV) {
+            if (++ab == C::NACC) ab = 0;
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
         }
       } else {
@@ -749,15 +821,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         constexpr int CHUNKS = C::W / C::CH;
         static_assert(CHUNKS >= 2 && CHUNKS % 2 == 0, "chunks");
         uint32_t r[2][C::CH];
-        float f = 0.0f;
         const float *sc = scales;
         // starts on a block whose sums (and so its scales) are there
         auto begin = [&]() {
           tc_fence_after();
           tmem_ld<C::CH>(t_lane + ab * C::NT, r[0]);
           sc = scales + slot * (C::SC_BYTES / 4);
-          f = C::PV ? sc[quad * 32 + lane] : sc[0];
-          if constexpr (!C::CV) f *= sc[C::SC_P + half * C::W / 128];
         };
         // the whole warp goes on or gives up
         auto wait_done = [&](bool ready) {
@@ -768,8 +837,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           if (ok) begin();
         }
         for (int kb = k0; kb < k1 && ok; ++kb) {
-          const uint64_t f2 = pack2(f, f);
           const float *scb = sc;
+          float f, first;
+          if (block_factors<C>(sc, quad, half, lane, f, first)) {
+            tmem_ld_wait();
+            tmem_scale<C::W>(t_lane + ab * C::NT, first);
+            tmem_ld<C::CH>(t_lane + ab * C::NT, r[0]);
+          }
           const int slot_b = slot, ab_b = ab;
           const int next = stage + C::NACC >= C::STAGES ? stage + C::NACC - C::STAGES : stage + C::NACC;  // the buffer's next block's stage
           const bool more = kb + 1 < k1;
@@ -792,20 +866,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               arrive_lane0(smem_u32(&full[next]), lane);
               if (more && ok) begin();
             }
-            uint32_t (&v)[C::CH] = r[i & 1];
-            uint64_t *sum = acc + i * C::CH / 2;
-            if constexpr (C::CV) {
-              const ulonglong2 *cs = reinterpret_cast<const ulonglong2 *>(scb + C::SC_P + half * C::W + i * C::CH);
-#pragma unroll
-              for (int j = 0; j < C::CH; j += 4) {
-                const ulonglong2 s = cs[j / 4];
-                sum[j / 2] = fma2(mul2f(pack2u(v[j], v[j + 1]), s.x), f2, sum[j / 2]);
-                sum[j / 2 + 1] = fma2(mul2f(pack2u(v[j + 2], v[j + 3]), s.y), f2, sum[j / 2 + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < C::CH; j += 2) sum[j / 2] = fma2(pack2u(v[j], v[j + 1]), f2, sum[j / 2]);
-            }
+            add_scaled<C>(r[i & 1], scb + C::SC_P + half * C::W + i * C::CH, f, acc + i * C::CH / 2);
           }
           __syncwarp();
           arrive_lane0(smem_u32(&sempty[slot_b]), lane);
