@@ -505,7 +505,7 @@ nvfp4_status_t sample_tokens(const void *logits, int logits_type, int64_t ld, co
  *               every row starts on 16 bytes
  *   src_rows    int32 [rows] or NULL: row r of the result is row src_rows[r] of x (without it rows ==
  *               x_rows).  An entry outside [0, x_rows) quantises zeros and makes nvfp4_check_status
- *               report NVFP4_ERR_INVALID_ARG.
+ *               report NVFP4_ERR_INVALID_ARG (x itself must not be NULL where rows > 0).
  *   q, sf       along the rows: e4m3 [rows, k], fp32 [ceil(k/128), rows]: one scale per row and
  *               128 columns (a block of columns' scales lie together), or both NULL
  *   qt, sft     along the columns, transposed: e4m3 [k, P], fp32 [P/128, k] with
@@ -542,7 +542,7 @@ nvfp4_status_t fp8_quantize_weight(const void *w, int w_type, int64_t matrices, 
  *   b, sfb   e4m3 [n, k]; block_b = 128: fp32 [ceil(n/128), ceil(k/128)] (fp8_quantize_weight);
  *            block_b = 1: fp32 [ceil(k/128), n] (fp8_quantize)
  *   d        bf16 or fp32 (d_type) [m, n];  accumulate != 0: D is added to (fp32 only)
- *   a, b and d 16-B aligned, the scales 4-B; k % 16 == 0, any m and n.
+ *   a, b and d 16-B aligned, the scales 4-B; k % 16 == 0, any m (0: nothing is done) and any n >= 1.
  * Gradients with the same call: of the input, fp8_gemm(dY, W^T) with W's qt and sft; of the weight,
  * fp8_gemm(dY^T, X^T) with block_b = 1 and both operands from qt and sft.
  * Every operand is read after the PDL wait.  Results do not depend on timing.  No workspace. */
@@ -568,7 +568,7 @@ nvfp4_status_t fp8_grouped_gemm(const uint8_t *a, const float *sfa, const int64_
  *   padded_rows  P, a multiple of 128 with room for every expert's padded rows (fp8_padded_rows)
  *   d            bf16 or fp32 (d_type) [num_experts, n, k];  accumulate != 0: D is added to (fp32 only).
  *                An expert without rows gets zeros (with accumulate: stays).
- * any n and k; otherwise as fp8_grouped_gemm. */
+ * any n (0: nothing is done) and any k >= 1; otherwise as fp8_grouped_gemm. */
 nvfp4_status_t fp8_grouped_weight_grad(const uint8_t *a, const float *sfa, const uint8_t *b, const float *sfb,
                                        const int64_t *row_offsets, int num_experts, void *d, int d_type, int accumulate,
                                        int64_t padded_rows, int64_t n, int64_t k, uint32_t flags, nvfp4_stream_t stream);

@@ -66,7 +66,8 @@ using Rows = fp8::Cfg<NT, false, true, PER_ROW, fp8::kDense>;
 // Tiles of more than 128 tokens, by what they cost: rounds of tiles over the SMs times the time of a tile's blocks.
 // Measured (ns a block): tokens in the lanes 270, 310 and 460 at 64, 128 and 256 columns with a scale per block of
 // B, 310, 440 and 630 with one per row; the weight in the lanes (whose K a cluster can share) 310 and 440 at 64
-// and 128 columns, 1000 more for a wider tile's ends, and 1400 to join a cluster's parts.
+// and 128 columns, 1000 more for a wider tile's ends, and 1400 to join a cluster's parts (all before the test of the
+// scales' range, which adds 1 to 5 %).
 template <bool PER_ROW>
 nvfp4_status_t run_many(const Call &c) {
   const int64_t rows_ns[3] = {PER_ROW ? 310 : 270, PER_ROW ? 440 : 310, PER_ROW ? 630 : 460}, swap_ns[2] = {310, 440};

@@ -9,11 +9,11 @@
 // What bounds it, measured on 128 x 256 tiles (cycles a block).  The products alone take 512 (8192 multiply-adds a
 // cycle), reading the sums 136 (0.53 a column and quarter of the SM).  Scaling with scalar multiply-adds slows the
 // products to 930; with pairs (fma.rn.f32x2) they take 566 beside it, and the scaling 475, twice that with a factor per
-// column too.  What is left of the 850 that a block takes (4096 x 4864 x 7168 in 103 us, 2.8 PFLOP/s; 1250 with a
-// factor per column, 145 us) is the chain from a block's products through the scaling warps back to the buffer:
-// without the loads of one operand it is 99 us still.  Four warps to a scheduler hide more of it than two with more
-// columns each (123 us), than CTA pairs, which halve the operands' traffic but lengthen the chain (111 us), or than two
-// CTAs an SM with 128 columns each (141 us).
+// column too.  What is left of the 860 that a block takes (4096 x 4864 x 7168 in 106 us, 2.7 PFLOP/s; 1300 with a
+// factor per column, 152 us) is the chain from a block's products through the scaling warps back to the buffer, and the
+// test of the scales' range (see block_factors): without the loads of one operand it was 99 us where it was 103 with
+// them.  Four warps to a scheduler hid more of it than two with more columns each (123 us then), than CTA pairs, which
+// halve the operands' traffic but lengthen the chain (111 us), or than two CTAs an SM with 128 columns each (141 us).
 //
 // The operand whose rows lie in the 128 tensor-memory lanes is P, the other (the columns) is Q.
 // Usually P is A (the tokens); with SWAP it is B (a weight), so that few tokens fill a narrow tile.
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   uint64_t acc[C::W / 2];  // pairs of columns
   if (warp < 4) {
     // (640 threads begin with 96 registers; 4 warps at 40 and 16 at 104 need 91 of them.  56 instead of 40 gives the
-    // scaling warps no less, but the compiler spilled more there: 107 and 156 us instead of 103 and 145.)
+    // scaling warps no less, but the compiler spilled more there: 107 and 156 us where it was 103 and 145.)
     if constexpr (C::SW == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
       // ------------------------------------------------------------ operands

@@ -67,7 +67,7 @@ extern "C" nvfp4_status_t fp8_grouped_gemm(const uint8_t *a, const float *sfa, c
   args.total_rows = t;
   // Few rows to an expert: the weight in the lanes and a narrow tile of tokens, for the weight is read from memory
   // once whatever the tile (128 experts of 1536 x 2048, us: 2 rows to an expert 55, 8 rows 68, 16 rows 71; at 48 rows
-  // 64 columns of tokens took 87, the rows in the lanes 76).  Else the rows in the lanes, 256 columns of the weight to
+  // 64 columns of tokens took 87, the rows in the lanes 76, 77 now).  Else the rows in the lanes, 256 columns of the weight to
   // a tile, or 128 where so few tiles would leave SMs idle.
   const int64_t mean = ceil_div(t, num_experts);
   if (mean <= 8)

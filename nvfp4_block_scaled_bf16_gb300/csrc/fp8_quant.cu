@@ -11,7 +11,7 @@
 // (6.2); an fp32 weight of 4096 x 7168 and its transpose 29 us (6.0).  Both ways from one read is half bound by
 // instructions (two products, two conversions and the exchange of the columns' magnitudes a value): 4096 x 7168 bf16
 // 22 us (5.3 TB/s), and 32,768 rows of 2048 gathered from 4096, whose reads stay in L2, 47 us where the writes alone
-// need 23.
+// need 23.  Along the columns alone: 4096 x 7168 bf16 16 us (5.6 TB/s), fp32 27 (5.6).
 #include "host.h"
 #include "ptx.cuh"
 
@@ -79,10 +79,6 @@ struct Vals {
       w[4 * i + 2] = v.z;
       w[4 * i + 3] = v.w;
     }
-  }
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (F32) return __uint_as_float(w[i]);
-    else return __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
   }
   // the bits of the largest magnitude, as fp32
   __device__ __forceinline__ uint32_t amax() const {
